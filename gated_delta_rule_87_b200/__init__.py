@@ -26,6 +26,8 @@ __all__ = [
     "chunk_workspace_size", "check_device_status", "EXPORTED_SYMBOLS",
     "checked_library_path", "use_library", "bounds_checked", "bounds_violations",
     "kda_chunk_fwd_host",
+    "glr_scan_fwd", "glr_scan_bwd", "glr_step", "gated_norm_fwd", "gated_norm_bwd",
+    "add_norm_fwd", "add_norm_bwd", "GLR_CHUNK",
     "trace_enable", "trace_read", "ERASE_THEN_DECAY", "DECAY_THEN_ERASE",
     "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_UNSUPPORTED", "KDA_ERR_CUDA",
     "KDA_ERR_DEVICE_CHECK", "KDA_ERR_WORKSPACE",
@@ -43,6 +45,10 @@ KDA_F32, KDA_BF16 = 0, 1
 KDA_DEVICE_OK, KDA_DEVICE_BAD_CU_SEQLENS, KDA_DEVICE_TIMEOUT = 0, 1, 2
 # decay order (KDA): the table's literal order, or the decay applied before the erase
 ERASE_THEN_DECAY, DECAY_THEN_ERASE = "erase_then_decay", "decay_then_erase"
+# gated linear recurrence: b_t = x_t, or (1 - a_t) x_t; tokens between two saved states
+_GLR_INPUT = {"given": 0, "complement": 1}
+GLR_CHUNK = 64
+_GATE = {None: 0, "silu": 1, "sigmoid": 2}
 _ORDER = {ERASE_THEN_DECAY: 0, DECAY_THEN_ERASE: 1}
 
 EXPORTED_SYMBOLS = (
@@ -53,13 +59,17 @@ EXPORTED_SYMBOLS = (
     "gdn_chunk_fwd_ex", "kda_recurrent_fwd", "gdn_recurrent_fwd", "kda_state_gather",
     "kda_state_scatter", "kda_selftest_wait_timeout", "kda_bounds_checked",
     "kda_bounds_violations", "kda_chunk_fwd_host", "kda_chunk_fwd_host_buffer_size",
+    "glr_chunk_states_size", "glr_scan_fwd_workspace_size", "glr_scan_fwd",
+    "glr_scan_bwd_workspace_size", "glr_scan_bwd", "glr_step", "kda_gated_norm_fwd",
+    "kda_gated_norm_bwd_workspace_size", "kda_gated_norm_bwd", "kda_add_norm_fwd",
+    "kda_add_norm_bwd_workspace_size", "kda_add_norm_bwd",
 )
 
 _lock = threading.Lock()
 _lib = None
 
 _vp, _fp, _i32, _sz = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
-_i64, _int = ctypes.c_int64, ctypes.c_int
+_i64, _int, _f = ctypes.c_int64, ctypes.c_int, ctypes.c_float
 _SIGS = {
     "kda_chunk_fwd_ex": ([_vp] * 9 + [_i64, _vp] + [_i32] * 6 + [_int, _int, _vp, _sz, _vp], _int),
     "gdn_chunk_fwd_ex": ([_vp] * 9 + [_i64, _vp] + [_i32] * 7 + [_int, _vp, _sz, _vp], _int),
@@ -84,6 +94,22 @@ _SIGS = {
     "kda_bounds_checked": ([], _i32),
     "kda_chunk_fwd_host_buffer_size": ([_i32] * 5 + [ctypes.c_int, _i32], _sz),
     "kda_chunk_fwd_host": ([_vp] * 8 + [_i32] * 5 + [ctypes.c_int, _i32, _vp, _sz, _vp], ctypes.c_int),
+    "glr_chunk_states_size": ([_i32] * 3, _sz),
+    "glr_scan_fwd_workspace_size": ([_i32] * 5, _sz),
+    "glr_scan_bwd_workspace_size": ([_i32] * 5, _sz),
+    "glr_scan_fwd": ([_vp, _i64, _vp, _i64] + [_vp] * 4 + [_i64, _vp, _vp] + [_i32] * 4
+                     + [_int, _int, _vp, _sz, _vp], _int),
+    "glr_scan_bwd": ([_vp, _i64, _vp, _vp, _i64, _vp, _i64] + [_vp] * 6 + [_i32] * 4
+                     + [_int, _int, _vp, _sz, _vp], _int),
+    "glr_step": ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _int, _int, _vp], _int),
+    "kda_gated_norm_fwd": ([_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _f, _int, _int, _vp],
+                           _int),
+    "kda_gated_norm_bwd_workspace_size": ([_i32], _sz),
+    "kda_gated_norm_bwd": ([_vp, _i64] * 3 + [_vp] * 4 + [_i64, _i32, _i32, _f, _int, _int, _vp,
+                                                          _sz, _vp], _int),
+    "kda_add_norm_fwd": ([_vp] * 6 + [_i64, _i32, _f, _int, _int, _vp], _int),
+    "kda_add_norm_bwd_workspace_size": ([_i32], _sz),
+    "kda_add_norm_bwd": ([_vp] * 10 + [_i64, _i32, _f, _int, _int, _vp, _sz, _vp], _int),
     "kda_bounds_violations": ([_vp, ctypes.POINTER(ctypes.c_uint32)], ctypes.c_int),
 }
 
@@ -445,6 +471,364 @@ def gdn_decode_step(q, k, v, g, beta, state, *, o=None, stream=None):
     """One Gated DeltaNet decode step (scalar gate, q/k heads shared by groups of
     v heads); ``state`` is updated in place.  Returns o [N,H_v,d_v]."""
     return _decode("scalar", q, k, v, g, beta, state, o, stream)
+
+
+# --------------------------------------------------------------------------- #
+# gated linear recurrence and the norms around a mixer block
+# --------------------------------------------------------------------------- #
+def _take(dev, **tensors):
+    """Every tensor given lives on ``dev``."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must live on {dev}, got {t.device}")
+
+
+def _dense(t, shape, dtype, name):
+    """Pointer of a contiguous tensor of this shape and type, or None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return _ptr(t)
+
+
+def _rows(t, shape, dtype, name, inner=1):
+    """(pointer, elements from one row to the next) of a tensor whose last
+    ``inner`` axes are contiguous and whose leading axes step evenly."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    width = 1
+    for n in shape[len(shape) - inner:]:
+        width *= n
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    step, strides = 1, t.stride()
+    for i in range(len(shape) - 1, len(shape) - 1 - inner, -1):
+        if shape[i] != 1 and strides[i] != step:
+            raise ValueError(f"{name}: the last {inner} axes must be contiguous")
+        step *= shape[i]
+    ld = None
+    for i in range(len(shape) - 1 - inner, -1, -1):
+        if shape[i] == 1:
+            continue
+        if ld is None:
+            ld = strides[i]
+            step = ld * shape[i]
+        elif strides[i] != step:
+            raise ValueError(f"{name}: the leading axes must step evenly (one row stride)")
+        else:
+            step *= shape[i]
+    ld = width if ld is None else ld
+    if ld < width:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.data_ptr(), ld
+
+
+@contextlib.contextmanager
+def _on(dev):
+    """The device current, where it is not."""
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        yield
+    else:
+        with torch.cuda.device(dev):
+            yield
+
+
+def _glr_input(name) -> int:
+    if name not in _GLR_INPUT:
+        raise ValueError(f"input_gate must be one of {sorted(_GLR_INPUT)}, got {name!r}")
+    return _GLR_INPUT[name]
+
+
+def _glr_common(x, g, cu_seqlens):
+    torch = _torch()
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, D]")
+    io = _dtype_code(x)
+    B, T, D = x.shape
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32:
+            raise TypeError("cu_seqlens must be int32")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [N + 1]")
+        return io, B, T, D, cu_seqlens.numel() - 1
+    return io, B, T, D, B
+
+
+def glr_scan_fwd(x, g, initial_state=None, cu_seqlens=None, *, input_gate: str = "given",
+                 output_final_state: bool = True, output_chunk_states: bool = False, h=None,
+                 final_state=None, chunk_states=None, workspace=None, stream=None,
+                 state_pool=None, state_slots=None):
+    """Gated linear recurrence h_t = exp(g_t) h_{t-1} + b_t over sequences.
+    x [B,T,D] (bf16 or fp32); g [B,T,D] fp32 log-decay; ``input_gate`` "given"
+    (b = x) or "complement" (b = (1 - exp(g)) x); initial_state [N,D] fp32 or
+    None; cu_seqlens int32 [N+1] (device) for packed sequences with B = 1.  x and
+    g may be slices of wider rows.  ``state_pool`` [num_slots,D] with
+    ``state_slots`` as in kda_chunk_fwd.  ``output_chunk_states`` (or a
+    ``chunk_states`` tensor [ceil(B T / 64), D] fp32) keeps what glr_scan_bwd
+    reads.  Returns (h, final_state, chunk_states, workspace)."""
+    torch = _torch()
+    io, B, T, D, N = _glr_common(x, g, cu_seqlens)
+    code, dev, f32 = _glr_input(input_gate), x.device, torch.float32
+    _take(dev, g=g, initial_state=initial_state, cu_seqlens=cu_seqlens, h=h,
+          final_state=final_state, chunk_states=chunk_states, workspace=workspace,
+          state_pool=state_pool, state_slots=state_slots)
+    xp, ld_x = _rows(x, (B, T, D), x.dtype, "x")
+    gp, ld_g = _rows(g, (B, T, D), f32, "g")
+    slots, num_slots = _slots(state_slots, state_pool, N)
+    rows = N
+    if slots is not None:
+        if initial_state is not None or final_state is not None:
+            raise ValueError("with state_pool, pass neither initial_state nor final_state")
+        initial_state = final_state = state_pool
+        rows = num_slots
+    with _on(dev):
+        if h is None:
+            h = torch.empty((B, T, D), dtype=x.dtype, device=dev)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N, D), dtype=f32, device=dev)
+        if chunk_states is None and output_chunk_states:
+            chunk_states = torch.empty((-(-B * T // GLR_CHUNK), D), dtype=f32, device=dev)
+        L = lib()
+        need = L.glr_scan_fwd_workspace_size(B, T, D, N, chunk_states is not None)
+        if workspace is None or workspace.numel() < need:
+            workspace = _alloc_workspace(need, dev)
+        _check(L.glr_scan_fwd(
+            xp, ld_x, gp, ld_g, _dense(h, (B, T, D), x.dtype, "h"),
+            _dense(initial_state, (rows, D), f32, "initial_state"),
+            _dense(final_state, (rows, D), f32, "final_state"), _ptr(slots), num_slots,
+            _dense(chunk_states, (-(-B * T // GLR_CHUNK), D), f32, "chunk_states"),
+            _ptr(cu_seqlens), N, B, T, D, code, io, _ptr(workspace), workspace.numel(),
+            _stream_handle(stream, dev)), "glr_scan_fwd")
+    return h, final_state, chunk_states, workspace
+
+
+def glr_scan_bwd(dh, x, g, initial_state=None, cu_seqlens=None, *, input_gate: str = "given",
+                 dfinal_state=None, chunk_states=None, output_dinitial_state: bool = True,
+                 dx=None, dg=None, dinitial_state=None, workspace=None, stream=None):
+    """Gradients of glr_scan_fwd: dh [B,T,D] is the gradient of h, dfinal_state
+    [N,D] that of the final state (None: zeros); x, g, initial_state, cu_seqlens
+    and input_gate as in the forward call, ``chunk_states`` what it returned
+    (None: computed again).  Returns (dx, dg, dinitial_state, workspace)."""
+    torch = _torch()
+    io, B, T, D, N = _glr_common(x, g, cu_seqlens)
+    code, dev, f32 = _glr_input(input_gate), x.device, torch.float32
+    _take(dev, dh=dh, g=g, initial_state=initial_state, cu_seqlens=cu_seqlens, dx=dx, dg=dg,
+          dfinal_state=dfinal_state, chunk_states=chunk_states, workspace=workspace,
+          dinitial_state=dinitial_state)
+    dp, ld_dh = _rows(dh, (B, T, D), x.dtype, "dh")
+    xp, ld_x = _rows(x, (B, T, D), x.dtype, "x")
+    gp, ld_g = _rows(g, (B, T, D), f32, "g")
+    with _on(dev):
+        if dx is None:
+            dx = torch.empty((B, T, D), dtype=x.dtype, device=dev)
+        if dg is None:
+            dg = torch.empty((B, T, D), dtype=f32, device=dev)
+        if dinitial_state is None and output_dinitial_state:
+            dinitial_state = torch.empty((N, D), dtype=f32, device=dev)
+        L = lib()
+        need = L.glr_scan_bwd_workspace_size(B, T, D, N, chunk_states is not None)
+        if workspace is None or workspace.numel() < need:
+            workspace = _alloc_workspace(need, dev)
+        _check(L.glr_scan_bwd(
+            dp, ld_dh, _dense(dfinal_state, (N, D), f32, "dfinal_state"), xp, ld_x, gp, ld_g,
+            _dense(initial_state, (N, D), f32, "initial_state"),
+            _dense(chunk_states, (-(-B * T // GLR_CHUNK), D), f32, "chunk_states"),
+            _dense(dx, (B, T, D), x.dtype, "dx"), _dense(dg, (B, T, D), f32, "dg"),
+            _dense(dinitial_state, (N, D), f32, "dinitial_state"), _ptr(cu_seqlens), N, B, T, D,
+            code, io, _ptr(workspace), workspace.numel(), _stream_handle(stream, dev)),
+            "glr_scan_bwd")
+    return dx, dg, dinitial_state, workspace
+
+
+def glr_step(x, g, state, *, state_slots=None, input_gate: str = "given", h=None, stream=None):
+    """One token of the gated linear recurrence for each of N sequences: x [N,D]
+    (bf16 or fp32), g [N,D] fp32; ``state`` [N,D] fp32, or a pool [num_slots,D]
+    indexed by ``state_slots`` (int32 [N]; a slot outside the pool is a padding
+    entry), is updated in place.  Returns h [N,D]."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [N, D]")
+    N, D = x.shape
+    io, code, dev, f32 = _dtype_code(x), _glr_input(input_gate), x.device, torch.float32
+    _take(dev, g=g, state=state, state_slots=state_slots, h=h)
+    xp, ld_x = _rows(x, (N, D), x.dtype, "x")
+    gp, ld_g = _rows(g, (N, D), f32, "g")
+    slots, num_slots = _slots(state_slots, state if state_slots is not None else None, N)
+    with _on(dev):
+        if h is None:
+            h = torch.empty((N, D), dtype=x.dtype, device=dev)
+        _check(lib().glr_step(
+            xp, ld_x, gp, ld_g, _dense(h, (N, D), x.dtype, "h"),
+            _dense(state, (num_slots if slots is not None else N, D), f32, "state"), _ptr(slots),
+            num_slots, N, D, code, io, _stream_handle(stream, dev)), "glr_step")
+    return h
+
+
+def _gate_code(gate) -> int:
+    if gate not in _GATE:
+        raise ValueError(f"gate must be None, 'silu' or 'sigmoid', got {gate!r}")
+    return _GATE[gate]
+
+
+def _heads(x):
+    """(tokens, H, d) of [..., H, d]."""
+    if x.dim() < 2:
+        raise ValueError("x must be [..., H, d]")
+    tokens = 1
+    for n in x.shape[:-2]:
+        tokens *= n
+    return tokens, x.shape[-2], x.shape[-1]
+
+
+def gated_norm_fwd(x, z=None, weight=None, *, gate: Optional[str] = "silu", eps: float = 1e-6,
+                   y=None, stream=None):
+    """Gated RMS norm over each head's channels: y = x / rms(x) * weight * s(z).
+    x, z [...,H,d] (bf16 or fp32; z may be a slice of wider token rows), weight
+    fp32 [d] or None; ``gate`` "silu", "sigmoid" or None (then no z).  Returns y."""
+    torch = _torch()
+    code, io, dev = _gate_code(gate), _dtype_code(x), x.device
+    tokens, H, d = _heads(x)
+    _take(dev, z=z, weight=weight, y=y)
+    if (z is None) != (code == 0):
+        raise ValueError("z goes with a gate, and a gate with z")
+    xp, ld_x = _rows(x, x.shape, x.dtype, "x", 2)
+    zp, ld_z = (None, 0) if z is None else _rows(z, x.shape, x.dtype, "z", 2)
+    with _on(dev):
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        _check(lib().kda_gated_norm_fwd(
+            xp, ld_x, zp, ld_z, _dense(weight, (d,), torch.float32, "weight"),
+            _dense(y, x.shape, x.dtype, "y"), tokens, H, d, eps, code, io,
+            _stream_handle(stream, dev)), "kda_gated_norm_fwd")
+    return y
+
+
+def gated_norm_bwd(dy, x, z=None, weight=None, *, gate: Optional[str] = "silu",
+                   eps: float = 1e-6, output_dweight: bool = True, dx=None, dz=None,
+                   dweight=None, workspace=None, stream=None):
+    """Gradients of gated_norm_fwd.  Returns (dx, dz, dweight, workspace); dz is
+    None without a gate, dweight None without a weight."""
+    torch = _torch()
+    code, io, dev = _gate_code(gate), _dtype_code(x), x.device
+    tokens, H, d = _heads(x)
+    _take(dev, dy=dy, z=z, weight=weight, dx=dx, dz=dz, dweight=dweight, workspace=workspace)
+    if (z is None) != (code == 0):
+        raise ValueError("z goes with a gate, and a gate with z")
+    dp, ld_dy = _rows(dy, x.shape, x.dtype, "dy", 2)
+    xp, ld_x = _rows(x, x.shape, x.dtype, "x", 2)
+    zp, ld_z = (None, 0) if z is None else _rows(z, x.shape, x.dtype, "z", 2)
+    with _on(dev):
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if dz is None and z is not None:
+            dz = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        if weight is None:
+            dweight = None
+        elif dweight is None and output_dweight:
+            dweight = torch.empty(d, dtype=torch.float32, device=dev)
+        L = lib()
+        if dweight is not None:
+            need = L.kda_gated_norm_bwd_workspace_size(d)
+            if workspace is None or workspace.numel() < need:
+                workspace = _alloc_workspace(need, dev)
+        _check(L.kda_gated_norm_bwd(
+            dp, ld_dy, xp, ld_x, zp, ld_z, _dense(weight, (d,), torch.float32, "weight"),
+            _dense(dx, x.shape, x.dtype, "dx"), _dense(dz, x.shape, x.dtype, "dz"),
+            _dense(dweight, (d,), torch.float32, "dweight"), tokens, H, d, eps, code, io,
+            _ptr(workspace), 0 if workspace is None else workspace.numel(),
+            _stream_handle(stream, dev)), "kda_gated_norm_bwd")
+    return dx, dz, dweight, workspace
+
+
+def _width(t):
+    if t.dim() < 1:
+        raise ValueError("the residual must be [..., D]")
+    D, rows = t.shape[-1], 1
+    for n in t.shape[:-1]:
+        rows *= n
+    return rows, D
+
+
+def add_norm_fwd(residual, y, weight=None, scale=None, *, eps: float = 1e-6, residual_out=None,
+                 n=None, stream=None):
+    """Residual add and RMS norm: residual_out = residual + scale * y, and
+    n = residual_out / rms(residual_out) * weight.  residual [...,D] (bf16, or
+    fp32 with either activation type), y [...,D]; scale, weight fp32 [D] or None.
+    ``residual_out`` may be ``residual`` itself.  Returns (residual_out, n)."""
+    torch = _torch()
+    rows, D = _width(residual)
+    dev, shape = residual.device, residual.shape
+    res, io = _dtype_code(residual), _dtype_code(y)
+    _take(dev, y=y, weight=weight, scale=scale, residual_out=residual_out, n=n)
+    with _on(dev):
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
+        if n is None:
+            n = torch.empty(shape, dtype=y.dtype, device=dev)
+        _check(lib().kda_add_norm_fwd(
+            _ptr(residual), _dense(y, shape, y.dtype, "y"),
+            _dense(scale, (D,), torch.float32, "scale"),
+            _dense(weight, (D,), torch.float32, "weight"),
+            _dense(residual_out, shape, residual.dtype, "residual_out"),
+            _dense(n, shape, y.dtype, "n"), rows, D, eps, res, io, _stream_handle(stream, dev)),
+            "kda_add_norm_fwd")
+    return residual_out, n
+
+
+def add_norm_bwd(dn, dresidual_out, residual_out, y=None, weight=None, scale=None, *,
+                 eps: float = 1e-6, dresidual=None, dy=None, dscale=None, dweight=None,
+                 workspace=None, stream=None):
+    """Gradients of add_norm_fwd from those of both outputs (dresidual_out None:
+    zeros) and the residual_out it wrote; ``y`` is needed with a scale.  Returns
+    (dresidual, dy, dweight, dscale, workspace).  Without a scale and with one
+    type dy IS dresidual, the same tensor; dweight (dscale) is None without a
+    weight (a scale)."""
+    torch = _torch()
+    rows, D = _width(residual_out)
+    dev, shape, f32 = residual_out.device, residual_out.shape, torch.float32
+    res, io = _dtype_code(residual_out), _dtype_code(dn)
+    _take(dev, dn=dn, dresidual_out=dresidual_out, y=y, weight=weight, scale=scale,
+          dresidual=dresidual, dy=dy, dscale=dscale, dweight=dweight, workspace=workspace)
+    if scale is not None and y is None:
+        raise ValueError("the gradient of scale needs y")
+    with _on(dev):
+        if dresidual is None:
+            dresidual = torch.empty(shape, dtype=residual_out.dtype, device=dev)
+        shared = dy is None and scale is None and dn.dtype == residual_out.dtype
+        if dy is None and not shared:
+            dy = torch.empty(shape, dtype=dn.dtype, device=dev)
+        if weight is None:
+            dweight = None
+        elif dweight is None:
+            dweight = torch.empty(D, dtype=f32, device=dev)
+        if scale is None:
+            dscale = None
+        elif dscale is None:
+            dscale = torch.empty(D, dtype=f32, device=dev)
+        L = lib()
+        if dweight is not None or dscale is not None:
+            need = L.kda_add_norm_bwd_workspace_size(D)
+            if workspace is None or workspace.numel() < need:
+                workspace = _alloc_workspace(need, dev)
+        _check(L.kda_add_norm_bwd(
+            _dense(dn, shape, dn.dtype, "dn"),
+            _dense(dresidual_out, shape, residual_out.dtype, "dresidual_out"), _ptr(residual_out),
+            _dense(y, shape, dn.dtype, "y") if scale is not None else None,
+            _dense(scale, (D,), f32, "scale"), _dense(weight, (D,), f32, "weight"),
+            _dense(dresidual, shape, residual_out.dtype, "dresidual"),
+            _dense(dy, shape, dn.dtype, "dy"), _dense(dscale, (D,), f32, "dscale"),
+            _dense(dweight, (D,), f32, "dweight"), rows, D, eps, res, io, _ptr(workspace),
+            0 if workspace is None else workspace.numel(), _stream_handle(stream, dev)),
+            "kda_add_norm_bwd")
+    return dresidual, dresidual if shared else dy, dweight, dscale, workspace
 
 
 def trace_enable(on: bool = True) -> None:

@@ -574,7 +574,8 @@ kda_status_t kda_bounds_violations(void *stream, uint32_t *count) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "synchronising before reading the bounds counters");
   const unsigned int parts[] = {gdr::oob_count_prefill_tc(), gdr::oob_count_prefill_simt(),
-                                gdr::oob_count_decode(), gdr::oob_count_api()};
+                                gdr::oob_count_decode(), gdr::oob_count_api(),
+                                gdr::oob_count_glr(), gdr::oob_count_norms()};
   uint64_t total = 0;
   for (unsigned int p : parts) {
     if (p == ~0u) return fail(KDA_ERR_CUDA, "a bounds counter could not be read");
@@ -582,6 +583,370 @@ kda_status_t kda_bounds_violations(void *stream, uint32_t *count) {
   }
   *count = total > 0xffffffffull ? 0xffffffffu : (uint32_t)total;
   return KDA_OK;
+}
+
+}  // extern "C"
+
+// ---- gated linear recurrence over a vector state ----
+namespace {
+
+bool io_aligned(const void *p, bool bf16) {
+  return (reinterpret_cast<uintptr_t>(p) & (bf16 ? 1u : 3u)) == 0;
+}
+
+// Workspace of a scan: the status word, then what its launches hand over.
+struct GlrLayout {
+  int64_t tiles;
+  size_t closed, map, carry, last, chunks, total;
+};
+GlrLayout glr_layout(int64_t tokens, int64_t num_seqs, int64_t D, bool backward, bool own_chunks) {
+  GlrLayout L{};
+  L.tiles = (tokens + gdr::kGlrChunk - 1) / gdr::kGlrChunk;
+  const size_t per = (size_t)L.tiles * D * sizeof(float);
+  size_t off = kStatusBytes;
+  L.closed = off; off = up256(off + (size_t)L.tiles * sizeof(int32_t));
+  L.map = off; off = up256(off + 2 * per);
+  L.carry = off; off = up256(off + (backward ? per : 0));
+  L.last = off; off = up256(off + (backward ? 0 : (size_t)num_seqs * D * sizeof(float)));
+  L.chunks = off; off = up256(off + (own_chunks ? per : 0));
+  L.total = off;
+  return L;
+}
+
+kda_status_t check_glr(gdr::GlrArgs &a, int32_t B, glr_input_t input, kda_dtype_t io_dtype,
+                       void *workspace, size_t workspace_bytes, bool backward) {
+  if (io_dtype != KDA_F32 && io_dtype != KDA_BF16)
+    return fail(KDA_ERR_INVALID_ARG, "io_dtype must be KDA_F32 or KDA_BF16");
+  if (input != GLR_INPUT_GIVEN && input != GLR_INPUT_COMPLEMENT)
+    return fail(KDA_ERR_INVALID_ARG, "input must be GLR_INPUT_GIVEN or GLR_INPUT_COMPLEMENT");
+  a.bf16 = io_dtype == KDA_BF16;
+  a.complement = input == GLR_INPUT_COMPLEMENT;
+  if (B <= 0 || a.T < 0 || a.D <= 0)
+    return fail(KDA_ERR_INVALID_ARG, "need B > 0, T >= 0, D > 0 (B=%d T=%d D=%d)", B, a.T, a.D);
+  if ((int64_t)B * a.T > INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "B*T must fit in int32");
+  a.tokens = (int64_t)B * a.T;
+  if (a.cu_seqlens) {
+    if (B != 1) return fail(KDA_ERR_INVALID_ARG, "packed sequences (cu_seqlens) need B == 1");
+    if (a.num_seqs < 0) return fail(KDA_ERR_INVALID_ARG, "num_seqs must be >= 0");
+  } else {
+    a.num_seqs = B;
+  }
+  if (a.tokens > 0) {
+    if (!a.x || !a.g) return fail(KDA_ERR_INVALID_ARG, "x and g must be non-NULL");
+    if (a.ld_x < a.D || a.ld_g < a.D || (backward && a.ld_dh < a.D))
+      return fail(KDA_ERR_INVALID_ARG, "rows must be at least D elements apart");
+  }
+  if (!io_aligned(a.x, a.bf16) || !io_aligned(a.h, a.bf16) || !io_aligned(a.dh, a.bf16) ||
+      !io_aligned(a.dx, a.bf16))
+    return fail(KDA_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+  const void *four[] = {a.g, a.initial_state, a.final_state, a.state_slots, a.chunk_states,
+                        a.dfinal, a.dg, a.dinitial, a.cu_seqlens};
+  for (const void *p : four)
+    if (!aligned4(p)) return fail(KDA_ERR_INVALID_ARG, "pointer %p is not 4-byte aligned", p);
+  if (a.state_slots && a.num_slots < 0) return fail(KDA_ERR_INVALID_ARG, "num_slots must be >= 0");
+  if (!a.state_slots) a.num_slots = a.num_seqs;
+  if (!workspace) return fail(KDA_ERR_WORKSPACE, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const GlrLayout L = glr_layout(a.tokens, a.num_seqs, a.D, backward, !a.chunk_states);
+  if (workspace_bytes < L.total)
+    return fail(KDA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, L.total);
+  unsigned char *w = static_cast<unsigned char *>(workspace);
+  a.tiles = L.tiles;
+  a.status = reinterpret_cast<int32_t *>(w);
+  a.tile_closed = reinterpret_cast<int32_t *>(w + L.closed);
+  a.tile_map = reinterpret_cast<float *>(w + L.map);
+  a.tile_carry = reinterpret_cast<float *>(w + L.carry);
+  a.last_state = reinterpret_cast<float *>(w + L.last);
+  return KDA_OK;
+}
+
+float *glr_own_chunks(const gdr::GlrArgs &a, bool backward) {
+  const GlrLayout L = glr_layout(a.tokens, a.num_seqs, a.D, backward, true);
+  return reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(a.status) + L.chunks);
+}
+
+// The status word, and the check of the packed offsets that the kernels go by.
+kda_status_t glr_begin(const gdr::GlrArgs &a, cudaStream_t s) {
+  cudaError_t e = cudaMemsetAsync(a.status, 0, kStatusBytes, s);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(status)");
+  if (a.cu_seqlens) {
+    e = gdr::launch_check_cu_seqlens(a.cu_seqlens, a.num_seqs, a.T, a.status, s);
+    if (e != cudaSuccess) return cuda_fail(e, "cu_seqlens check launch");
+  }
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t glr_chunk_states_size(int32_t B, int32_t T, int32_t D) {
+  if (B <= 0 || T < 0 || D <= 0) return 0;
+  return (size_t)(((int64_t)B * T + gdr::kGlrChunk - 1) / gdr::kGlrChunk) * D * sizeof(float);
+}
+
+size_t glr_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
+                                   int32_t with_chunk_states) {
+  if (B <= 0 || T < 0 || D <= 0) return 0;
+  return glr_layout((int64_t)B * T, num_seqs > 0 ? num_seqs : B, D, false, !with_chunk_states).total;
+}
+
+size_t glr_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
+                                   int32_t with_chunk_states) {
+  if (B <= 0 || T < 0 || D <= 0) return 0;
+  return glr_layout((int64_t)B * T, num_seqs > 0 ? num_seqs : B, D, true, !with_chunk_states).total;
+}
+
+kda_status_t glr_scan_fwd(const void *x, int64_t ld_x, const float *g, int64_t ld_g, void *h,
+                          const float *initial_state, float *final_state,
+                          const int32_t *state_slots, int64_t num_slots, float *chunk_states,
+                          const int32_t *cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
+                          int32_t D, glr_input_t input, kda_dtype_t io_dtype, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+  gdr::GlrArgs a{};
+  a.x = x; a.ld_x = ld_x; a.g = g; a.ld_g = ld_g; a.h = h;
+  a.initial_state = initial_state; a.final_state = final_state;
+  a.state_slots = state_slots; a.num_slots = num_slots; a.chunk_states = chunk_states;
+  a.cu_seqlens = cu_seqlens; a.num_seqs = num_seqs; a.T = T; a.D = D;
+  kda_status_t st = check_glr(a, B, input, io_dtype, workspace, workspace_bytes, false);
+  if (st != KDA_OK) return st;
+  if (a.tokens > 0 && !h) return fail(KDA_ERR_INVALID_ARG, "h must be non-NULL");
+  if (a.tokens > 0 && (h == x || h == (const void *)g))
+    return fail(KDA_ERR_INVALID_ARG, "h must not alias x or g");
+  if (!a.chunk_states) a.chunk_states = glr_own_chunks(a, false);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = glr_begin(a, s);
+  if (st != KDA_OK) return st;
+  cudaError_t e = gdr::launch_glr_fwd(a, s);
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e, "scan launch");
+}
+
+kda_status_t glr_scan_bwd(const void *dh, int64_t ld_dh, const float *dfinal_state, const void *x,
+                          int64_t ld_x, const float *g, int64_t ld_g, const float *initial_state,
+                          const float *chunk_states, void *dx, float *dg, float *dinitial_state,
+                          const int32_t *cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
+                          int32_t D, glr_input_t input, kda_dtype_t io_dtype, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+  gdr::GlrArgs a{};
+  a.dh = dh; a.ld_dh = ld_dh; a.dfinal = dfinal_state;
+  a.x = x; a.ld_x = ld_x; a.g = g; a.ld_g = ld_g;
+  a.initial_state = initial_state; a.chunk_states = const_cast<float *>(chunk_states);
+  a.dx = dx; a.dg = dg; a.dinitial = dinitial_state;
+  a.cu_seqlens = cu_seqlens; a.num_seqs = num_seqs; a.T = T; a.D = D;
+  kda_status_t st = check_glr(a, B, input, io_dtype, workspace, workspace_bytes, true);
+  if (st != KDA_OK) return st;
+  if (a.tokens > 0 && (!dh || !dx || !dg))
+    return fail(KDA_ERR_INVALID_ARG, "dh, dx and dg must be non-NULL");
+  if (a.tokens > 0) {
+    const void *in[] = {dh, x, g};
+    for (const void *p : in)
+      if (dx == p || (const void *)dg == p)
+        return fail(KDA_ERR_INVALID_ARG, "dx and dg must not alias an input");
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = glr_begin(a, s);
+  if (st != KDA_OK) return st;
+  cudaError_t e = cudaSuccess;
+  if (!a.chunk_states) {
+    a.chunk_states = glr_own_chunks(a, true);
+    e = gdr::launch_glr_chunk_states(a, s);
+  }
+  if (e == cudaSuccess) e = gdr::launch_glr_bwd(a, s);
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e, "scan gradient launch");
+}
+
+kda_status_t glr_step(const void *x, int64_t ld_x, const float *g, int64_t ld_g, void *h,
+                      float *state, const int32_t *state_slots, int64_t num_slots, int32_t N,
+                      int32_t D, glr_input_t input, kda_dtype_t io_dtype, void *stream) {
+  if (io_dtype != KDA_F32 && io_dtype != KDA_BF16)
+    return fail(KDA_ERR_INVALID_ARG, "io_dtype must be KDA_F32 or KDA_BF16");
+  if (input != GLR_INPUT_GIVEN && input != GLR_INPUT_COMPLEMENT)
+    return fail(KDA_ERR_INVALID_ARG, "input must be GLR_INPUT_GIVEN or GLR_INPUT_COMPLEMENT");
+  if (N < 0 || D <= 0) return fail(KDA_ERR_INVALID_ARG, "need N >= 0 and D > 0");
+  if (N == 0) return KDA_OK;
+  if (!x || !g || !h || !state)
+    return fail(KDA_ERR_INVALID_ARG, "x, g, h and state must be non-NULL");
+  if (ld_x < D || ld_g < D)
+    return fail(KDA_ERR_INVALID_ARG, "rows must be at least D elements apart");
+  gdr::GlrArgs a{};
+  a.bf16 = io_dtype == KDA_BF16;
+  a.complement = input == GLR_INPUT_COMPLEMENT;
+  if (!io_aligned(x, a.bf16) || !io_aligned(h, a.bf16) || !aligned4(g) || !aligned4(state) ||
+      !aligned4(state_slots))
+    return fail(KDA_ERR_INVALID_ARG, "a pointer is not aligned to its element size");
+  if (h == x || h == (const void *)g || h == (const void *)state)
+    return fail(KDA_ERR_INVALID_ARG, "h must not alias an input or the state");
+  if (state_slots && num_slots < 0) return fail(KDA_ERR_INVALID_ARG, "num_slots must be >= 0");
+  a.x = x; a.ld_x = ld_x; a.g = g; a.ld_g = ld_g; a.h = h; a.final_state = state;
+  a.state_slots = state_slots; a.num_slots = state_slots ? num_slots : N;
+  a.num_seqs = N; a.T = 1; a.D = D; a.tokens = N;
+  cudaError_t e = gdr::launch_glr_step(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e, "step launch");
+}
+
+// ---- norms around a mixer block ----
+static kda_status_t check_row(int64_t rows, int32_t d, float eps) {
+  if (rows < 0 || rows > INT32_MAX || d <= 0)
+    return fail(KDA_ERR_INVALID_ARG, "need 0 <= rows <= 2^31 - 1 and a row length > 0");
+  if (d > gdr::kNormMaxRow)
+    return fail(KDA_ERR_UNSUPPORTED, "rows of up to %d elements (got %d)", gdr::kNormMaxRow, d);
+  if (!(eps > 0.f) || eps > 1e30f) return fail(KDA_ERR_INVALID_ARG, "eps must be positive and finite");
+  return KDA_OK;
+}
+
+static kda_status_t check_norm_workspace(void *workspace, size_t have, size_t need) {
+  if (!workspace) return fail(KDA_ERR_WORKSPACE, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (have < need) return fail(KDA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", have, need);
+  return KDA_OK;
+}
+
+static kda_status_t check_gated(const gdr::GatedNormArgs &a, kda_gate_t gate, kda_dtype_t io_dtype,
+                                bool backward) {
+  if (io_dtype != KDA_F32 && io_dtype != KDA_BF16)
+    return fail(KDA_ERR_INVALID_ARG, "io_dtype must be KDA_F32 or KDA_BF16");
+  if (gate != KDA_GATE_NONE && gate != KDA_GATE_SILU && gate != KDA_GATE_SIGMOID)
+    return fail(KDA_ERR_INVALID_ARG, "gate must be KDA_GATE_NONE, KDA_GATE_SILU or KDA_GATE_SIGMOID");
+  if (a.tokens < 0 || a.H <= 0) return fail(KDA_ERR_INVALID_ARG, "need tokens >= 0 and H > 0");
+  if (a.tokens > INT32_MAX) return fail(KDA_ERR_INVALID_ARG, "tokens must fit in int32");
+  kda_status_t st = check_row(a.tokens * a.H, a.d, a.eps);
+  if (st != KDA_OK) return st;
+  const bool gated = gate != KDA_GATE_NONE;
+  if (a.tokens > 0) {
+    if (!a.x || (gated && !a.z) || (backward ? !a.dy || !a.dx || (gated && !a.dz) : !a.y))
+      return fail(KDA_ERR_INVALID_ARG, "a tensor that the call needs is NULL");
+    const int64_t row = (int64_t)a.H * a.d;
+    if (a.ld_x < row || (gated && a.ld_z < row) || (backward && a.ld_dy < row))
+      return fail(KDA_ERR_INVALID_ARG, "rows must be at least H*d elements apart");
+  }
+  const void *ptrs[] = {a.dy, a.x, a.z, a.y, a.dx, a.dz};
+  for (const void *p : ptrs)
+    if (!io_aligned(p, a.bf16))
+      return fail(KDA_ERR_INVALID_ARG, "pointer %p is not aligned to its element size", p);
+  if (!aligned4(a.weight) || !aligned4(a.dweight))
+    return fail(KDA_ERR_INVALID_ARG, "weight and dweight must be 4-byte aligned");
+  return KDA_OK;
+}
+
+kda_status_t kda_gated_norm_fwd(const void *x, int64_t ld_x, const void *z, int64_t ld_z,
+                                const float *weight, void *y, int64_t tokens, int32_t H, int32_t d,
+                                float eps, kda_gate_t gate, kda_dtype_t io_dtype, void *stream) {
+  gdr::GatedNormArgs a{};
+  const bool gated = gate != KDA_GATE_NONE;
+  a.x = x; a.ld_x = ld_x; a.z = gated ? z : nullptr; a.ld_z = gated ? ld_z : 0; a.weight = weight;
+  a.y = y; a.tokens = tokens; a.H = H; a.d = d; a.eps = eps; a.gate = gate;
+  a.bf16 = io_dtype == KDA_BF16;
+  kda_status_t st = check_gated(a, gate, io_dtype, false);
+  if (st != KDA_OK || tokens == 0) return st;
+  cudaError_t e = gdr::launch_gated_norm_fwd(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e, "gated norm launch");
+}
+
+size_t kda_gated_norm_bwd_workspace_size(int32_t d) {
+  return d > 0 ? up256((size_t)gdr::kNormBlocks * d * sizeof(float)) : 0;
+}
+
+kda_status_t kda_gated_norm_bwd(const void *dy, int64_t ld_dy, const void *x, int64_t ld_x,
+                                const void *z, int64_t ld_z, const float *weight, void *dx,
+                                void *dz, float *dweight, int64_t tokens, int32_t H, int32_t d,
+                                float eps, kda_gate_t gate, kda_dtype_t io_dtype, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+  gdr::GatedNormArgs a{};
+  const bool gated = gate != KDA_GATE_NONE;
+  a.dy = dy; a.ld_dy = ld_dy; a.x = x; a.ld_x = ld_x;
+  a.z = gated ? z : nullptr; a.ld_z = gated ? ld_z : 0; a.dz = gated ? dz : nullptr;
+  a.weight = weight; a.dx = dx; a.dweight = dweight;
+  a.tokens = tokens; a.H = H; a.d = d; a.eps = eps; a.gate = gate;
+  a.bf16 = io_dtype == KDA_BF16;
+  kda_status_t st = check_gated(a, gate, io_dtype, true);
+  if (st == KDA_OK && dweight)
+    st = check_norm_workspace(workspace, workspace_bytes, kda_gated_norm_bwd_workspace_size(d));
+  if (st != KDA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  a.partial = dweight ? static_cast<float *>(workspace) : nullptr;
+  cudaError_t e = cudaSuccess;
+  if (tokens > 0) e = gdr::launch_gated_norm_bwd(a, s);
+  else if (dweight) e = cudaMemsetAsync(dweight, 0, (size_t)d * sizeof(float), s);
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e, "gated norm gradient launch");
+}
+
+static kda_status_t check_add(gdr::AddNormArgs &a, kda_dtype_t res_dtype, kda_dtype_t io_dtype) {
+  if ((io_dtype != KDA_F32 && io_dtype != KDA_BF16) || (res_dtype != KDA_F32 && res_dtype != KDA_BF16))
+    return fail(KDA_ERR_INVALID_ARG, "res_dtype and io_dtype must be KDA_F32 or KDA_BF16");
+  if (res_dtype == KDA_BF16 && io_dtype == KDA_F32)
+    return fail(KDA_ERR_UNSUPPORTED, "a bf16 residual goes with bf16 activations");
+  a.res_bf16 = res_dtype == KDA_BF16;
+  a.bf16 = io_dtype == KDA_BF16;
+  kda_status_t st = check_row(a.rows, a.D, a.eps);
+  if (st != KDA_OK) return st;
+  const void *res[] = {a.residual, a.residual_out, a.dresidual_out, a.dresidual};
+  const void *io[] = {a.y, a.n, a.dn, a.dy};
+  for (const void *p : res)
+    if (!io_aligned(p, a.res_bf16))
+      return fail(KDA_ERR_INVALID_ARG, "pointer %p is not aligned to its element size", p);
+  for (const void *p : io)
+    if (!io_aligned(p, a.bf16))
+      return fail(KDA_ERR_INVALID_ARG, "pointer %p is not aligned to its element size", p);
+  if (!aligned4(a.scale) || !aligned4(a.weight) || !aligned4(a.dscale) || !aligned4(a.dweight))
+    return fail(KDA_ERR_INVALID_ARG, "scale, weight and their gradients must be 4-byte aligned");
+  return KDA_OK;
+}
+
+kda_status_t kda_add_norm_fwd(const void *residual, const void *y, const float *scale,
+                              const float *weight, void *residual_out, void *n, int64_t rows,
+                              int32_t D, float eps, kda_dtype_t res_dtype, kda_dtype_t io_dtype,
+                              void *stream) {
+  gdr::AddNormArgs a{};
+  a.residual = residual; a.y = y; a.scale = scale; a.weight = weight;
+  a.residual_out = residual_out; a.n = n; a.rows = rows; a.D = D; a.eps = eps;
+  kda_status_t st = check_add(a, res_dtype, io_dtype);
+  if (st != KDA_OK || rows == 0) return st;
+  if (!residual || !y || !residual_out || !n)
+    return fail(KDA_ERR_INVALID_ARG, "residual, y, residual_out and n must be non-NULL");
+  if (n == residual || n == residual_out || residual_out == y)
+    return fail(KDA_ERR_INVALID_ARG, "n must not alias the residual, nor residual_out alias y");
+  cudaError_t e = gdr::launch_add_norm_fwd(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e, "add norm launch");
+}
+
+size_t kda_add_norm_bwd_workspace_size(int32_t D) {
+  return D > 0 ? up256(2 * (size_t)gdr::kNormBlocks * D * sizeof(float)) : 0;
+}
+
+kda_status_t kda_add_norm_bwd(const void *dn, const void *dresidual_out, const void *residual_out,
+                              const void *y, const float *scale, const float *weight,
+                              void *dresidual, void *dy, float *dscale, float *dweight,
+                              int64_t rows, int32_t D, float eps, kda_dtype_t res_dtype,
+                              kda_dtype_t io_dtype, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+  gdr::AddNormArgs a{};
+  a.dn = dn; a.dresidual_out = dresidual_out; a.residual_out = const_cast<void *>(residual_out);
+  a.y = y; a.scale = scale; a.weight = weight; a.dresidual = dresidual; a.dy = dy;
+  a.dscale = dscale; a.dweight = dweight; a.rows = rows; a.D = D; a.eps = eps;
+  kda_status_t st = check_add(a, res_dtype, io_dtype);
+  if (st == KDA_OK && (dscale || dweight))
+    st = check_norm_workspace(workspace, workspace_bytes, kda_add_norm_bwd_workspace_size(D));
+  if (st != KDA_OK) return st;
+  if (rows > 0) {
+    if (!dn || !residual_out || !dresidual)
+      return fail(KDA_ERR_INVALID_ARG, "dn, residual_out and dresidual must be non-NULL");
+    if (dscale && (!y || !scale))
+      return fail(KDA_ERR_INVALID_ARG, "dscale needs y and scale");
+    if (dy && dy == dresidual)
+      return fail(KDA_ERR_INVALID_ARG, "dy must not alias dresidual (pass NULL where they are equal)");
+  }
+  a.partial = static_cast<float *>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (rows > 0) {
+    e = gdr::launch_add_norm_bwd(a, s);
+  } else {
+    if (dweight) e = cudaMemsetAsync(dweight, 0, (size_t)D * sizeof(float), s);
+    if (e == cudaSuccess && dscale) e = cudaMemsetAsync(dscale, 0, (size_t)D * sizeof(float), s);
+  }
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e, "add norm gradient launch");
 }
 
 }  // extern "C"

@@ -35,6 +35,8 @@ unsigned int oob_count_prefill_tc();
 unsigned int oob_count_prefill_simt();
 unsigned int oob_count_decode();
 unsigned int oob_count_api();
+unsigned int oob_count_glr();
+unsigned int oob_count_norms();
 
 // Token-by-token form: T tokens for each of N sequences ([N, T, H, d]
 // layout), state updated in place.  T = 1 is one decode step.
@@ -93,6 +95,83 @@ size_t prefill_workspace_bytes(int T, int H_v, int d_k, int d_v, int num_seqs, b
 
 cudaError_t launch_prefill_f32(const PrefillArgs &a, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);
+
+// Gated linear recurrence over a vector state.  Tokens are numbered along one
+// axis (sequence b of a dense batch begins at b T).
+constexpr int kGlrChunk = 64;  // tokens between two saved states
+
+struct GlrArgs {
+  const void *x;
+  const float *g;
+  int64_t ld_x, ld_g;  // elements from one token's row to the next
+  void *h;
+  const float *initial_state;
+  float *final_state;          // glr_step: the states, updated in place
+  const int32_t *state_slots;  // device [num_seqs] pool slots, or nullptr
+  int64_t num_slots;
+  float *chunk_states;  // [tiles, D]: the state that enters each chunk
+  // backward
+  const void *dh;
+  int64_t ld_dh;
+  const float *dfinal;
+  void *dx;
+  float *dg, *dinitial;
+  const int32_t *cu_seqlens;  // device [num_seqs + 1], or nullptr (dense)
+  int num_seqs, T, D;
+  int64_t tokens, tiles;
+  bool complement, bf16;
+  // workspace
+  int32_t *status;
+  float *tile_map, *tile_carry, *last_state;
+  int32_t *tile_closed;
+};
+
+cudaError_t launch_glr_fwd(const GlrArgs &a, cudaStream_t stream);
+// chunk_states alone (reduce and carry, no token states)
+cudaError_t launch_glr_chunk_states(const GlrArgs &a, cudaStream_t stream);
+cudaError_t launch_glr_bwd(const GlrArgs &a, cudaStream_t stream);
+cudaError_t launch_glr_step(const GlrArgs &a, cudaStream_t stream);
+
+// RMS norm of each head's d channels, a weight, and a gate.
+struct GatedNormArgs {
+  const void *dy, *x, *z;
+  int64_t ld_dy, ld_x, ld_z;  // elements from one token's row to the next
+  const float *weight;        // [d] or nullptr
+  void *y, *dx, *dz;
+  float *dweight;
+  float *partial;  // workspace: [norm_blocks(), d] sums of the weight's gradient
+  int64_t tokens;
+  int H, d, gate;
+  float eps;
+  bool bf16;
+};
+cudaError_t launch_gated_norm_fwd(const GatedNormArgs &a, cudaStream_t stream);
+cudaError_t launch_gated_norm_bwd(const GatedNormArgs &a, cudaStream_t stream);
+
+// residual + scale y and the RMS norm of the sum.
+struct AddNormArgs {
+  const void *residual, *y;
+  const float *scale, *weight;  // [D] or nullptr
+  void *residual_out, *n;
+  // backward
+  const void *dn, *dresidual_out;
+  void *dresidual, *dy;
+  float *dscale, *dweight;
+  float *partial;  // workspace: [2][norm_blocks(), D]
+  int64_t rows;
+  int D;
+  float eps;
+  bool res_bf16, bf16;
+};
+cudaError_t launch_add_norm_fwd(const AddNormArgs &a, cudaStream_t stream);
+cudaError_t launch_add_norm_bwd(const AddNormArgs &a, cudaStream_t stream);
+
+// Most blocks that a norm's backward pass launches, i.e. the rows of its
+// partial column sums.  The same on every device, so that a workspace size does
+// not depend on the current one.
+constexpr int kNormBlocks = 1184;
+// Longest row of the norms.
+constexpr int kNormMaxRow = 16384;
 
 // Device-side check of cu_seqlens; writes KDA_DEVICE_BAD_CU_SEQLENS into the
 // status word on failure (kernels then skip all work).

@@ -349,7 +349,160 @@ KDA_API kda_status_t kda_chunk_fwd_host(const void *q, const void *k, const void
                                         void *device_buffer, size_t device_buffer_bytes,
                                         void *stream);
 
-/* Wait for `stream`, then read the device status word of a prefill workspace.
+/* --------------------------------------------------------------------------
+ * Gated linear recurrence over a vector state: the token mixer without a
+ * matrix state that hybrid stacks put beside KDA and Gated DeltaNet layers.
+ *
+ *     h_t = a_t h_{t-1} + b_t      per channel,  a_t = exp(g_t),  g_t <= 0
+ *     b_t = x_t              GLR_INPUT_GIVEN
+ *     b_t = (1 - a_t) x_t    GLR_INPUT_COMPLEMENT  (h stays a mean of the x)
+ *
+ *   x             [B, T, D] io_dtype, rows ld_x elements apart
+ *   g             [B, T, D] fp32 log-decay (<= 0; -inf forgets everything
+ *                 before the token), rows ld_g elements apart
+ *   h             [B, T, D] io_dtype, contiguous, written: every state
+ *   initial_state [N, D] fp32, or NULL for zeros
+ *   final_state   [N, D] fp32, written, or NULL
+ *   state_slots, num_slots
+ *                 as kda_chunk_fwd_ex: the states are pools [num_slots, D],
+ *                 sequence n reads and writes row state_slots[n]; a slot
+ *                 outside the pool starts from zeros and stores nothing
+ *   chunk_states  fp32, glr_chunk_states_size() bytes, written, or NULL: the
+ *                 state that enters each chunk of 64 tokens of the token
+ *                 axis, which glr_scan_bwd takes to read each input once
+ *   cu_seqlens    as kda_chunk_fwd (packed sequences, B = 1); NULL: B dense
+ *                 sequences of T tokens
+ *   workspace     glr_scan_fwd_workspace_size() bytes (with_chunk_states:
+ *                 whether chunk_states is given), 256-byte aligned
+ *
+ * Any D > 0 and T >= 0.  Rows start `ld` elements apart (>= D), the same for
+ * every token of the batch.  Data pointers are aligned to their element size
+ * (even D with rows aligned to two elements runs faster).  States,
+ * products and sums are fp32; only h is rounded to io_dtype.  A non-finite
+ * value of one sequence never reaches another.  final_state may be the
+ * buffer of initial_state.  An invalid cu_seqlens leaves every output
+ * unwritten (kda_check_device_status on the workspace).
+ * ------------------------------------------------------------------------ */
+typedef enum { GLR_INPUT_GIVEN = 0, GLR_INPUT_COMPLEMENT = 1 } glr_input_t;
+
+KDA_API size_t glr_chunk_states_size(int32_t B, int32_t T, int32_t D);
+KDA_API size_t glr_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
+                                           int32_t with_chunk_states);
+KDA_API kda_status_t glr_scan_fwd(const void *x, int64_t ld_x, const float *g, int64_t ld_g,
+                                  void *h, const float *initial_state, float *final_state,
+                                  const int32_t *state_slots, int64_t num_slots,
+                                  float *chunk_states, const int32_t *cu_seqlens,
+                                  int32_t num_seqs, int32_t B, int32_t T, int32_t D,
+                                  glr_input_t input, kda_dtype_t io_dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* Backward pass of glr_scan_fwd (without a state pool).  With d_t the whole
+ * gradient of h_t,
+ *     d_t  = dh_t + a_{t+1} d_{t+1}     (+ dfinal_state at the last token)
+ *     dx_t = d_t  or  (1 - a_t) d_t,    dg_t = a_t d_t (h_{t-1}  or  h_{t-1} - x_t)
+ *     dinitial_state = a_1 d_1
+ *
+ *   dh             [B, T, D] io_dtype, rows ld_dh elements apart
+ *   dfinal_state   [N, D] fp32, or NULL for zeros
+ *   x, g, initial_state, cu_seqlens, input    what the forward call was given
+ *   chunk_states   what the forward call wrote for the same inputs, or NULL:
+ *                  then it is computed again in the workspace, at the price of
+ *                  reading x and g once more
+ *   dx             [B, T, D] io_dtype, written;  dg [B, T, D] fp32, written
+ *   dinitial_state [N, D] fp32, written, or NULL
+ * The states are formed again in fp32 from x and g: the rounding of h plays no
+ * part in the gradients. */
+KDA_API size_t glr_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
+                                           int32_t with_chunk_states);
+KDA_API kda_status_t glr_scan_bwd(const void *dh, int64_t ld_dh, const float *dfinal_state,
+                                  const void *x, int64_t ld_x, const float *g, int64_t ld_g,
+                                  const float *initial_state, const float *chunk_states,
+                                  void *dx, float *dg, float *dinitial_state,
+                                  const int32_t *cu_seqlens, int32_t num_seqs, int32_t B,
+                                  int32_t T, int32_t D, glr_input_t input,
+                                  kda_dtype_t io_dtype, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* One token for each of N sequences, the states updated in place:
+ *   x [N, D] io_dtype (rows ld_x apart), g [N, D] fp32 (rows ld_g apart),
+ *   h [N, D] io_dtype, written;  state [N, D] fp32, or with state_slots a pool
+ *   [num_slots, D] of which sequence n uses row state_slots[n].  A slot outside
+ *   the pool is a padding entry: its row of h is zeros, no state is touched.
+ *   Slots of different sequences must differ.  No workspace.  (A few tokens
+ *   per sequence: glr_scan_fwd with state_slots.) */
+KDA_API kda_status_t glr_step(const void *x, int64_t ld_x, const float *g, int64_t ld_g, void *h,
+                              float *state, const int32_t *state_slots, int64_t num_slots,
+                              int32_t N, int32_t D, glr_input_t input, kda_dtype_t io_dtype,
+                              void *stream);
+
+/* --------------------------------------------------------------------------
+ * Gated RMS norm: the output stage of a mixer.  For each head row x of d
+ * channels, with u = x / sqrt(mean(x^2) + eps):
+ *
+ *     y = u * weight * s(z),   s(z) = z sigmoid(z) | sigmoid(z) | 1 (no gate)
+ *
+ *   x, z    [tokens, H, d] io_dtype, tokens ld_x / ld_z elements apart (>= H d;
+ *           z may be a slice of a wider projection); z unused without a gate
+ *   weight  [d] fp32, shared by the heads, or NULL (ones)
+ *   y       [tokens, H, d] io_dtype, contiguous, written
+ * d up to 16384; eps > 0; tokens * H up to 2^31 - 1.  fp32 throughout, rounded
+ * once at the end.  No workspace.
+ *
+ * Backward: dx, dz [tokens, H, d] io_dtype (contiguous, written; dz unused
+ * without a gate) and dweight [d] fp32 (written, or NULL), summed in a fixed
+ * order.  dweight needs a workspace of kda_gated_norm_bwd_workspace_size()
+ * bytes, 256-byte aligned. */
+typedef enum { KDA_GATE_NONE = 0, KDA_GATE_SILU = 1, KDA_GATE_SIGMOID = 2 } kda_gate_t;
+
+KDA_API kda_status_t kda_gated_norm_fwd(const void *x, int64_t ld_x, const void *z, int64_t ld_z,
+                                        const float *weight, void *y, int64_t tokens, int32_t H,
+                                        int32_t d, float eps, kda_gate_t gate,
+                                        kda_dtype_t io_dtype, void *stream);
+KDA_API size_t kda_gated_norm_bwd_workspace_size(int32_t d);
+KDA_API kda_status_t kda_gated_norm_bwd(const void *dy, int64_t ld_dy, const void *x, int64_t ld_x,
+                                        const void *z, int64_t ld_z, const float *weight,
+                                        void *dx, void *dz, float *dweight, int64_t tokens,
+                                        int32_t H, int32_t d, float eps, kda_gate_t gate,
+                                        kda_dtype_t io_dtype, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/* --------------------------------------------------------------------------
+ * Residual add and RMS norm: the boundary between two blocks.
+ *
+ *     residual_out = residual + scale * y
+ *     n            = residual_out / sqrt(mean(residual_out^2) + eps) * weight
+ *
+ *   residual, residual_out  [rows, D] res_dtype; may be the same buffer
+ *   y, n          [rows, D] io_dtype
+ *   scale, weight [D] fp32, or NULL (ones)
+ * res_dtype is io_dtype, or KDA_F32 with bf16 activations.  The norm is taken
+ * of the fp32 sum, before residual_out is rounded.  D up to 16384; eps > 0.
+ *
+ * Backward, from the gradients of both outputs:
+ *   dn            [rows, D] io_dtype;  dresidual_out [rows, D] res_dtype, or
+ *                 NULL for zeros;  residual_out as the forward call wrote it
+ *   y, scale      as in the forward call (y is read only for dscale)
+ *   dresidual     [rows, D] res_dtype, written (may be dresidual_out's buffer)
+ *   dy            [rows, D] io_dtype, written, or NULL (without a scale and
+ *                 with one type it equals dresidual)
+ *   dscale, dweight  [D] fp32, written, or NULL; summed in a fixed order.  They
+ *                 need a workspace of kda_add_norm_bwd_workspace_size() bytes,
+ *                 256-byte aligned. */
+KDA_API kda_status_t kda_add_norm_fwd(const void *residual, const void *y, const float *scale,
+                                      const float *weight, void *residual_out, void *n,
+                                      int64_t rows, int32_t D, float eps, kda_dtype_t res_dtype,
+                                      kda_dtype_t io_dtype, void *stream);
+KDA_API size_t kda_add_norm_bwd_workspace_size(int32_t D);
+KDA_API kda_status_t kda_add_norm_bwd(const void *dn, const void *dresidual_out,
+                                      const void *residual_out, const void *y,
+                                      const float *scale, const float *weight, void *dresidual,
+                                      void *dy, float *dscale, float *dweight, int64_t rows,
+                                      int32_t D, float eps, kda_dtype_t res_dtype,
+                                      kda_dtype_t io_dtype, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* Wait for `stream`, then read the device status word of a prefill or scan
+ * workspace.
  * Returns KDA_OK or KDA_ERR_DEVICE_CHECK (device code in *device_code when
  * non-NULL), or KDA_ERR_CUDA.  Synchronises the stream. */
 KDA_API kda_status_t kda_check_device_status(const void *workspace, void *stream,
