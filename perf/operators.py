@@ -286,6 +286,12 @@ def _own(st, op):
             return [h, final]
         dx, dg, dh0, _ = gdr.glr_scan_bwd(st["dh"], st["x"], st["g"], st["h0"], st["cu"], input_gate=st["input"],
                                           dfinal_state=st["dfinal"], chunk_states=chunks)
+        if st["dh"].dtype == torch.float32:
+            # the plain form adds the final states' gradient into a 32-bit dh itself: so does this program,
+            # or the two would go on from different inputs when a pass is run again
+            cu = st["cu64"]
+            full = (cu[1:] > cu[:-1])[:, None]
+            st["dh"].flatten(0, 1).index_add_(0, (cu[1:] - 1).clamp_(min=0), torch.where(full, st["dfinal"], 0.0))
         return [h, final, dx, dg, dh0]
     if op == "gnorm":
         return [gdr.gated_norm_fwd(st["x"], st["z"], st["w"], gate=st["case"]["gate"], eps=EPS)]
