@@ -95,8 +95,8 @@ _SIGS = {
     "kda_chunk_fwd_host_buffer_size": ([_i32] * 5 + [ctypes.c_int, _i32], _sz),
     "kda_chunk_fwd_host": ([_vp] * 8 + [_i32] * 5 + [ctypes.c_int, _i32, _vp, _sz, _vp], ctypes.c_int),
     "glr_chunk_states_size": ([_i32] * 3, _sz),
-    "glr_scan_fwd_workspace_size": ([_i32] * 5, _sz),
-    "glr_scan_bwd_workspace_size": ([_i32] * 5, _sz),
+    "glr_scan_fwd_workspace_size": ([_i32] * 3, _sz),
+    "glr_scan_bwd_workspace_size": ([_i32] * 4, _sz),
     "glr_scan_fwd": ([_vp, _i64, _vp, _i64] + [_vp] * 4 + [_i64, _vp, _vp] + [_i32] * 4
                      + [_int, _int, _vp, _sz, _vp], _int),
     "glr_scan_bwd": ([_vp, _i64, _vp, _vp, _i64, _vp, _i64] + [_vp] * 6 + [_i32] * 4
@@ -597,7 +597,7 @@ def glr_scan_fwd(x, g, initial_state=None, cu_seqlens=None, *, input_gate: str =
         if chunk_states is None and output_chunk_states:
             chunk_states = torch.empty((-(-B * T // GLR_CHUNK), D), dtype=f32, device=dev)
         L = lib()
-        need = L.glr_scan_fwd_workspace_size(B, T, D, N, chunk_states is not None)
+        need = L.glr_scan_fwd_workspace_size(B, T, D)
         if workspace is None or workspace.numel() < need:
             workspace = _alloc_workspace(need, dev)
         _check(L.glr_scan_fwd(
@@ -634,7 +634,7 @@ def glr_scan_bwd(dh, x, g, initial_state=None, cu_seqlens=None, *, input_gate: s
         if dinitial_state is None and output_dinitial_state:
             dinitial_state = torch.empty((N, D), dtype=f32, device=dev)
         L = lib()
-        need = L.glr_scan_bwd_workspace_size(B, T, D, N, chunk_states is not None)
+        need = L.glr_scan_bwd_workspace_size(B, T, D, chunk_states is not None)
         if workspace is None or workspace.numel() < need:
             workspace = _alloc_workspace(need, dev)
         _check(L.glr_scan_bwd(

@@ -594,20 +594,21 @@ bool io_aligned(const void *p, bool bf16) {
   return (reinterpret_cast<uintptr_t>(p) & (bf16 ? 1u : 3u)) == 0;
 }
 
-// Workspace of a scan: the status word, then what its launches hand over.
+// Workspace of a scan: the status word, then what its tiles hand over.  Stripes
+// are counted at their narrowest (32 channels) and groups at their shortest.
 struct GlrLayout {
   int64_t tiles;
-  size_t closed, map, carry, last, chunks, total;
+  size_t flags, map, carry, chunks, total;
 };
-GlrLayout glr_layout(int64_t tokens, int64_t num_seqs, int64_t D, bool backward, bool own_chunks) {
+GlrLayout glr_layout(int64_t tokens, int64_t D, bool own_chunks) {
   GlrLayout L{};
   L.tiles = (tokens + gdr::kGlrChunk - 1) / gdr::kGlrChunk;
-  const size_t per = (size_t)L.tiles * D * sizeof(float);
+  const size_t per = (size_t)L.tiles * D * sizeof(float), stripes = (size_t)(D + 31) / 32;
+  const size_t groups = (size_t)L.tiles / gdr::kGlrShortestGroup + 1;
   size_t off = kStatusBytes;
-  L.closed = off; off = up256(off + (size_t)L.tiles * sizeof(int32_t));
+  L.flags = off; off = up256(off + (1 + (L.tiles + groups) * stripes) * sizeof(int32_t));
   L.map = off; off = up256(off + 2 * per);
-  L.carry = off; off = up256(off + (backward ? per : 0));
-  L.last = off; off = up256(off + (backward ? 0 : (size_t)num_seqs * D * sizeof(float)));
+  L.carry = off; off = up256(off + groups * D * sizeof(float));
   L.chunks = off; off = up256(off + (own_chunks ? per : 0));
   L.total = off;
   return L;
@@ -648,32 +649,20 @@ kda_status_t check_glr(gdr::GlrArgs &a, int32_t B, glr_input_t input, kda_dtype_
   if (!workspace) return fail(KDA_ERR_WORKSPACE, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(workspace) & 255u)
     return fail(KDA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  const GlrLayout L = glr_layout(a.tokens, a.num_seqs, a.D, backward, !a.chunk_states);
+  a.own_chunks = backward && !a.chunk_states;
+  const GlrLayout L = glr_layout(a.tokens, a.D, a.own_chunks);
   if (workspace_bytes < L.total)
     return fail(KDA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, L.total);
   unsigned char *w = static_cast<unsigned char *>(workspace);
   a.tiles = L.tiles;
   a.status = reinterpret_cast<int32_t *>(w);
-  a.tile_closed = reinterpret_cast<int32_t *>(w + L.closed);
+  a.ticket = reinterpret_cast<int32_t *>(w + L.flags);
   a.tile_map = reinterpret_cast<float *>(w + L.map);
-  a.tile_carry = reinterpret_cast<float *>(w + L.carry);
-  a.last_state = reinterpret_cast<float *>(w + L.last);
-  return KDA_OK;
-}
-
-float *glr_own_chunks(const gdr::GlrArgs &a, bool backward) {
-  const GlrLayout L = glr_layout(a.tokens, a.num_seqs, a.D, backward, true);
-  return reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(a.status) + L.chunks);
-}
-
-// The status word, and the check of the packed offsets that the kernels go by.
-kda_status_t glr_begin(const gdr::GlrArgs &a, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(a.status, 0, kStatusBytes, s);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(status)");
-  if (a.cu_seqlens) {
-    e = gdr::launch_check_cu_seqlens(a.cu_seqlens, a.num_seqs, a.T, a.status, s);
-    if (e != cudaSuccess) return cuda_fail(e, "cu_seqlens check launch");
-  }
+  a.carry = reinterpret_cast<float *>(w + L.carry);
+  if (a.own_chunks) a.chunk_states = reinterpret_cast<float *>(w + L.chunks);
+  // a block a tile of 64 tokens x 32 channels at least
+  if (a.tiles * ((a.D + 31) / 32) > INT32_MAX)
+    return fail(KDA_ERR_UNSUPPORTED, "too many tokens times channels for one call");
   return KDA_OK;
 }
 
@@ -686,16 +675,14 @@ size_t glr_chunk_states_size(int32_t B, int32_t T, int32_t D) {
   return (size_t)(((int64_t)B * T + gdr::kGlrChunk - 1) / gdr::kGlrChunk) * D * sizeof(float);
 }
 
-size_t glr_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
-                                   int32_t with_chunk_states) {
+size_t glr_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t D) {
   if (B <= 0 || T < 0 || D <= 0) return 0;
-  return glr_layout((int64_t)B * T, num_seqs > 0 ? num_seqs : B, D, false, !with_chunk_states).total;
+  return glr_layout((int64_t)B * T, D, false).total;
 }
 
-size_t glr_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
-                                   int32_t with_chunk_states) {
+size_t glr_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t with_chunk_states) {
   if (B <= 0 || T < 0 || D <= 0) return 0;
-  return glr_layout((int64_t)B * T, num_seqs > 0 ? num_seqs : B, D, true, !with_chunk_states).total;
+  return glr_layout((int64_t)B * T, D, !with_chunk_states).total;
 }
 
 kda_status_t glr_scan_fwd(const void *x, int64_t ld_x, const float *g, int64_t ld_g, void *h,
@@ -714,11 +701,7 @@ kda_status_t glr_scan_fwd(const void *x, int64_t ld_x, const float *g, int64_t l
   if (a.tokens > 0 && !h) return fail(KDA_ERR_INVALID_ARG, "h must be non-NULL");
   if (a.tokens > 0 && (h == x || h == (const void *)g))
     return fail(KDA_ERR_INVALID_ARG, "h must not alias x or g");
-  if (!a.chunk_states) a.chunk_states = glr_own_chunks(a, false);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = glr_begin(a, s);
-  if (st != KDA_OK) return st;
-  cudaError_t e = gdr::launch_glr_fwd(a, s);
+  cudaError_t e = gdr::launch_glr_fwd(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : cuda_fail(e, "scan launch");
 }
 
@@ -744,15 +727,7 @@ kda_status_t glr_scan_bwd(const void *dh, int64_t ld_dh, const float *dfinal_sta
       if (dx == p || (const void *)dg == p)
         return fail(KDA_ERR_INVALID_ARG, "dx and dg must not alias an input");
   }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = glr_begin(a, s);
-  if (st != KDA_OK) return st;
-  cudaError_t e = cudaSuccess;
-  if (!a.chunk_states) {
-    a.chunk_states = glr_own_chunks(a, true);
-    e = gdr::launch_glr_chunk_states(a, s);
-  }
-  if (e == cudaSuccess) e = gdr::launch_glr_bwd(a, s);
+  cudaError_t e = gdr::launch_glr_bwd(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : cuda_fail(e, "scan gradient launch");
 }
 

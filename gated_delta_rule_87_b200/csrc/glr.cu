@@ -115,35 +115,241 @@ __device__ __forceinline__ void load_tokens(const GlrArgs &p, int64_t t0, int c,
 #pragma unroll
     for (int v = 0; v < V; ++v) x[i][v] = g[i][v] = 0.f;
     const int64_t t = t0 + i;
-    if (on && t < p.tokens) {
+    if (on && t < p.tokens && GDR_IN_BOUNDS(c + V <= p.D)) {
       row<IO, V>::load(static_cast<const IO *>(p.x) + t * p.ld_x + c, x[i]);
       row<float, V>::load(p.g + t * p.ld_g + c, g[i]);
     }
   }
 }
 
-// The value that enters warp w: what enters the tile, `in`, taken through the
-// maps of the warps before it (after it, for REV).
+// Affine map of a span of tokens, for V channels: out = A in + H, or out = H
+// where the span is closed.
+template <int V> struct Map {
+  float A[V], H[V];
+  bool closed;
+  __device__ __forceinline__ void identity() {
+    closed = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
+  }
+  // this span, then the one of (a, h, c)
+  __device__ __forceinline__ void then(const float (&a)[V], const float (&h)[V], bool c) {
+    closed |= c;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      H[v] = c ? h[v] : fmaf(a[v], H[v], h[v]);
+      A[v] *= a[v];
+    }
+  }
+  __device__ __forceinline__ float of(float in, int v) const { return closed ? H[v] : fmaf(A[v], in, H[v]); }
+};
+
+template <int V> struct TileShared {
+  float G[kScanWarps][32 * V], A[kScanWarps][32 * V], H[kScanWarps][32 * V];  // per warp: sum of g, its exp, H
+  float before_A[kScanWarps][32 * V], before_H[kScanWarps][32 * V];           // earlier tiles, a part a warp
+  bool closed[kScanWarps], before_closed[kScanWarps];
+  int ticket;
+};
+
+// ---- the chain of tiles -------------------------------------------------
+// Tiles are taken in order of a ticket, so every tile that another waits for
+// has been taken by a block that runs or has ended.  Groups of `group` tiles:
+// a tile publishes its map as soon as it has it; what enters a tile is what
+// enters its group, through the maps of the group's tiles before it; the last
+// tile of a group publishes what leaves the group.  Which values are joined,
+// and in which order, depends on the sizes alone, never on timing.
+constexpr int kMapOpen = 1, kMapClosed = 2;
+constexpr uint32_t kMaxChainPolls = 1u << 20;  // about a second
+
+__device__ __forceinline__ int load_acquire(const int32_t *p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_release(int32_t *p, int v) {
+  asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// Waits for a flag; 0 if it gave up (or another block did: the status word says so).
+__device__ __forceinline__ int wait_flag(const GlrArgs &p, const int32_t *flag) {
+  for (uint32_t i = 0; i < kMaxChainPolls; ++i) {
+    const int v = load_acquire(flag);
+    if (v) return v;
+    if ((i & 1023) == 1023 && load_acquire(p.status) != KDA_DEVICE_OK) return 0;
+  }
+  *p.status = KDA_DEVICE_TIMEOUT;
+  return 0;
+}
+
+// The place of a tile in the chain (REV: from the last tile on).
+struct Place {
+  int64_t tile, step;  // its number on the token axis, and in the chain
+  int stripe, in_group;
+  int64_t group;
+};
+template <bool REV> __device__ __forceinline__ Place place_of(const GlrArgs &p, int64_t ticket) {
+  Place q;
+  q.step = ticket / p.stripes;
+  q.stripe = (int)(ticket - q.step * p.stripes);
+  q.tile = REV ? p.tiles - 1 - q.step : q.step;
+  q.group = q.step / p.group;
+  q.in_group = (int)(q.step - q.group * p.group);
+  return q;
+}
+
+// The block's tile: a ticket where tiles wait for one another, else the block's number.
+template <int V> __device__ __forceinline__ int64_t take_tile(const GlrArgs &p, TileShared<V> &sh) {
+  if (!p.chained) return blockIdx.x;
+  if (threadIdx.x == 0) sh.ticket = atomicAdd(p.ticket, 1);
+  __syncthreads();
+  return sh.ticket;
+}
+
+// Publishes a tile's map (one warp, the tile's 32 V channels).
+template <int V>
+__device__ __forceinline__ void publish_map(const GlrArgs &p, const Place &q, const Map<V> &m, int c,
+                                            bool on, int lane) {
+  if (on && GDR_IN_BOUNDS(q.step < p.tiles && c + V <= p.D)) {
+    float2 *to = reinterpret_cast<float2 *>(p.tile_map) + q.step * p.D + c;
+#pragma unroll
+    for (int v = 0; v < V; ++v) __stcg(to + v, make_float2(m.A[v], m.H[v]));
+  }
+  __threadfence();
+  __syncwarp();
+  if (lane == 0) store_release(p.tile_flag + q.step * p.stripes + q.stripe, m.closed ? kMapClosed : kMapOpen);
+}
+template <int V>
+__device__ __forceinline__ void publish_carry(const GlrArgs &p, const Place &q, const float (&h)[V],
+                                              int c, bool on, int lane) {
+  if (on && GDR_IN_BOUNDS(q.group < p.groups && c + V <= p.D)) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) __stcg(p.carry + q.group * p.D + c + v, h[v]);
+  }
+  __threadfence();
+  __syncwarp();
+  if (lane == 0) store_release(p.carry_flag + q.group * p.stripes + q.stripe, kMapOpen);
+}
+
+// What enters the tile.  Each warp joins its part of the group's earlier maps,
+// then all join the parts.  Every thread of the block takes part.  False: a wait gave up.
+template <int V>
+__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared<V> &sh, const Place &q, int c,
+                                           bool on, int w, int lane, float (&h)[V]) {
+  const int per = p.group / kScanWarps;  // maps a warp joins, 1 to 4
+  Map<V> m;
+  m.identity();
+  float carry[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) carry[v] = 0.f;
+  bool ok = true;
+  const int j0 = w * per;
+  const int n = min(per, q.in_group - j0);  // <= 0: none
+  const int64_t first = q.group * p.group + j0;
+  int flag = kMapOpen;
+  if (lane < n) flag = wait_flag(p, p.tile_flag + (first + lane) * p.stripes + q.stripe);
+  // the group's start is needed by whoever joins the parts; warp 0 has the most time for it
+  if (w == 0 && lane == 31 && q.group > 0)
+    flag = wait_flag(p, p.carry_flag + (q.group - 1) * p.stripes + q.stripe);
+  ok = __all_sync(0xffffffffu, flag != 0);
+  const uint32_t closed = __ballot_sync(0xffffffffu, flag == kMapClosed);
+  if (ok && n > 0) {
+    float2 t[4][V];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        t[j][v] = make_float2(1.f, 0.f);
+        if (j < n && on && GDR_IN_BOUNDS(first + j < p.tiles && c + V <= p.D))
+          t[j][v] = __ldcg(reinterpret_cast<const float2 *>(p.tile_map) + (first + j) * p.D + c + v);
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a[V], hh[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) { a[v] = t[j][v].x; hh[v] = t[j][v].y; }
+      if (j < n) m.then(a, hh, closed >> j & 1);
+    }
+  }
+  if (ok && w == 0 && q.group > 0 && on && GDR_IN_BOUNDS(q.group <= p.groups))
+#pragma unroll
+    for (int v = 0; v < V; ++v) carry[v] = __ldcg(p.carry + (q.group - 1) * p.D + c + v);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    // warp 0's part starts from what enters the group
+    if (w == 0) m.H[v] = m.of(carry[v], v);
+    sh.before_A[w][lane * V + v] = m.A[v];
+    sh.before_H[w][lane * V + v] = m.H[v];
+  }
+  if (lane == 0) sh.before_closed[w] = m.closed;
+  if (__syncthreads_or(!ok)) return false;
+  const int parts = min(kScanWarps, (q.in_group + per - 1) / per);
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = sh.before_H[0][lane * V + v];
+  for (int k = 1; k < parts; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      h[v] = sh.before_closed[k] ? sh.before_H[k][lane * V + v]
+                                 : fmaf(sh.before_A[k][lane * V + v], h[v], sh.before_H[k][lane * V + v]);
+  return true;
+}
+
+// A warp's map goes to shared memory ...
+template <int V>
+__device__ __forceinline__ void share_map(float (&G)[32 * V], float (&A)[32 * V], float (&H)[32 * V],
+                                          int lane, const float (&gs)[V], const float (&h)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    G[lane * V + v] = gs[v];
+    A[lane * V + v] = expf(gs[v]);
+    H[lane * V + v] = h[v];
+  }
+}
+// ... and this is the map of the tile's tokens before warp w's (after them, for
+// REV).  Its decay is exp of the whole sum.
 template <int V, bool REV>
-__device__ __forceinline__ void enter_warp(const float (&sA)[kScanWarps][32 * V],
-                                           const float (&sH)[kScanWarps][32 * V],
-                                           const bool (&closed)[kScanWarps], int w, int lane,
-                                           float (&h)[V]) {
+__device__ __forceinline__ Map<V> map_before(const TileShared<V> &sh, int w, int lane) {
+  Map<V> m;
+  m.identity();
+  float gs[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) gs[v] = 0.f;
 #pragma unroll
   for (int k = 0; k < kScanWarps; ++k) {
     const int j = REV ? kScanWarps - 1 - k : k;
     if (REV ? j > w : j < w) {
+      m.closed |= sh.closed[j];
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        h[v] = closed[j] ? sH[j][lane * V + v] : fmaf(sA[j][lane * V + v], h[v], sH[j][lane * V + v]);
+      for (int v = 0; v < V; ++v) {
+        gs[v] += sh.G[j][lane * V + v];
+        m.H[v] = sh.closed[j] ? sh.H[j][lane * V + v]
+                              : fmaf(sh.A[j][lane * V + v], m.H[v], sh.H[j][lane * V + v]);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) m.A[v] = expf(gs[v]);
+  return m;
+}
+
+// Sequences without tokens, by the blocks of the first tile: what leaves them
+// is what enters them.
+__device__ __forceinline__ void pass_empty(const GlrArgs &p, const float *src, float *dst, bool pooled,
+                                           int c0, int width) {
+  if (!dst || !p.cu_seqlens) return;
+  const int lane = threadIdx.x & 31;
+  for (int n0 = (threadIdx.x >> 5) * 32; n0 < p.num_seqs; n0 += kScanWarps * 32) {
+    const int n = n0 + lane;
+    const bool empty = n < p.num_seqs && __ldg(p.cu_seqlens + n) == __ldg(p.cu_seqlens + n + 1);
+    uint32_t todo = __ballot_sync(0xffffffffu, empty);
+    while (todo) {
+      const int k = n0 + __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int64_t r = pooled ? state_row(p, k) : k;
+      if (r < 0) continue;
+      for (int c = c0 + lane; c < c0 + width && c < p.D; c += 32) dst[r * p.D + c] = src ? src[r * p.D + c] : 0.f;
     }
   }
 }
-
-template <int V> struct TileShared {
-  float A[kScanWarps][32 * V], H[kScanWarps][32 * V], C[kScanWarps][32 * V];
-  bool closed[kScanWarps], closed_rev[kScanWarps];
-};
 
 // b_t of a warp's tokens, with the initial state folded in at a sequence's
 // first token: there h = a h0 + b, and nothing before it counts.
@@ -162,8 +368,9 @@ __device__ __forceinline__ void make_inputs(const GlrArgs &p, const Marks &m, in
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       if (m.first >> i & 1) {
-        const int64_t r = state_row(p, __shfl_sync(0xffffffffu, m.seq, i));
-        if (on && r >= 0) {
+        const int n = __shfl_sync(0xffffffffu, m.seq, i);
+        const int64_t r = state_row(p, n);
+        if (on && r >= 0 && GDR_IN_BOUNDS(n < p.num_seqs && r < p.num_slots && c + V <= p.D)) {
           float h0[V];
           state_load<V>(p.initial_state + r * p.D + c, h0);
 #pragma unroll
@@ -174,24 +381,27 @@ __device__ __forceinline__ void make_inputs(const GlrArgs &p, const Marks &m, in
   }
 }
 
-// Phase 1: every tile's maps.  FWD: (A, H) of the states; REV: (A, C) of the gradient.
-template <typename IO, int V, bool COMPLEMENT, bool REV>
-__global__ void __launch_bounds__(kScanWarps * 32) glr_tile_kernel(GlrArgs p) {
+// ---- forward ------------------------------------------------------------
+// Reads x and g once and keeps the tokens' a and b in registers while the tile
+// waits for what enters it.  STATES_ONLY: the saved chunk states alone.
+template <typename IO, int V, bool COMPLEMENT, bool STATES_ONLY>
+__global__ void __launch_bounds__(kScanWarps * 32) glr_scan_kernel(GlrArgs p) {
   __shared__ TileShared<V> sh;
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t tile = blockIdx.x, t0 = tile * kTile + w * kTok;
-  const int c = (blockIdx.y * 32 + lane) * V;
+  const Place q = place_of<false>(p, take_tile(p, sh));
+  const int64_t t0 = q.tile * kTile + w * kTok;
+  const int c = (q.stripe * 32 + lane) * V;
   const bool on = c < p.D;
-  float x[kTok][V], g[kTok][V];
-  load_tokens<IO, V>(p, t0, c, on, x, g);
-  const Marks m = find_marks(p, t0, lane);
-  float gs[V], h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) gs[v] = h[v] = 0.f;
-  if (!REV) {
-    float a[kTok][V], b[kTok][V];
+  float a[kTok][V], b[kTok][V], gs[V], h[V];
+  Marks m;
+  {
+    float x[kTok][V], g[kTok][V];
+    load_tokens<IO, V>(p, t0, c, on, x, g);
+    m = find_marks(p, t0, lane);
     make_inputs<V, COMPLEMENT>(p, m, c, on, x, g, a, b);
+#pragma unroll
+    for (int v = 0; v < V; ++v) gs[v] = h[v] = 0.f;
 #pragma unroll
     for (int i = 0; i < kTok; ++i)
 #pragma unroll
@@ -199,124 +409,63 @@ __global__ void __launch_bounds__(kScanWarps * 32) glr_tile_kernel(GlrArgs p) {
         h[v] = m.first >> i & 1 ? b[i][v] : fmaf(a[i][v], h[v], b[i][v]);
         gs[v] += g[i][v];
       }
-  } else {
-#pragma unroll
-    for (int i = kTok - 1; i >= 0; --i) {
-      const int64_t t = t0 + i;
-      const bool last = m.last >> i & 1;
-      const int n = __shfl_sync(0xffffffffu, m.seq, i);
-      if (on && t < p.tokens) {
-        float d[V];
-        row<IO, V>::load(static_cast<const IO *>(p.dh) + t * p.ld_dh + c, d);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (last) h[v] = p.dfinal ? __ldg(p.dfinal + (int64_t)n * p.D + c + v) : 0.f;
-          h[v] = expf(g[i][v]) * (d[v] + h[v]);
-          gs[v] += g[i][v];
-        }
-      }
-    }
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sh.A[w][lane * V + v] = expf(gs[v]);
-    sh.H[w][lane * V + v] = h[v];
-  }
-  if (lane == 0) sh.closed[w] = (REV ? m.last : m.first) != 0;
-  // the tile's decay: the sums over its warps
-#pragma unroll
-  for (int v = 0; v < V; ++v) sh.C[w][lane * V + v] = gs[v];
-  __syncthreads();
-  if (w != 0) return;
-  bool closed = false;
-  float hh[V], gt[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) hh[v] = gt[v] = 0.f;
-  enter_warp<V, REV>(sh.A, sh.H, sh.closed, REV ? -1 : kScanWarps, lane, hh);
-#pragma unroll
-  for (int k = 0; k < kScanWarps; ++k) {
-    closed |= sh.closed[k];
-#pragma unroll
-    for (int v = 0; v < V; ++v) gt[v] += sh.C[k][lane * V + v];
-  }
-  if (on)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      p.tile_map[(tile * p.D + c + v) * 2] = expf(gt[v]);
-      p.tile_map[(tile * p.D + c + v) * 2 + 1] = hh[v];
-    }
-  if (blockIdx.y == 0 && lane == 0) p.tile_closed[tile] = closed;
-}
-
-// Phase 2: what enters each tile, channel by channel.
-template <bool REV> __global__ void __launch_bounds__(128) glr_carry_kernel(GlrArgs p) {
-  if (bad_offsets(p)) return;
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= p.D) return;
-  float h = 0.f;
-  float *out = REV ? p.tile_carry : p.chunk_states;
-  for (int64_t k = 0; k < p.tiles; ++k) {
-    const int64_t tile = REV ? p.tiles - 1 - k : k;
-    out[tile * p.D + c] = h;
-    const float2 m = *reinterpret_cast<const float2 *>(p.tile_map + (tile * p.D + c) * 2);
-    h = p.tile_closed[tile] ? m.y : fmaf(m.x, h, m.y);
-  }
-}
-
-// Phase 3, forward: the states of every token.
-template <typename IO, int V, bool COMPLEMENT>
-__global__ void __launch_bounds__(kScanWarps * 32) glr_apply_kernel(GlrArgs p) {
-  __shared__ TileShared<V> sh;
-  if (bad_offsets(p)) return;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t tile = blockIdx.x, t0 = tile * kTile + w * kTok;
-  const int c = (blockIdx.y * 32 + lane) * V;
-  const bool on = c < p.D;
-  float x[kTok][V], g[kTok][V], a[kTok][V], b[kTok][V];
-  load_tokens<IO, V>(p, t0, c, on, x, g);
-  const Marks m = find_marks(p, t0, lane);
-  make_inputs<V, COMPLEMENT>(p, m, c, on, x, g, a, b);
-  float gs[V], h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) gs[v] = h[v] = 0.f;
-#pragma unroll
-  for (int i = 0; i < kTok; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = m.first >> i & 1 ? b[i][v] : fmaf(a[i][v], h[v], b[i][v]);
-      gs[v] += g[i][v];
-    }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sh.A[w][lane * V + v] = expf(gs[v]);
-    sh.H[w][lane * V + v] = h[v];
-    h[v] = on ? p.chunk_states[tile * p.D + c + v] : 0.f;
-  }
+  share_map<V>(sh.G[w], sh.A[w], sh.H[w], lane, gs, h);
   if (lane == 0) sh.closed[w] = m.first != 0;
   __syncthreads();
-  enter_warp<V, false>(sh.A, sh.H, sh.closed, w, lane, h);
+  Map<V> before = map_before<V, false>(sh, w, lane);
+  const bool group_end = q.in_group == p.group - 1;
+  if (p.chained && w == kScanWarps - 1 && !group_end) {
+    const Map<V> tile = map_before<V, false>(sh, kScanWarps, lane);
+    publish_map<V>(p, q, tile, c, on, lane);
+  }
+  float in[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) in[v] = 0.f;
+  if (p.chained && !enter_tile<V>(p, sh, q, c, on, w, lane, in)) return;
+  if (w == 0 && on && p.chunk_states && GDR_IN_BOUNDS(q.tile < p.tiles && c + V <= p.D))
+    row<float, V>::store(p.chunk_states + q.tile * p.D + c, in);
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = before.of(in[v], v);
+  if (p.chained && w == kScanWarps - 1 && group_end) {
+    float out[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      out[v] = sh.closed[w] ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], h[v], sh.H[w][lane * V + v]);
+    publish_carry<V>(p, q, out, c, on, lane);
+  }
+  if (STATES_ONLY) return;
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
     const int64_t t = t0 + i;
 #pragma unroll
     for (int v = 0; v < V; ++v)
       h[v] = m.first >> i & 1 ? b[i][v] : fmaf(a[i][v], h[v], b[i][v]);
-    if (on && t < p.tokens && p.h) row<IO, V>::store(static_cast<IO *>(p.h) + t * p.D + c, h);
+    if (on && t < p.tokens && GDR_IN_BOUNDS(c + V <= p.D))
+      row<IO, V>::store(static_cast<IO *>(p.h) + t * p.D + c, h);
     if (p.final_state && (m.last >> i & 1)) {
       const int n = __shfl_sync(0xffffffffu, m.seq, i);
-      if (on) row<float, V>::store(p.last_state + (int64_t)n * p.D + c, h);
+      const int64_t r = state_row(p, n);
+      if (on && r >= 0 && GDR_IN_BOUNDS(n < p.num_seqs && r < p.num_slots && c + V <= p.D))
+        row<float, V>::store(p.final_state + r * p.D + c, h);
     }
   }
+  if (q.tile == 0) pass_empty(p, p.initial_state, p.final_state, true, q.stripe * 32 * V, 32 * V);
 }
 
-// Phase 3, backward: the states again from what enters the tile, then the gradients.
+// ---- backward -----------------------------------------------------------
+// The states again from what enters the tile (saved), the gradients from what
+// enters it from the tokens after it (chained): x, g and dh are read once.
 template <typename IO, int V, bool COMPLEMENT>
 __global__ void __launch_bounds__(kScanWarps * 32) glr_gradient_kernel(GlrArgs p) {
   __shared__ TileShared<V> sh;
+  __shared__ float state_H[kScanWarps][32 * V];
+  __shared__ bool state_closed[kScanWarps];
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t tile = blockIdx.x, t0 = tile * kTile + w * kTok;
-  const int c = (blockIdx.y * 32 + lane) * V;
+  const Place pl = place_of<true>(p, take_tile(p, sh));
+  const int64_t t0 = pl.tile * kTile + w * kTok;
+  const int c = (pl.stripe * 32 + lane) * V;
   const bool on = c < p.D;
   float x[kTok][V], g[kTok][V], a[kTok][V], b[kTok][V], d[kTok][V];
   load_tokens<IO, V>(p, t0, c, on, x, g);
@@ -324,48 +473,76 @@ __global__ void __launch_bounds__(kScanWarps * 32) glr_gradient_kernel(GlrArgs p
   for (int i = 0; i < kTok; ++i) {
 #pragma unroll
     for (int v = 0; v < V; ++v) d[i][v] = 0.f;
-    if (on && t0 + i < p.tokens)
+    if (on && t0 + i < p.tokens && GDR_IN_BOUNDS(c + V <= p.D))
       row<IO, V>::load(static_cast<const IO *>(p.dh) + (t0 + i) * p.ld_dh + c, d[i]);
   }
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = 0.f;
+  if (on && GDR_IN_BOUNDS(pl.tile < p.tiles && c + V <= p.D))
+    row<float, V>::load(p.chunk_states + pl.tile * p.D + c, h);
   const Marks m = find_marks(p, t0, lane);
   make_inputs<V, COMPLEMENT>(p, m, c, on, x, g, a, b);
-  float gs[V], h[V], q[V];
+  float gs[V], s[V], q[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) gs[v] = h[v] = q[v] = 0.f;
+  for (int v = 0; v < V; ++v) gs[v] = s[v] = q[v] = 0.f;
 #pragma unroll
   for (int i = 0; i < kTok; ++i)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      h[v] = m.first >> i & 1 ? b[i][v] : fmaf(a[i][v], h[v], b[i][v]);
+      s[v] = m.first >> i & 1 ? b[i][v] : fmaf(a[i][v], s[v], b[i][v]);
       gs[v] += g[i][v];
     }
 #pragma unroll
   for (int i = kTok - 1; i >= 0; --i) {
     const int n = __shfl_sync(0xffffffffu, m.seq, i);
+    const bool last = m.last >> i & 1;  // the gradient of the sequence's final state enters here
+    float df[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) df[v] = 0.f;
+    if (last && p.dfinal && on && GDR_IN_BOUNDS(n < p.num_seqs))
+      row<float, V>::load(p.dfinal + (int64_t)n * p.D + c, df);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (m.last >> i & 1) {  // the gradient of the sequence's final state enters here
-        d[i][v] += on && p.dfinal ? __ldg(p.dfinal + (int64_t)n * p.D + c + v) : 0.f;
+      if (last) {
+        d[i][v] += df[v];
         q[v] = 0.f;
       }
       q[v] = a[i][v] * (d[i][v] + q[v]);
     }
   }
+  share_map<V>(sh.G[w], sh.A[w], sh.H[w], lane, gs, q);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sh.A[w][lane * V + v] = expf(gs[v]);
-    sh.H[w][lane * V + v] = h[v];
-    sh.C[w][lane * V + v] = q[v];
-    h[v] = on ? p.chunk_states[tile * p.D + c + v] : 0.f;
-    q[v] = on ? p.tile_carry[tile * p.D + c + v] : 0.f;
-  }
+  for (int v = 0; v < V; ++v) state_H[w][lane * V + v] = s[v];
   if (lane == 0) {
-    sh.closed[w] = m.first != 0;
-    sh.closed_rev[w] = m.last != 0;
+    sh.closed[w] = m.last != 0;
+    state_closed[w] = m.first != 0;
   }
   __syncthreads();
-  enter_warp<V, false>(sh.A, sh.H, sh.closed, w, lane, h);
-  enter_warp<V, true>(sh.A, sh.C, sh.closed_rev, w, lane, q);
+  for (int k = 0; k < w; ++k)  // the state that enters the warp
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      h[v] = state_closed[k] ? state_H[k][lane * V + v]
+                             : fmaf(sh.A[k][lane * V + v], h[v], state_H[k][lane * V + v]);
+  Map<V> after = map_before<V, true>(sh, w, lane);
+  const bool group_end = pl.in_group == p.group - 1;
+  if (p.chained && w == 0 && !group_end) {
+    const Map<V> tile = map_before<V, true>(sh, -1, lane);
+    publish_map<V>(p, pl, tile, c, on, lane);
+  }
+  float in[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) in[v] = 0.f;
+  if (p.chained && !enter_tile<V>(p, sh, pl, c, on, w, lane, in)) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v) q[v] = after.of(in[v], v);
+  if (p.chained && w == 0 && group_end) {
+    float out[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      out[v] = sh.closed[w] ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], q[v], sh.H[w][lane * V + v]);
+    publish_carry<V>(p, pl, out, c, on, lane);
+  }
   float before[kTok][V];  // h_{t-1}
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
@@ -376,8 +553,9 @@ __global__ void __launch_bounds__(kScanWarps * 32) glr_gradient_kernel(GlrArgs p
       h[v] = first ? b[i][v] : fmaf(a[i][v], h[v], b[i][v]);
     }
     if (first && p.initial_state) {
-      const int64_t r = state_row(p, __shfl_sync(0xffffffffu, m.seq, i));
-      if (on && r >= 0) state_load<V>(p.initial_state + r * p.D + c, before[i]);
+      const int n = __shfl_sync(0xffffffffu, m.seq, i);
+      if (on && GDR_IN_BOUNDS(n < p.num_seqs))
+        state_load<V>(p.initial_state + (int64_t)n * p.D + c, before[i]);
     }
   }
 #pragma unroll
@@ -392,28 +570,43 @@ __global__ void __launch_bounds__(kScanWarps * 32) glr_gradient_kernel(GlrArgs p
       dx[v] = COMPLEMENT ? -expm1f(g[i][v]) * dt : dt;
       dg[v] = q[v] * (COMPLEMENT ? before[i][v] - x[i][v] : before[i][v]);
     }
-    if (on && t < p.tokens) {
+    if (on && t < p.tokens && GDR_IN_BOUNDS(c + V <= p.D)) {
       row<IO, V>::store(static_cast<IO *>(p.dx) + t * p.D + c, dx);
       row<float, V>::store(p.dg + t * p.D + c, dg);
-      if (p.dinitial && (m.first >> i & 1)) row<float, V>::store(p.dinitial + (int64_t)n * p.D + c, q);
+      if (p.dinitial && (m.first >> i & 1) && GDR_IN_BOUNDS(n < p.num_seqs))
+        row<float, V>::store(p.dinitial + (int64_t)n * p.D + c, q);
     }
   }
+  if (pl.tile == 0) pass_empty(p, p.dfinal, p.dinitial, false, pl.stripe * 32 * V, 32 * V);
 }
 
-// The states that leave the sequences: of those without tokens what enters
-// them.  (Final states wait for this launch in the workspace: they may go to
-// the very slots that the initial states are read from.)
-__global__ void __launch_bounds__(256) glr_finish_kernel(GlrArgs p, bool backward) {
+// Before the chained kernels: zeroes the ticket and the flags, checks the packed
+// offsets and writes the status word.
+__global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words) {
+  if (blockIdx.x == 0) {
+    bool bad = false;
+    if (p.cu_seqlens)
+      for (int i = threadIdx.x; i <= p.num_seqs; i += blockDim.x) {
+        const int32_t x = p.cu_seqlens[i];
+        bad |= (i == 0 && x != 0) || (i == p.num_seqs && x != p.T) ||
+               (i < p.num_seqs && p.cu_seqlens[i + 1] < x);
+      }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *p.status = bad ? KDA_DEVICE_BAD_CU_SEQLENS : KDA_DEVICE_OK;
+  }
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (int64_t)gridDim.x * blockDim.x)
+    p.ticket[i] = 0;
+}
+
+// Without any token: what leaves each sequence is what enters it.
+__global__ void __launch_bounds__(256) glr_no_tokens_kernel(GlrArgs p, bool backward) {
   if (bad_offsets(p)) return;
   const int n = blockIdx.x;
-  const bool empty = p.cu_seqlens ? __ldg(p.cu_seqlens + n) == __ldg(p.cu_seqlens + n + 1) : p.T == 0;
-  if (backward && !empty) return;
   const int64_t r = backward ? n : state_row(p, n);
   if (r < 0) return;
   const float *src = backward ? p.dfinal : p.initial_state;
   float *dst = backward ? p.dinitial : p.final_state;
-  for (int c = threadIdx.x; c < p.D; c += blockDim.x)
-    dst[r * p.D + c] = !empty ? p.last_state[(int64_t)n * p.D + c] : src ? src[r * p.D + c] : 0.f;
+  for (int c = threadIdx.x; c < p.D; c += blockDim.x) dst[r * p.D + c] = src ? src[r * p.D + c] : 0.f;
 }
 
 // One token for each sequence, the state in place.
@@ -426,7 +619,7 @@ __global__ void __launch_bounds__(256) glr_step_kernel(GlrArgs p) {
     float x[V], g[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = 0.f;
-    if (r >= 0) {
+    if (r >= 0 && GDR_IN_BOUNDS(r < p.num_slots && c + V <= p.D)) {
       row<IO, V>::load(static_cast<const IO *>(p.x) + n * p.ld_x + c, x);
       row<float, V>::load(p.g + n * p.ld_g + c, g);
       state_load<V>(p.final_state + r * p.D + c, h);
@@ -451,53 +644,62 @@ bool pairs_ok(const GlrArgs &p) {
          aligned_to(p.dinitial, 8) && aligned_to(p.chunk_states, 8);
 }
 
+cudaError_t launch_begin(const GlrArgs &p, cudaStream_t s) {
+  const int64_t words = p.chained ? 1 + (p.tiles + p.groups) * p.stripes : 0;
+  const int64_t want = (words + 1023) / 1024;
+  TraceScope tr("glr_begin_kernel", s);
+  glr_begin_kernel<<<(unsigned)(want < 1 ? 1 : want > 148 ? 148 : want), 256, 0, s>>>(p, words);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_no_tokens(const GlrArgs &p, bool backward, cudaStream_t s) {
+  if (p.num_seqs == 0 || !(backward ? p.dinitial : p.final_state)) return cudaSuccess;
+  TraceScope tr("glr_no_tokens_kernel", s);
+  glr_no_tokens_kernel<<<p.num_seqs, 256, 0, s>>>(p, backward);
+  return cudaGetLastError();
+}
+
+// The stripes of a call, and whether its tiles wait for one another: not where
+// each begins with a sequence's first token.
+template <int V> GlrArgs with_chain(const GlrArgs &a) {
+  GlrArgs p = a;
+  p.stripes = (p.D + 32 * V - 1) / (32 * V);
+  p.chained = p.tiles > 1 && (p.cu_seqlens || p.T > kTile || kTile % p.T != 0);
+  p.group = 4 * kScanWarps;
+  p.groups = (p.tiles + p.group - 1) / p.group;
+  p.tile_flag = p.ticket + 1;
+  p.carry_flag = p.tile_flag + p.tiles * p.stripes;
+  return p;
+}
+
 template <typename IO, int V, bool COMPLEMENT>
-cudaError_t launch_chunk_states(const GlrArgs &p, cudaStream_t s) {
-  const dim3 grid((unsigned)p.tiles, (unsigned)((p.D + 32 * V - 1) / (32 * V)));
-  if (p.tiles == 0) return cudaSuccess;
-  {
-    TraceScope tr("glr_tile_kernel", s);
-    glr_tile_kernel<IO, V, COMPLEMENT, false><<<grid, kScanWarps * 32, 0, s>>>(p);
-  }
-  TraceScope tr("glr_carry_kernel", s);
-  glr_carry_kernel<false><<<(p.D + 127) / 128, 128, 0, s>>>(p);
+cudaError_t launch_fwd(const GlrArgs &a, cudaStream_t s) {
+  const GlrArgs p = with_chain<V>(a);
+  cudaError_t e = launch_begin(p, s);
+  if (e != cudaSuccess) return e;
+  if (p.tiles == 0) return launch_no_tokens(p, false, s);
+  TraceScope tr("glr_scan_kernel", s);
+  glr_scan_kernel<IO, V, COMPLEMENT, false><<<(unsigned)(p.tiles * p.stripes), kScanWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename IO, int V, bool COMPLEMENT>
-cudaError_t launch_fwd(const GlrArgs &p, cudaStream_t s) {
-  const dim3 grid((unsigned)p.tiles, (unsigned)((p.D + 32 * V - 1) / (32 * V)));
-  if (p.tiles > 0) {
-    launch_chunk_states<IO, V, COMPLEMENT>(p, s);
-    TraceScope tr("glr_apply_kernel", s);
-    glr_apply_kernel<IO, V, COMPLEMENT><<<grid, kScanWarps * 32, 0, s>>>(p);
-  }
-  if (p.num_seqs > 0 && p.final_state) {
-    TraceScope tr("glr_finish_kernel", s);
-    glr_finish_kernel<<<p.num_seqs, 256, 0, s>>>(p, false);
-  }
-  return cudaGetLastError();
-}
-
-template <typename IO, int V, bool COMPLEMENT>
-cudaError_t launch_bwd(const GlrArgs &p, cudaStream_t s) {
-  const dim3 grid((unsigned)p.tiles, (unsigned)((p.D + 32 * V - 1) / (32 * V)));
-  if (p.tiles > 0) {
+cudaError_t launch_bwd(const GlrArgs &a, cudaStream_t s) {
+  GlrArgs p = with_chain<V>(a);
+  cudaError_t e = launch_begin(p, s);
+  if (e != cudaSuccess) return e;
+  if (p.tiles == 0) return launch_no_tokens(p, true, s);
+  const unsigned grid = (unsigned)(p.tiles * p.stripes);
+  if (p.own_chunks) {
     {
-      TraceScope tr("glr_tile_kernel", s);
-      glr_tile_kernel<IO, V, COMPLEMENT, true><<<grid, kScanWarps * 32, 0, s>>>(p);
+      TraceScope tr("glr_scan_kernel", s);
+      glr_scan_kernel<IO, V, COMPLEMENT, true><<<grid, kScanWarps * 32, 0, s>>>(p);
     }
-    {
-      TraceScope tr("glr_carry_kernel", s);
-      glr_carry_kernel<true><<<(p.D + 127) / 128, 128, 0, s>>>(p);
-    }
-    TraceScope tr("glr_gradient_kernel", s);
-    glr_gradient_kernel<IO, V, COMPLEMENT><<<grid, kScanWarps * 32, 0, s>>>(p);
+    e = launch_begin(p, s);
+    if (e != cudaSuccess) return e;
   }
-  if ((p.cu_seqlens || p.T == 0) && p.num_seqs > 0 && p.dinitial) {
-    TraceScope tr("glr_finish_kernel", s);
-    glr_finish_kernel<<<p.num_seqs, 256, 0, s>>>(p, true);
-  }
+  TraceScope tr("glr_gradient_kernel", s);
+  glr_gradient_kernel<IO, V, COMPLEMENT><<<grid, kScanWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -525,9 +727,6 @@ cudaError_t launch_step(const GlrArgs &p, cudaStream_t s) {
 GDR_DEFINE_OOB_COUNTER(oob_count_glr)
 
 cudaError_t launch_glr_fwd(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_fwd); }
-cudaError_t launch_glr_chunk_states(const GlrArgs &p, cudaStream_t s) {
-  GDR_GLR_DISPATCH(launch_chunk_states);
-}
 cudaError_t launch_glr_bwd(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_bwd); }
 cudaError_t launch_glr_step(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_step); }
 

@@ -98,7 +98,8 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);
 
 // Gated linear recurrence over a vector state.  Tokens are numbered along one
 // axis (sequence b of a dense batch begins at b T).
-constexpr int kGlrChunk = 64;  // tokens between two saved states
+constexpr int kGlrChunk = 64;         // tokens between two saved states
+constexpr int kGlrShortestGroup = 8;  // tiles of a group of the chain, at least
 
 struct GlrArgs {
   const void *x;
@@ -122,13 +123,17 @@ struct GlrArgs {
   bool complement, bf16;
   // workspace
   int32_t *status;
-  float *tile_map, *tile_carry, *last_state;
-  int32_t *tile_closed;
+  int32_t *ticket;  // followed by the flags of the tiles, then of the groups
+  float *tile_map, *carry;
+  bool own_chunks;  // backward: chunk_states is workspace, to be filled first
+  // set at the launch
+  int32_t *tile_flag, *carry_flag;
+  int stripes, group;
+  int64_t groups;
+  bool chained;
 };
 
 cudaError_t launch_glr_fwd(const GlrArgs &a, cudaStream_t stream);
-// chunk_states alone (reduce and carry, no token states)
-cudaError_t launch_glr_chunk_states(const GlrArgs &a, cudaStream_t stream);
 cudaError_t launch_glr_bwd(const GlrArgs &a, cudaStream_t stream);
 cudaError_t launch_glr_step(const GlrArgs &a, cudaStream_t stream);
 

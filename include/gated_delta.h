@@ -372,8 +372,7 @@ KDA_API kda_status_t kda_chunk_fwd_host(const void *q, const void *k, const void
  *                 axis, which glr_scan_bwd takes to read each input once
  *   cu_seqlens    as kda_chunk_fwd (packed sequences, B = 1); NULL: B dense
  *                 sequences of T tokens
- *   workspace     glr_scan_fwd_workspace_size() bytes (with_chunk_states:
- *                 whether chunk_states is given), 256-byte aligned
+ *   workspace     glr_scan_fwd_workspace_size() bytes, 256-byte aligned
  *
  * Any D > 0 and T >= 0.  Rows start `ld` elements apart (>= D), the same for
  * every token of the batch.  Data pointers are aligned to their element size
@@ -381,13 +380,13 @@ KDA_API kda_status_t kda_chunk_fwd_host(const void *q, const void *k, const void
  * products and sums are fp32; only h is rounded to io_dtype.  A non-finite
  * value of one sequence never reaches another.  final_state may be the
  * buffer of initial_state.  An invalid cu_seqlens leaves every output
- * unwritten (kda_check_device_status on the workspace).
+ * unwritten (kda_check_device_status on the workspace).  B T D / 2048 must fit
+ * in int32 (else KDA_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 typedef enum { GLR_INPUT_GIVEN = 0, GLR_INPUT_COMPLEMENT = 1 } glr_input_t;
 
 KDA_API size_t glr_chunk_states_size(int32_t B, int32_t T, int32_t D);
-KDA_API size_t glr_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
-                                           int32_t with_chunk_states);
+KDA_API size_t glr_scan_fwd_workspace_size(int32_t B, int32_t T, int32_t D);
 KDA_API kda_status_t glr_scan_fwd(const void *x, int64_t ld_x, const float *g, int64_t ld_g,
                                   void *h, const float *initial_state, float *final_state,
                                   const int32_t *state_slots, int64_t num_slots,
@@ -410,9 +409,11 @@ KDA_API kda_status_t glr_scan_fwd(const void *x, int64_t ld_x, const float *g, i
  *                  reading x and g once more
  *   dx             [B, T, D] io_dtype, written;  dg [B, T, D] fp32, written
  *   dinitial_state [N, D] fp32, written, or NULL
+ *   workspace      glr_scan_bwd_workspace_size() bytes (with_chunk_states:
+ *                  whether chunk_states is given), 256-byte aligned
  * The states are formed again in fp32 from x and g: the rounding of h plays no
  * part in the gradients. */
-KDA_API size_t glr_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t D, int32_t num_seqs,
+KDA_API size_t glr_scan_bwd_workspace_size(int32_t B, int32_t T, int32_t D,
                                            int32_t with_chunk_states);
 KDA_API kda_status_t glr_scan_bwd(const void *dh, int64_t ld_dh, const float *dfinal_state,
                                   const void *x, int64_t ld_x, const float *g, int64_t ld_g,
