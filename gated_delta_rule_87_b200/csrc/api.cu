@@ -598,7 +598,7 @@ bool io_aligned(const void *p, bool bf16) {
 // are counted at their narrowest (32 channels) and groups at their shortest.
 struct GlrLayout {
   int64_t tiles;
-  size_t flags, map, carry, chunks, total;
+  size_t flags, marks, map, carry, chunks, total;
 };
 GlrLayout glr_layout(int64_t tokens, int64_t D, bool own_chunks) {
   GlrLayout L{};
@@ -607,6 +607,7 @@ GlrLayout glr_layout(int64_t tokens, int64_t D, bool own_chunks) {
   const size_t groups = (size_t)L.tiles / gdr::kGlrShortestGroup + 1;
   size_t off = kStatusBytes;
   L.flags = off; off = up256(off + (1 + (L.tiles + groups) * stripes) * sizeof(int32_t));
+  L.marks = off; off = up256(off + (size_t)L.tiles * sizeof(int32_t));
   L.map = off; off = up256(off + 2 * per);
   L.carry = off; off = up256(off + groups * D * sizeof(float));
   L.chunks = off; off = up256(off + (own_chunks ? per : 0));
@@ -657,6 +658,7 @@ kda_status_t check_glr(gdr::GlrArgs &a, int32_t B, glr_input_t input, kda_dtype_
   a.tiles = L.tiles;
   a.status = reinterpret_cast<int32_t *>(w);
   a.ticket = reinterpret_cast<int32_t *>(w + L.flags);
+  a.tile_marks = reinterpret_cast<int32_t *>(w + L.marks);
   a.tile_map = reinterpret_cast<float *>(w + L.map);
   a.carry = reinterpret_cast<float *>(w + L.carry);
   if (a.own_chunks) a.chunk_states = reinterpret_cast<float *>(w + L.chunks);
@@ -727,6 +729,8 @@ kda_status_t glr_scan_bwd(const void *dh, int64_t ld_dh, const float *dfinal_sta
       if (dx == p || (const void *)dg == p)
         return fail(KDA_ERR_INVALID_ARG, "dx and dg must not alias an input");
   }
+  if (dinitial_state && (dinitial_state == initial_state || dinitial_state == dfinal_state))
+    return fail(KDA_ERR_INVALID_ARG, "dinitial_state must not alias initial_state or dfinal_state");
   cudaError_t e = gdr::launch_glr_bwd(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : cuda_fail(e, "scan gradient launch");
 }

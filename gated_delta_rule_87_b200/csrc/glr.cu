@@ -21,73 +21,89 @@
 namespace gdr {
 namespace {
 
-constexpr int kTok = 8;                    // tokens of a warp
-constexpr int kScanWarps = 8;              // warps of a block
-constexpr int kTile = kTok * kScanWarps;   // tokens of a tile
-static_assert(kTile == kGlrChunk, "a tile is a chunk");
+constexpr int kTile = kGlrChunk;  // tokens of a tile; a block's warps share them evenly
 
-// V adjacent channels of one row.
-template <typename IO, int V> struct row;
-template <typename IO> struct row<IO, 1> {
-  static __device__ __forceinline__ void load(const IO *p, float *x) { x[0] = io<IO>::load(p); }
-  static __device__ __forceinline__ void store(IO *p, const float *x) { io<IO>::store(p, x[0]); }
+// V adjacent channels of one token, as they are read.
+template <typename IO, int V> struct Raw;
+template <> struct Raw<float, 1> {
+  float r;
+  __device__ __forceinline__ void zero() { r = 0.f; }
+  __device__ __forceinline__ void load(const float *p) { r = __ldg(p); }
+  __device__ __forceinline__ float at(int) const { return r; }
 };
-template <> struct row<float, 2> {
-  static __device__ __forceinline__ void load(const float *p, float *x) {
-    const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
-    x[0] = v.x; x[1] = v.y;
-  }
-  static __device__ __forceinline__ void store(float *p, const float *x) {
-    *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
-  }
+template <> struct Raw<float, 2> {
+  float2 r;
+  __device__ __forceinline__ void zero() { r = make_float2(0.f, 0.f); }
+  __device__ __forceinline__ void load(const float *p) { r = __ldg(reinterpret_cast<const float2 *>(p)); }
+  __device__ __forceinline__ float at(int v) const { return v ? r.y : r.x; }
 };
-template <> struct row<__nv_bfloat16, 2> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *x) {
-    const uint32_t u = __ldg(reinterpret_cast<const unsigned int *>(p));
-    x[0] = bf16_lo(u); x[1] = bf16_hi(u);
+template <> struct Raw<__nv_bfloat16, 1> {
+  uint32_t r;
+  __device__ __forceinline__ void zero() { r = 0; }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    r = __ldg(reinterpret_cast<const unsigned short *>(p));
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x) {
-    *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(x[0], x[1]);
+  __device__ __forceinline__ float at(int) const { return bf16_lo(r); }
+};
+template <> struct Raw<__nv_bfloat16, 2> {
+  uint32_t r;
+  __device__ __forceinline__ void zero() { r = 0; }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    r = __ldg(reinterpret_cast<const unsigned int *>(p));
   }
+  __device__ __forceinline__ float at(int v) const { return v ? bf16_hi(r) : bf16_lo(r); }
 };
 
+template <typename IO, int V> __device__ __forceinline__ void store_row(IO *p, const float *x) {
+  if constexpr (V == 1) io<IO>::store(p, x[0]);
+  else if constexpr (sizeof(IO) == 4) *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+  else *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(x[0], x[1]);
+}
 // States are read and written in place by some calls: plain (coherent) accesses.
-template <int V> __device__ __forceinline__ void state_load(const float *p, float *x) {
-  if constexpr (V == 2) {
+template <int V> __device__ __forceinline__ void load_state(const float *p, float *x) {
+  if constexpr (V == 1) {
+    x[0] = *p;
+  } else {
     const float2 v = *reinterpret_cast<const float2 *>(p);
     x[0] = v.x; x[1] = v.y;
-  } else {
-    x[0] = *p;
   }
 }
 
-// Which of a warp's tokens begin or end a sequence (bit i: token t0 + i), and,
+// The decay of one token.  With bf16 activations the fast exponential: its error
+// (2^-22 of the value) enters the state of a span of at most 16 tokens only,
+// the decay of longer spans comes from the sum of their g.
+template <typename IO> __device__ __forceinline__ float decay(float g) {
+  if constexpr (sizeof(IO) == 2) return __expf(g);
+  else return expf(g);
+}
+
+// Which of a warp's TOK tokens begin or end a sequence (bit i: token t0 + i), and,
 // in lane i, the sequence of token t0 + i.
 struct Marks {
   uint32_t first, last;
   int seq;
 };
-__device__ __forceinline__ Marks find_marks(const GlrArgs &p, int64_t t0, int lane) {
+template <int TOK> __device__ __forceinline__ Marks find_marks(const GlrArgs &p, uint32_t t0, int lane) {
   Marks m;
   bool f = false, l = false;
   m.seq = 0;
-  const int64_t t = t0 + lane;
-  if (lane < kTok && t < p.tokens) {
+  const uint32_t t = t0 + lane;
+  if (lane < TOK && t < (uint32_t)p.tokens) {
     if (p.cu_seqlens) {  // the last sequence that starts at or before t (empty ones start there too)
       int lo = 0, hi = p.num_seqs;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(p.cu_seqlens + mid) <= t) lo = mid;
+        if ((uint32_t)__ldg(p.cu_seqlens + mid) <= t) lo = mid;
         else hi = mid;
       }
       m.seq = lo;
-      f = __ldg(p.cu_seqlens + lo) == t;
-      l = __ldg(p.cu_seqlens + lo + 1) == t + 1;
+      f = (uint32_t)__ldg(p.cu_seqlens + lo) == t;
+      l = (uint32_t)__ldg(p.cu_seqlens + lo + 1) == t + 1;
     } else {
-      m.seq = (int)(t / p.T);
-      const int64_t r = t - (int64_t)m.seq * p.T;
+      m.seq = (int)(t / (uint32_t)p.T);
+      const uint32_t r = t - (uint32_t)m.seq * (uint32_t)p.T;
       f = r == 0;
-      l = r == p.T - 1;
+      l = r == (uint32_t)p.T - 1;
     }
   }
   m.first = __ballot_sync(0xffffffffu, f);
@@ -102,24 +118,19 @@ __device__ __forceinline__ int64_t state_row(const GlrArgs &p, int n) {
   return s >= 0 && s < p.num_slots ? s : -1;
 }
 
-__device__ __forceinline__ bool bad_offsets(const GlrArgs &p) {
-  return p.cu_seqlens && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK;
+// The initial state of sequence n.
+template <int V>
+__device__ __forceinline__ void initial_of(const GlrArgs &p, int n, int c, bool on, float (&h0)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) h0[v] = 0.f;
+  if (!p.initial_state) return;
+  const int64_t r = state_row(p, n);
+  if (on && r >= 0 && GDR_IN_BOUNDS(n < p.num_seqs && r < p.num_slots && c + V <= p.D))
+    load_state<V>(p.initial_state + r * p.D + c, h0);
 }
 
-// One warp's tokens: per token the decay a, the gate value g and the input x.
-template <typename IO, int V>
-__device__ __forceinline__ void load_tokens(const GlrArgs &p, int64_t t0, int c, bool on,
-                                            float (&x)[kTok][V], float (&g)[kTok][V]) {
-#pragma unroll
-  for (int i = 0; i < kTok; ++i) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) x[i][v] = g[i][v] = 0.f;
-    const int64_t t = t0 + i;
-    if (on && t < p.tokens && GDR_IN_BOUNDS(c + V <= p.D)) {
-      row<IO, V>::load(static_cast<const IO *>(p.x) + t * p.ld_x + c, x[i]);
-      row<float, V>::load(p.g + t * p.ld_g + c, g[i]);
-    }
-  }
+__device__ __forceinline__ bool bad_offsets(const GlrArgs &p) {
+  return p.cu_seqlens && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK;
 }
 
 // Affine map of a span of tokens, for V channels: out = A in + H, or out = H
@@ -132,32 +143,27 @@ template <int V> struct Map {
 #pragma unroll
     for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
   }
-  // this span, then the one of (a, h, c)
-  __device__ __forceinline__ void then(const float (&a)[V], const float (&h)[V], bool c) {
-    closed |= c;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      H[v] = c ? h[v] : fmaf(a[v], H[v], h[v]);
-      A[v] *= a[v];
-    }
-  }
   __device__ __forceinline__ float of(float in, int v) const { return closed ? H[v] : fmaf(A[v], in, H[v]); }
 };
 
-template <int V> struct TileShared {
-  float G[kScanWarps][32 * V], A[kScanWarps][32 * V], H[kScanWarps][32 * V];  // per warp: sum of g, its exp, H
-  float before_A[kScanWarps][32 * V], before_H[kScanWarps][32 * V];           // earlier tiles, a part a warp
-  bool closed[kScanWarps], before_closed[kScanWarps];
-  int ticket;
+template <int V, int WARPS> struct TileShared {
+  float G[WARPS][32 * V], A[WARPS][32 * V], H[WARPS][32 * V];     // per warp: sum of g, its exp, H
+  float before_A[WARPS][32 * V], before_H[WARPS][32 * V];         // earlier tiles, a part a warp
+  bool closed[WARPS], before_closed[WARPS];
+  uint32_t ticket;
 };
 
 // ---- the chain of tiles -------------------------------------------------
-// Tiles are taken in order of a ticket, so every tile that another waits for
-// has been taken by a block that runs or has ended.  Groups of `group` tiles:
-// a tile publishes its map as soon as it has it; what enters a tile is what
-// enters its group, through the maps of the group's tiles before it; the last
-// tile of a group publishes what leaves the group.  Which values are joined,
-// and in which order, depends on the sizes alone, never on timing.
+// Blocks take tiles in order of a ticket, each its own in rising order, so
+// every tile that another waits for is done or in the hands of a block that
+// waits for earlier ones only: the lowest open ticket always proceeds.  In
+// groups of kGroup tiles a tile publishes its map as soon as it has it; what
+// enters a tile is what enters its group, through the maps of the group's tiles
+// before it; the last tile of a group publishes what leaves the group.  Which
+// values are joined, and in which order, depends on the sizes alone, never on
+// timing.
+constexpr int kGroup = 16;
+static_assert(kGroup >= kGlrShortestGroup, "the workspace counts groups of at least this length");
 constexpr int kMapOpen = 1, kMapClosed = 2;
 constexpr uint32_t kMaxChainPolls = 1u << 20;  // about a second
 
@@ -181,28 +187,20 @@ __device__ __forceinline__ int wait_flag(const GlrArgs &p, const int32_t *flag) 
   return 0;
 }
 
-// The place of a tile in the chain (REV: from the last tile on).
+// The place of a ticket's tile in the chain (REV: from the last tile on).
 struct Place {
-  int64_t tile, step;  // its number on the token axis, and in the chain
+  uint32_t tile, step;  // its number on the token axis, and in the chain
   int stripe, in_group;
-  int64_t group;
+  uint32_t group;
 };
-template <bool REV> __device__ __forceinline__ Place place_of(const GlrArgs &p, int64_t ticket) {
+template <bool REV> __device__ __forceinline__ Place place_of(const GlrArgs &p, uint32_t ticket) {
   Place q;
-  q.step = ticket / p.stripes;
-  q.stripe = (int)(ticket - q.step * p.stripes);
-  q.tile = REV ? p.tiles - 1 - q.step : q.step;
-  q.group = q.step / p.group;
-  q.in_group = (int)(q.step - q.group * p.group);
+  q.step = ticket / (uint32_t)p.stripes;
+  q.stripe = (int)(ticket - q.step * (uint32_t)p.stripes);
+  q.tile = REV ? (uint32_t)p.tiles - 1 - q.step : q.step;
+  q.group = q.step / kGroup;
+  q.in_group = (int)(q.step % kGroup);
   return q;
-}
-
-// The block's tile: a ticket where tiles wait for one another, else the block's number.
-template <int V> __device__ __forceinline__ int64_t take_tile(const GlrArgs &p, TileShared<V> &sh) {
-  if (!p.chained) return blockIdx.x;
-  if (threadIdx.x == 0) sh.ticket = atomicAdd(p.ticket, 1);
-  __syncthreads();
-  return sh.ticket;
 }
 
 // Publishes a tile's map (one warp, the tile's 32 V channels).
@@ -210,112 +208,105 @@ template <int V>
 __device__ __forceinline__ void publish_map(const GlrArgs &p, const Place &q, const Map<V> &m, int c,
                                             bool on, int lane) {
   if (on && GDR_IN_BOUNDS(q.step < p.tiles && c + V <= p.D)) {
-    float2 *to = reinterpret_cast<float2 *>(p.tile_map) + q.step * p.D + c;
+    float2 *to = reinterpret_cast<float2 *>(p.tile_map) + (int64_t)q.step * p.D + c;
 #pragma unroll
     for (int v = 0; v < V; ++v) __stcg(to + v, make_float2(m.A[v], m.H[v]));
   }
   __threadfence();
   __syncwarp();
-  if (lane == 0) store_release(p.tile_flag + q.step * p.stripes + q.stripe, m.closed ? kMapClosed : kMapOpen);
+  if (lane == 0)
+    store_release(p.tile_flag + (int64_t)q.step * p.stripes + q.stripe, m.closed ? kMapClosed : kMapOpen);
 }
 template <int V>
 __device__ __forceinline__ void publish_carry(const GlrArgs &p, const Place &q, const float (&h)[V],
                                               int c, bool on, int lane) {
   if (on && GDR_IN_BOUNDS(q.group < p.groups && c + V <= p.D)) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) __stcg(p.carry + q.group * p.D + c + v, h[v]);
+    for (int v = 0; v < V; ++v) __stcg(p.carry + (int64_t)q.group * p.D + c + v, h[v]);
   }
   __threadfence();
   __syncwarp();
-  if (lane == 0) store_release(p.carry_flag + q.group * p.stripes + q.stripe, kMapOpen);
+  if (lane == 0) store_release(p.carry_flag + (int64_t)q.group * p.stripes + q.stripe, kMapOpen);
 }
 
 // What enters the tile.  Each warp joins its part of the group's earlier maps,
 // then all join the parts.  Every thread of the block takes part.  False: a wait gave up.
-template <int V>
-__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared<V> &sh, const Place &q, int c,
-                                           bool on, int w, int lane, float (&h)[V]) {
-  const int per = p.group / kScanWarps;  // maps a warp joins, 1 to 4
+template <int V, int WARPS>
+__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared<V, WARPS> &sh, const Place &q,
+                                           int c, bool on, int w, int lane, float (&h)[V]) {
+  constexpr int PER = kGroup / WARPS;  // maps a warp joins
   Map<V> m;
   m.identity();
-  float carry[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = 0.f;
-  bool ok = true;
-  const int j0 = w * per;
-  const int n = min(per, q.in_group - j0);  // <= 0: none
-  const int64_t first = q.group * p.group + j0;
+  const int j0 = w * PER;
+  const int n = min(PER, q.in_group - j0);  // <= 0: none
+  const uint32_t first = q.group * kGroup + j0;
   int flag = kMapOpen;
-  if (lane < n) flag = wait_flag(p, p.tile_flag + (first + lane) * p.stripes + q.stripe);
-  // the group's start is needed by whoever joins the parts; warp 0 has the most time for it
-  if (w == 0 && lane == 31 && q.group > 0)
-    flag = wait_flag(p, p.carry_flag + (q.group - 1) * p.stripes + q.stripe);
-  ok = __all_sync(0xffffffffu, flag != 0);
+  if (lane < n) flag = wait_flag(p, p.tile_flag + (int64_t)(first + lane) * p.stripes + q.stripe);
+  if (w == 0 && lane == 31 && q.group > 0)  // warp 0's part starts from what enters the group
+    flag = wait_flag(p, p.carry_flag + (int64_t)(q.group - 1) * p.stripes + q.stripe);
+  const bool ok = __all_sync(0xffffffffu, flag != 0);
   const uint32_t closed = __ballot_sync(0xffffffffu, flag == kMapClosed);
-  if (ok && n > 0) {
-    float2 t[4][V];
+  if (ok) {
+    float2 t[PER][V];
+    float carry[V];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int v = 0; v < V; ++v) carry[v] = 0.f;
+    if (w == 0 && q.group > 0 && on && GDR_IN_BOUNDS(q.group <= p.groups && c + V <= p.D))
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = __ldcg(p.carry + (int64_t)(q.group - 1) * p.D + c + v);
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         t[j][v] = make_float2(1.f, 0.f);
         if (j < n && on && GDR_IN_BOUNDS(first + j < p.tiles && c + V <= p.D))
-          t[j][v] = __ldcg(reinterpret_cast<const float2 *>(p.tile_map) + (first + j) * p.D + c + v);
+          t[j][v] = __ldcg(reinterpret_cast<const float2 *>(p.tile_map) + (int64_t)(first + j) * p.D + c + v);
       }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float a[V], hh[V];
+    for (int v = 0; v < V; ++v) m.H[v] = carry[v];
 #pragma unroll
-      for (int v = 0; v < V; ++v) { a[v] = t[j][v].x; hh[v] = t[j][v].y; }
-      if (j < n) m.then(a, hh, closed >> j & 1);
+    for (int j = 0; j < PER; ++j) {
+      const bool shut = closed >> j & 1;
+      m.closed |= j < n && shut;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        m.H[v] = j < n && shut ? t[j][v].y : fmaf(t[j][v].x, m.H[v], t[j][v].y);
+        m.A[v] *= t[j][v].x;
+      }
     }
   }
-  if (ok && w == 0 && q.group > 0 && on && GDR_IN_BOUNDS(q.group <= p.groups))
-#pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = __ldcg(p.carry + (q.group - 1) * p.D + c + v);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    // warp 0's part starts from what enters the group
-    if (w == 0) m.H[v] = m.of(carry[v], v);
     sh.before_A[w][lane * V + v] = m.A[v];
     sh.before_H[w][lane * V + v] = m.H[v];
   }
   if (lane == 0) sh.before_closed[w] = m.closed;
   if (__syncthreads_or(!ok)) return false;
-  const int parts = min(kScanWarps, (q.in_group + per - 1) / per);
 #pragma unroll
   for (int v = 0; v < V; ++v) h[v] = sh.before_H[0][lane * V + v];
-  for (int k = 1; k < parts; ++k)
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      h[v] = sh.before_closed[k] ? sh.before_H[k][lane * V + v]
-                                 : fmaf(sh.before_A[k][lane * V + v], h[v], sh.before_H[k][lane * V + v]);
+  for (int k = 1; k < WARPS; ++k)
+    if (k * PER < q.in_group) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        h[v] = sh.before_closed[k] ? sh.before_H[k][lane * V + v]
+                                   : fmaf(sh.before_A[k][lane * V + v], h[v], sh.before_H[k][lane * V + v]);
+    }
   return true;
 }
 
-// A warp's map goes to shared memory ...
-template <int V>
-__device__ __forceinline__ void share_map(float (&G)[32 * V], float (&A)[32 * V], float (&H)[32 * V],
-                                          int lane, const float (&gs)[V], const float (&h)[V]) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    G[lane * V + v] = gs[v];
-    A[lane * V + v] = expf(gs[v]);
-    H[lane * V + v] = h[v];
-  }
-}
-// ... and this is the map of the tile's tokens before warp w's (after them, for
-// REV).  Its decay is exp of the whole sum.
-template <int V, bool REV>
-__device__ __forceinline__ Map<V> map_before(const TileShared<V> &sh, int w, int lane) {
+// The map of the tile's tokens before warp w's (after them, for REV) from what
+// the warps have shared.  Its decay is exp of the whole sum.
+template <int V, int WARPS, bool REV>
+__device__ __forceinline__ Map<V> map_before(const TileShared<V, WARPS> &sh, int w, int lane) {
   Map<V> m;
   m.identity();
   float gs[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) gs[v] = 0.f;
 #pragma unroll
-  for (int k = 0; k < kScanWarps; ++k) {
-    const int j = REV ? kScanWarps - 1 - k : k;
+  for (int k = 0; k < WARPS; ++k) {
+    const int j = REV ? WARPS - 1 - k : k;
     if (REV ? j > w : j < w) {
       m.closed |= sh.closed[j];
 #pragma unroll
@@ -333,11 +324,12 @@ __device__ __forceinline__ Map<V> map_before(const TileShared<V> &sh, int w, int
 
 // Sequences without tokens, by the blocks of the first tile: what leaves them
 // is what enters them.
+template <int WARPS>
 __device__ __forceinline__ void pass_empty(const GlrArgs &p, const float *src, float *dst, bool pooled,
                                            int c0, int width) {
   if (!dst || !p.cu_seqlens) return;
   const int lane = threadIdx.x & 31;
-  for (int n0 = (threadIdx.x >> 5) * 32; n0 < p.num_seqs; n0 += kScanWarps * 32) {
+  for (int n0 = (threadIdx.x >> 5) * 32; n0 < p.num_seqs; n0 += WARPS * 32) {
     const int n = n0 + lane;
     const bool empty = n < p.num_seqs && __ldg(p.cu_seqlens + n) == __ldg(p.cu_seqlens + n + 1);
     uint32_t todo = __ballot_sync(0xffffffffu, empty);
@@ -346,242 +338,358 @@ __device__ __forceinline__ void pass_empty(const GlrArgs &p, const float *src, f
       todo &= todo - 1;
       const int64_t r = pooled ? state_row(p, k) : k;
       if (r < 0) continue;
-      for (int c = c0 + lane; c < c0 + width && c < p.D; c += 32) dst[r * p.D + c] = src ? src[r * p.D + c] : 0.f;
+      for (int c = c0 + lane; c < c0 + width && c < p.D; c += 32)
+        dst[r * p.D + c] = src ? src[r * p.D + c] : 0.f;
     }
   }
 }
 
-// b_t of a warp's tokens, with the initial state folded in at a sequence's
-// first token: there h = a h0 + b, and nothing before it counts.
-template <int V, bool COMPLEMENT>
-__device__ __forceinline__ void make_inputs(const GlrArgs &p, const Marks &m, int c, bool on,
-                                            const float (&x)[kTok][V], const float (&g)[kTok][V],
-                                            float (&a)[kTok][V], float (&b)[kTok][V]) {
-#pragma unroll
-  for (int i = 0; i < kTok; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      a[i][v] = expf(g[i][v]);
-      b[i][v] = COMPLEMENT ? -expm1f(g[i][v]) * x[i][v] : x[i][v];
-    }
-  if (m.first && p.initial_state) {
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      if (m.first >> i & 1) {
-        const int n = __shfl_sync(0xffffffffu, m.seq, i);
-        const int64_t r = state_row(p, n);
-        if (on && r >= 0 && GDR_IN_BOUNDS(n < p.num_seqs && r < p.num_slots && c + V <= p.D)) {
-          float h0[V];
-          state_load<V>(p.initial_state + r * p.D + c, h0);
-#pragma unroll
-          for (int v = 0; v < V; ++v) b[i][v] = fmaf(a[i][v], h0[v], b[i][v]);
-        }
-      }
-    }
-  }
+// Whether a tile holds the start or the end of a sequence (else its tokens take
+// the path without marks).
+__device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
+  if (p.cu_seqlens) return __ldg(p.tile_marks + tile) != 0;
+  const uint32_t t = tile * kTile, r = t % (uint32_t)p.T;
+  return r == 0 || r + kTile >= (uint32_t)p.T;
 }
 
 // ---- forward ------------------------------------------------------------
-// Reads x and g once and keeps the tokens' a and b in registers while the tile
-// waits for what enters it.  STATES_ONLY: the saved chunk states alone.
+template <typename IO, int V, int TOK> struct Tokens {
+  Raw<IO, V> x[TOK];
+  Raw<float, V> g[TOK];
+  bool marked;
+  __device__ __forceinline__ void load(const GlrArgs &p, uint32_t tile, uint32_t t0, int c, bool on) {
+    const IO *x0 = static_cast<const IO *>(p.x) + (int64_t)t0 * p.ld_x + c;
+    const float *g0 = p.g + (int64_t)t0 * p.ld_g + c;
+    const int n = on ? (int)min((int64_t)TOK, p.tokens - t0) : 0;
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
+      x[i].zero();
+      g[i].zero();
+      if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) {
+        x[i].load(x0 + i * p.ld_x);
+        g[i].load(g0 + i * p.ld_g);
+      }
+    }
+    marked = has_marks(p, tile);
+  }
+};
+
+// Persistent blocks: the loads of a block's next tile are under way while this
+// one waits for what enters it and is written.  x and g are read once; the
+// tokens' a stays in registers in between.  STATES_ONLY: only the saved chunk
+// states are written.
 template <typename IO, int V, bool COMPLEMENT, bool STATES_ONLY>
-__global__ void __launch_bounds__(kScanWarps * 32) glr_scan_kernel(GlrArgs p) {
-  __shared__ TileShared<V> sh;
+__global__ void __launch_bounds__(128, 4) glr_scan_kernel(GlrArgs p) {
+  constexpr int WARPS = 4, TOK = kTile / WARPS;
+  __shared__ TileShared<V, WARPS> sh;
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const Place q = place_of<false>(p, take_tile(p, sh));
-  const int64_t t0 = q.tile * kTile + w * kTok;
-  const int c = (q.stripe * 32 + lane) * V;
-  const bool on = c < p.D;
-  float a[kTok][V], b[kTok][V], gs[V], h[V];
-  Marks m;
+  const uint32_t total = (uint32_t)(p.tiles * p.stripes);
+  if (threadIdx.x == 0) sh.ticket = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : blockIdx.x;
+  __syncthreads();
+  uint32_t ticket = sh.ticket;
+  __syncthreads();
+  if (ticket >= total) return;
+  Place q = place_of<false>(p, ticket);
+  Tokens<IO, V, TOK> k;
   {
-    float x[kTok][V], g[kTok][V];
-    load_tokens<IO, V>(p, t0, c, on, x, g);
-    m = find_marks(p, t0, lane);
-    make_inputs<V, COMPLEMENT>(p, m, c, on, x, g, a, b);
+    const int c = (q.stripe * 32 + lane) * V;
+    k.load(p, q.tile, q.tile * kTile + w * TOK, c, c < p.D);
+  }
+  while (true) {
+    if (threadIdx.x == 0) sh.ticket = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : ticket + gridDim.x;
+    const uint32_t t0 = q.tile * kTile + w * TOK;
+    const int c = (q.stripe * 32 + lane) * V;
+    const bool on = c < p.D;
+    Marks m;
+    m.first = m.last = 0;
+    m.seq = 0;
+    if (k.marked) m = find_marks<TOK>(p, t0, lane);
+    // the span from zeros; b of a token is x, or (1 - a) x
+    float a[TOK][V], b[COMPLEMENT ? TOK : 1][V], gs[V], h[V];
+    Raw<IO, V> x[TOK];
 #pragma unroll
     for (int v = 0; v < V; ++v) gs[v] = h[v] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kTok; ++i)
+    for (int i = 0; i < TOK; ++i) {
+      x[i] = k.x[i];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        h[v] = m.first >> i & 1 ? b[i][v] : fmaf(a[i][v], h[v], b[i][v]);
-        gs[v] += g[i][v];
+        const float g = k.g[i].at(v);
+        a[i][v] = decay<IO>(g);
+        if (COMPLEMENT) b[i][v] = -expm1f(g) * x[i].at(v);
+        gs[v] += g;
       }
-  }
-  share_map<V>(sh.G[w], sh.A[w], sh.H[w], lane, gs, h);
-  if (lane == 0) sh.closed[w] = m.first != 0;
-  __syncthreads();
-  Map<V> before = map_before<V, false>(sh, w, lane);
-  const bool group_end = q.in_group == p.group - 1;
-  if (p.chained && w == kScanWarps - 1 && !group_end) {
-    const Map<V> tile = map_before<V, false>(sh, kScanWarps, lane);
-    publish_map<V>(p, q, tile, c, on, lane);
-  }
-  float in[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) in[v] = 0.f;
-  if (p.chained && !enter_tile<V>(p, sh, q, c, on, w, lane, in)) return;
-  if (w == 0 && on && p.chunk_states && GDR_IN_BOUNDS(q.tile < p.tiles && c + V <= p.D))
-    row<float, V>::store(p.chunk_states + q.tile * p.D + c, in);
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = before.of(in[v], v);
-  if (p.chained && w == kScanWarps - 1 && group_end) {
-    float out[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      out[v] = sh.closed[w] ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], h[v], sh.H[w][lane * V + v]);
-    publish_carry<V>(p, q, out, c, on, lane);
-  }
-  if (STATES_ONLY) return;
-#pragma unroll
-  for (int i = 0; i < kTok; ++i) {
-    const int64_t t = t0 + i;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      h[v] = m.first >> i & 1 ? b[i][v] : fmaf(a[i][v], h[v], b[i][v]);
-    if (on && t < p.tokens && GDR_IN_BOUNDS(c + V <= p.D))
-      row<IO, V>::store(static_cast<IO *>(p.h) + t * p.D + c, h);
-    if (p.final_state && (m.last >> i & 1)) {
-      const int n = __shfl_sync(0xffffffffu, m.seq, i);
-      const int64_t r = state_row(p, n);
-      if (on && r >= 0 && GDR_IN_BOUNDS(n < p.num_seqs && r < p.num_slots && c + V <= p.D))
-        row<float, V>::store(p.final_state + r * p.D + c, h);
     }
+    auto b_of = [&](int i, int v) { return COMPLEMENT ? b[COMPLEMENT ? i : 0][v] : x[i].at(v); };
+    if (m.first == 0) {
+#pragma unroll
+      for (int i = 0; i < TOK; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+    } else {
+#pragma unroll
+      for (int i = 0; i < TOK; ++i) {
+        if (m.first >> i & 1) {
+          // a start's state takes the place of its a: the initial state is read
+          // once, before the map is published (the sequence's last tile may
+          // write the final state over it as soon as that is done)
+          float h0[V];
+          initial_of<V>(p, __shfl_sync(0xffffffffu, m.seq, i), c, on, h0);
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[v] = a[i][v] = fmaf(a[i][v], h0[v], b_of(i, v));
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+        }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      sh.G[w][lane * V + v] = gs[v];
+      sh.A[w][lane * V + v] = expf(gs[v]);
+      sh.H[w][lane * V + v] = h[v];
+    }
+    if (lane == 0) sh.closed[w] = m.first != 0;
+    __syncthreads();
+    // the next tile's loads
+    const uint32_t next = sh.ticket;
+    const Place nq = place_of<false>(p, next < total ? next : 0);
+    {
+      const int nc = (nq.stripe * 32 + lane) * V;
+      k.load(p, nq.tile, nq.tile * kTile + w * TOK, nc, next < total && nc < p.D);
+    }
+    const bool group_end = q.in_group == kGroup - 1;
+    if (p.chained && w == WARPS - 1 && !group_end)
+      publish_map<V>(p, q, map_before<V, WARPS, false>(sh, WARPS, lane), c, on, lane);
+    const Map<V> before = map_before<V, WARPS, false>(sh, w, lane);
+    float in[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) in[v] = 0.f;
+    if (p.chained) {
+      if (!enter_tile<V, WARPS>(p, sh, q, c, on, w, lane, in)) return;
+    } else {
+      __syncthreads();  // the maps are read before the next tile's are written
+    }
+    if (w == 0 && on && p.chunk_states && GDR_IN_BOUNDS(q.tile < p.tiles && c + V <= p.D))
+      store_row<float, V>(p.chunk_states + (int64_t)q.tile * p.D + c, in);
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = before.of(in[v], v);
+    if (p.chained && w == WARPS - 1 && group_end) {
+      float out[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        out[v] = m.first ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], h[v], sh.H[w][lane * V + v]);
+      publish_carry<V>(p, q, out, c, on, lane);
+    }
+    if (!STATES_ONLY) {
+      IO *out = static_cast<IO *>(p.h) + (int64_t)t0 * p.D + c;
+      const int n = on ? (int)min((int64_t)TOK, p.tokens - t0) : 0;
+      if ((m.first | m.last) == 0) {
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+          if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) store_row<IO, V>(out + (int64_t)i * p.D, h);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) {
+          const int s = __shfl_sync(0xffffffffu, m.seq, i);
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[v] = m.first >> i & 1 ? a[i][v] : fmaf(a[i][v], h[v], b_of(i, v));
+          if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) store_row<IO, V>(out + (int64_t)i * p.D, h);
+          if ((m.last >> i & 1) && p.final_state) {
+            const int64_t r = state_row(p, s);
+            if (on && r >= 0 && GDR_IN_BOUNDS(s < p.num_seqs && r < p.num_slots && c + V <= p.D))
+              store_row<float, V>(p.final_state + r * p.D + c, h);
+          }
+        }
+      }
+      if (q.tile == 0) pass_empty<WARPS>(p, p.initial_state, p.final_state, true, q.stripe * 32 * V, 32 * V);
+    }
+    if (next >= total) return;
+    ticket = next;
+    q = nq;
   }
-  if (q.tile == 0) pass_empty(p, p.initial_state, p.final_state, true, q.stripe * 32 * V, 32 * V);
 }
 
 // ---- backward -----------------------------------------------------------
 // The states again from what enters the tile (saved), the gradients from what
 // enters it from the tokens after it (chained): x, g and dh are read once.
 template <typename IO, int V, bool COMPLEMENT>
-__global__ void __launch_bounds__(kScanWarps * 32) glr_gradient_kernel(GlrArgs p) {
-  __shared__ TileShared<V> sh;
-  __shared__ float state_H[kScanWarps][32 * V];
-  __shared__ bool state_closed[kScanWarps];
+__global__ void __launch_bounds__(256, 2) glr_gradient_kernel(GlrArgs p) {
+  constexpr int WARPS = 8, TOK = kTile / WARPS;
+  __shared__ TileShared<V, WARPS> sh;
+  __shared__ float state_H[WARPS][32 * V];
+  __shared__ bool state_closed[WARPS];
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const Place pl = place_of<true>(p, take_tile(p, sh));
-  const int64_t t0 = pl.tile * kTile + w * kTok;
-  const int c = (pl.stripe * 32 + lane) * V;
-  const bool on = c < p.D;
-  float x[kTok][V], g[kTok][V], a[kTok][V], b[kTok][V], d[kTok][V];
-  load_tokens<IO, V>(p, t0, c, on, x, g);
-#pragma unroll
-  for (int i = 0; i < kTok; ++i) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) d[i][v] = 0.f;
-    if (on && t0 + i < p.tokens && GDR_IN_BOUNDS(c + V <= p.D))
-      row<IO, V>::load(static_cast<const IO *>(p.dh) + (t0 + i) * p.ld_dh + c, d[i]);
-  }
-  float h[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = 0.f;
-  if (on && GDR_IN_BOUNDS(pl.tile < p.tiles && c + V <= p.D))
-    row<float, V>::load(p.chunk_states + pl.tile * p.D + c, h);
-  const Marks m = find_marks(p, t0, lane);
-  make_inputs<V, COMPLEMENT>(p, m, c, on, x, g, a, b);
-  float gs[V], s[V], q[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) gs[v] = s[v] = q[v] = 0.f;
-#pragma unroll
-  for (int i = 0; i < kTok; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s[v] = m.first >> i & 1 ? b[i][v] : fmaf(a[i][v], s[v], b[i][v]);
-      gs[v] += g[i][v];
-    }
-#pragma unroll
-  for (int i = kTok - 1; i >= 0; --i) {
-    const int n = __shfl_sync(0xffffffffu, m.seq, i);
-    const bool last = m.last >> i & 1;  // the gradient of the sequence's final state enters here
-    float df[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) df[v] = 0.f;
-    if (last && p.dfinal && on && GDR_IN_BOUNDS(n < p.num_seqs))
-      row<float, V>::load(p.dfinal + (int64_t)n * p.D + c, df);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (last) {
-        d[i][v] += df[v];
-        q[v] = 0.f;
-      }
-      q[v] = a[i][v] * (d[i][v] + q[v]);
-    }
-  }
-  share_map<V>(sh.G[w], sh.A[w], sh.H[w], lane, gs, q);
-#pragma unroll
-  for (int v = 0; v < V; ++v) state_H[w][lane * V + v] = s[v];
-  if (lane == 0) {
-    sh.closed[w] = m.last != 0;
-    state_closed[w] = m.first != 0;
-  }
+  const uint32_t total = (uint32_t)(p.tiles * p.stripes);
+  if (threadIdx.x == 0) sh.ticket = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : blockIdx.x;
   __syncthreads();
-  for (int k = 0; k < w; ++k)  // the state that enters the warp
+  uint32_t ticket = sh.ticket;
+  __syncthreads();
+  if (ticket >= total) return;
+  Place q = place_of<true>(p, ticket);
+  Tokens<IO, V, TOK> k;
+  Raw<IO, V> kd[TOK];
+  float kh[V];
+  auto load = [&](const Place &at, bool live) {
+    const uint32_t t0 = at.tile * kTile + w * TOK;
+    const int c = (at.stripe * 32 + lane) * V;
+    const bool on = live && c < p.D;
+    k.load(p, at.tile, t0, c, on);
+    const IO *d0 = static_cast<const IO *>(p.dh) + (int64_t)t0 * p.ld_dh + c;
+    const int n = on ? (int)min((int64_t)TOK, p.tokens - t0) : 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      h[v] = state_closed[k] ? state_H[k][lane * V + v]
-                             : fmaf(sh.A[k][lane * V + v], h[v], state_H[k][lane * V + v]);
-  Map<V> after = map_before<V, true>(sh, w, lane);
-  const bool group_end = pl.in_group == p.group - 1;
-  if (p.chained && w == 0 && !group_end) {
-    const Map<V> tile = map_before<V, true>(sh, -1, lane);
-    publish_map<V>(p, pl, tile, c, on, lane);
-  }
-  float in[V];
+    for (int i = 0; i < TOK; ++i) {
+      kd[i].zero();
+      if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) kd[i].load(d0 + i * p.ld_dh);
+    }
 #pragma unroll
-  for (int v = 0; v < V; ++v) in[v] = 0.f;
-  if (p.chained && !enter_tile<V>(p, sh, pl, c, on, w, lane, in)) return;
-#pragma unroll
-  for (int v = 0; v < V; ++v) q[v] = after.of(in[v], v);
-  if (p.chained && w == 0 && group_end) {
-    float out[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      out[v] = sh.closed[w] ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], q[v], sh.H[w][lane * V + v]);
-    publish_carry<V>(p, pl, out, c, on, lane);
-  }
-  float before[kTok][V];  // h_{t-1}
-#pragma unroll
-  for (int i = 0; i < kTok; ++i) {
-    const bool first = m.first >> i & 1;
+    for (int v = 0; v < V; ++v) kh[v] = 0.f;
+    if (on && GDR_IN_BOUNDS(at.tile < p.tiles && c + V <= p.D))
+      load_state<V>(p.chunk_states + (int64_t)at.tile * p.D + c, kh);
+  };
+  load(q, true);
+  while (true) {
+    if (threadIdx.x == 0) sh.ticket = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : ticket + gridDim.x;
+    const uint32_t t0 = q.tile * kTile + w * TOK;
+    const int c = (q.stripe * 32 + lane) * V;
+    const bool on = c < p.D;
+    Marks m;
+    m.first = m.last = 0;
+    m.seq = 0;
+    if (k.marked) m = find_marks<TOK>(p, t0, lane);
+    float a[TOK][V], u[COMPLEMENT ? TOK : 1][V], x[TOK][V], d[TOK][V], gs[V], s[V], qv[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      before[i][v] = first ? 0.f : h[v];
-      h[v] = first ? b[i][v] : fmaf(a[i][v], h[v], b[i][v]);
+      gs[v] = s[v] = qv[v] = 0.f;
+      h[v] = kh[v];
     }
-    if (first && p.initial_state) {
-      const int n = __shfl_sync(0xffffffffu, m.seq, i);
-      if (on && GDR_IN_BOUNDS(n < p.num_seqs))
-        state_load<V>(p.initial_state + (int64_t)n * p.D + c, before[i]);
-    }
-  }
 #pragma unroll
-  for (int i = kTok - 1; i >= 0; --i) {
-    const int64_t t = t0 + i;
-    const int n = __shfl_sync(0xffffffffu, m.seq, i);
-    float dx[V], dg[V];
+    for (int i = 0; i < TOK; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float g = k.g[i].at(v);
+        a[i][v] = decay<IO>(g);
+        if (COMPLEMENT) u[i][v] = -expm1f(g);
+        x[i][v] = k.x[i].at(v);
+        d[i][v] = kd[i].at(v);
+        gs[v] += g;
+      }
+    auto b_of = [&](int i, int v) { return COMPLEMENT ? u[COMPLEMENT ? i : 0][v] * x[i][v] : x[i][v]; };
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
+      if (m.first >> i & 1) initial_of<V>(p, __shfl_sync(0xffffffffu, m.seq, i), c, on, s);
+#pragma unroll
+      for (int v = 0; v < V; ++v) s[v] = fmaf(a[i][v], s[v], b_of(i, v));
+    }
+#pragma unroll
+    for (int i = TOK - 1; i >= 0; --i) {
+      if (m.last >> i & 1) {  // the gradient of the sequence's final state enters here
+        const int n = __shfl_sync(0xffffffffu, m.seq, i);
+        float df[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) df[v] = 0.f;
+        if (p.dfinal && on && GDR_IN_BOUNDS(n < p.num_seqs && c + V <= p.D))
+          load_state<V>(p.dfinal + (int64_t)n * p.D + c, df);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          d[i][v] += df[v];
+          qv[v] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) qv[v] = a[i][v] * (d[i][v] + qv[v]);
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float dt = m.last >> i & 1 ? d[i][v] : d[i][v] + q[v];
-      q[v] = a[i][v] * dt;
-      dx[v] = COMPLEMENT ? -expm1f(g[i][v]) * dt : dt;
-      dg[v] = q[v] * (COMPLEMENT ? before[i][v] - x[i][v] : before[i][v]);
+      sh.G[w][lane * V + v] = gs[v];
+      sh.A[w][lane * V + v] = expf(gs[v]);
+      sh.H[w][lane * V + v] = qv[v];
+      state_H[w][lane * V + v] = s[v];
     }
-    if (on && t < p.tokens && GDR_IN_BOUNDS(c + V <= p.D)) {
-      row<IO, V>::store(static_cast<IO *>(p.dx) + t * p.D + c, dx);
-      row<float, V>::store(p.dg + t * p.D + c, dg);
-      if (p.dinitial && (m.first >> i & 1) && GDR_IN_BOUNDS(n < p.num_seqs))
-        row<float, V>::store(p.dinitial + (int64_t)n * p.D + c, q);
+    if (lane == 0) {
+      sh.closed[w] = m.last != 0;
+      state_closed[w] = m.first != 0;
     }
+    __syncthreads();
+    const uint32_t next = sh.ticket;
+    const Place nq = place_of<true>(p, next < total ? next : 0);
+    load(nq, next < total);
+#pragma unroll
+    for (int j = 0; j < WARPS - 1; ++j)  // the state that enters the warp
+      if (j < w)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          h[v] = state_closed[j] ? state_H[j][lane * V + v]
+                                 : fmaf(sh.A[j][lane * V + v], h[v], state_H[j][lane * V + v]);
+    const bool group_end = q.in_group == kGroup - 1;
+    if (p.chained && w == 0 && !group_end)
+      publish_map<V>(p, q, map_before<V, WARPS, true>(sh, -1, lane), c, on, lane);
+    const Map<V> after = map_before<V, WARPS, true>(sh, w, lane);
+    float in[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) in[v] = 0.f;
+    if (p.chained) {
+      if (!enter_tile<V, WARPS>(p, sh, q, c, on, w, lane, in)) return;
+    } else {
+      __syncthreads();  // the maps are read before the next tile's are written
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) qv[v] = after.of(in[v], v);
+    if (p.chained && w == 0 && group_end) {
+      float out[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        out[v] = m.last ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], qv[v], sh.H[w][lane * V + v]);
+      publish_carry<V>(p, q, out, c, on, lane);
+    }
+    float before[TOK][V];  // h_{t-1}
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
+      if (m.first >> i & 1) initial_of<V>(p, __shfl_sync(0xffffffffu, m.seq, i), c, on, h);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        before[i][v] = COMPLEMENT ? h[v] - x[i][v] : h[v];
+        h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+      }
+    }
+    IO *dx0 = static_cast<IO *>(p.dx) + (int64_t)t0 * p.D + c;
+    float *dg0 = p.dg + (int64_t)t0 * p.D + c;
+    const int n = on ? (int)min((int64_t)TOK, p.tokens - t0) : 0;
+#pragma unroll
+    for (int i = TOK - 1; i >= 0; --i) {
+      float dx[V], dg[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float dt = m.last >> i & 1 ? d[i][v] : d[i][v] + qv[v];
+        qv[v] = a[i][v] * dt;
+        dx[v] = COMPLEMENT ? u[COMPLEMENT ? i : 0][v] * dt : dt;
+        dg[v] = qv[v] * before[i][v];
+      }
+      if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) {
+        store_row<IO, V>(dx0 + (int64_t)i * p.D, dx);
+        store_row<float, V>(dg0 + (int64_t)i * p.D, dg);
+      }
+      if (p.dinitial && (m.first >> i & 1)) {
+        const int sq = __shfl_sync(0xffffffffu, m.seq, i);
+        if (on && GDR_IN_BOUNDS(sq < p.num_seqs && c + V <= p.D))
+          store_row<float, V>(p.dinitial + (int64_t)sq * p.D + c, qv);
+      }
+    }
+    if (q.tile == 0) pass_empty<WARPS>(p, p.dfinal, p.dinitial, false, q.stripe * 32 * V, 32 * V);
+    if (next >= total) return;
+    ticket = next;
+    q = nq;
   }
-  if (pl.tile == 0) pass_empty(p, p.dfinal, p.dinitial, false, pl.stripe * 32 * V, 32 * V);
 }
 
-// Before the chained kernels: zeroes the ticket and the flags, checks the packed
-// offsets and writes the status word.
+// Before the scan kernels: zeroes the ticket and the flags, checks the packed
+// offsets, writes the status word and marks the tiles in which a sequence
+// begins or ends.
 __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words) {
   if (blockIdx.x == 0) {
     bool bad = false;
@@ -594,8 +702,19 @@ __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) *p.status = bad ? KDA_DEVICE_BAD_CU_SEQLENS : KDA_DEVICE_OK;
   }
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (int64_t)gridDim.x * blockDim.x)
-    p.ticket[i] = 0;
+  const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = at; i < words; i += step) p.ticket[i] = 0;
+  if (p.cu_seqlens && p.num_seqs > 0)
+    for (int64_t tile = at; tile < p.tiles; tile += step) {
+      const int64_t t = tile * kTile;
+      int lo = 0, hi = p.num_seqs;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.cu_seqlens[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      p.tile_marks[tile] = p.cu_seqlens[lo] == t || p.cu_seqlens[lo + 1] <= t + kTile;
+    }
 }
 
 // Without any token: what leaves each sequence is what enters it.
@@ -616,19 +735,21 @@ __global__ void __launch_bounds__(256) glr_step_kernel(GlrArgs p) {
   if (c >= p.D) return;
   for (int n = blockIdx.y; n < p.num_seqs; n += gridDim.y) {
     const int64_t r = state_row(p, n);
-    float x[V], g[V], h[V];
+    float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = 0.f;
     if (r >= 0 && GDR_IN_BOUNDS(r < p.num_slots && c + V <= p.D)) {
-      row<IO, V>::load(static_cast<const IO *>(p.x) + n * p.ld_x + c, x);
-      row<float, V>::load(p.g + n * p.ld_g + c, g);
-      state_load<V>(p.final_state + r * p.D + c, h);
+      Raw<IO, V> x;
+      Raw<float, V> g;
+      x.load(static_cast<const IO *>(p.x) + n * p.ld_x + c);
+      g.load(p.g + n * p.ld_g + c);
+      load_state<V>(p.final_state + r * p.D + c, h);
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        h[v] = fmaf(expf(g[v]), h[v], COMPLEMENT ? -expm1f(g[v]) * x[v] : x[v]);
-      row<float, V>::store(p.final_state + r * p.D + c, h);
+        h[v] = fmaf(expf(g.at(v)), h[v], COMPLEMENT ? -expm1f(g.at(v)) * x.at(v) : x.at(v));
+      store_row<float, V>(p.final_state + r * p.D + c, h);
     }
-    row<IO, V>::store(static_cast<IO *>(p.h) + (int64_t)n * p.D + c, h);
+    if (GDR_IN_BOUNDS(c + V <= p.D)) store_row<IO, V>(static_cast<IO *>(p.h) + (int64_t)n * p.D + c, h);
   }
 }
 
@@ -646,7 +767,7 @@ bool pairs_ok(const GlrArgs &p) {
 
 cudaError_t launch_begin(const GlrArgs &p, cudaStream_t s) {
   const int64_t words = p.chained ? 1 + (p.tiles + p.groups) * p.stripes : 0;
-  const int64_t want = (words + 1023) / 1024;
+  const int64_t most = words > p.tiles ? words : p.tiles, want = (most + 1023) / 1024;
   TraceScope tr("glr_begin_kernel", s);
   glr_begin_kernel<<<(unsigned)(want < 1 ? 1 : want > 148 ? 148 : want), 256, 0, s>>>(p, words);
   return cudaGetLastError();
@@ -665,11 +786,16 @@ template <int V> GlrArgs with_chain(const GlrArgs &a) {
   GlrArgs p = a;
   p.stripes = (p.D + 32 * V - 1) / (32 * V);
   p.chained = p.tiles > 1 && (p.cu_seqlens || p.T > kTile || kTile % p.T != 0);
-  p.group = 4 * kScanWarps;
-  p.groups = (p.tiles + p.group - 1) / p.group;
+  p.groups = (p.tiles + kGroup - 1) / kGroup;
   p.tile_flag = p.ticket + 1;
   p.carry_flag = p.tile_flag + p.tiles * p.stripes;
   return p;
+}
+
+// As many blocks as run at once, or one a tile.
+unsigned persistent_grid(const GlrArgs &p, int per_sm) {
+  const int64_t tiles = p.tiles * p.stripes, most = (int64_t)sm_count() * per_sm;
+  return (unsigned)(tiles < most ? tiles : most);
 }
 
 template <typename IO, int V, bool COMPLEMENT>
@@ -679,27 +805,26 @@ cudaError_t launch_fwd(const GlrArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, false, s);
   TraceScope tr("glr_scan_kernel", s);
-  glr_scan_kernel<IO, V, COMPLEMENT, false><<<(unsigned)(p.tiles * p.stripes), kScanWarps * 32, 0, s>>>(p);
+  glr_scan_kernel<IO, V, COMPLEMENT, false><<<persistent_grid(p, 4), 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename IO, int V, bool COMPLEMENT>
 cudaError_t launch_bwd(const GlrArgs &a, cudaStream_t s) {
-  GlrArgs p = with_chain<V>(a);
+  const GlrArgs p = with_chain<V>(a);
   cudaError_t e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, true, s);
-  const unsigned grid = (unsigned)(p.tiles * p.stripes);
   if (p.own_chunks) {
     {
       TraceScope tr("glr_scan_kernel", s);
-      glr_scan_kernel<IO, V, COMPLEMENT, true><<<grid, kScanWarps * 32, 0, s>>>(p);
+      glr_scan_kernel<IO, V, COMPLEMENT, true><<<persistent_grid(p, 4), 128, 0, s>>>(p);
     }
     e = launch_begin(p, s);
     if (e != cudaSuccess) return e;
   }
   TraceScope tr("glr_gradient_kernel", s);
-  glr_gradient_kernel<IO, V, COMPLEMENT><<<grid, kScanWarps * 32, 0, s>>>(p);
+  glr_gradient_kernel<IO, V, COMPLEMENT><<<persistent_grid(p, 2), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -125,10 +125,11 @@ struct GlrArgs {
   int32_t *status;
   int32_t *ticket;  // followed by the flags of the tiles, then of the groups
   float *tile_map, *carry;
+  int32_t *tile_marks;  // packed: whether a sequence begins or ends in the tile
   bool own_chunks;  // backward: chunk_states is workspace, to be filled first
   // set at the launch
   int32_t *tile_flag, *carry_flag;
-  int stripes, group;
+  int stripes;
   int64_t groups;
   bool chained;
 };

@@ -44,6 +44,7 @@ def _bwd(**over):
     (dict(dh=None), ARG), (dict(x=None), ARG), (dict(g=None), ARG), (dict(dx=None), ARG), (dict(dg=None), ARG),
     (dict(ld_dh=4), ARG), (dict(dh=FAKE + 1), ARG), (dict(df=FAKE + 2), ARG), (dict(dh0=FAKE + 2), ARG),
     (dict(dx=FAKE), ARG), (dict(dg=FAKE + 8192), ARG), (dict(dx=FAKE + 4096), ARG),  # aliases
+    (dict(h0=FAKE, dh0=FAKE), ARG), (dict(df=FAKE, dh0=FAKE), ARG),
     (dict(input=3), ARG), (dict(io=2), ARG), (dict(D=-1), ARG), (dict(cu=FAKE, n=1, B=3), ARG),
     (dict(ws=None), WORKSPACE), (dict(ws=FAKE + 128), WORKSPACE), (dict(ws_bytes=0), WORKSPACE),
 ])

@@ -250,6 +250,22 @@ def test_state_pool_in_place(T):
     assert torch.equal(pool[rest], pool0[rest])
 
 
+def test_many_sequences_over_many_tiles_in_place():
+    """A sequence's last tile writes the slot that its first tile reads."""
+    import torch
+    import gated_delta_rule_87_b200 as gdr
+    N, T, D = 60, 70, 256
+    d, a = _inputs(N * T, D, N, "f32", seed=21)
+    rh, rf, eh, ef = R.scan(a["x"], a["g"], a["h0"], [T * n for n in range(N + 1)], False)
+    slots = torch.randperm(N, device="cuda").to(torch.int32)
+    for _ in range(20):
+        pool = torch.empty((N, D), device="cuda")
+        pool[slots.long()] = d["h0"]
+        h, _, _, _ = gdr.glr_scan_fwd(d["x"].view(N, T, D), d["g"].view(N, T, D), state_pool=pool, state_slots=slots)
+        R.check(_host(h), rh, eh, "f32", "h")
+        R.check(_host(pool[slots.long()]), rf, ef, "f32", "pool")
+
+
 def test_empty_sequences_in_a_pool_leave_their_slots():
     import torch
     import gated_delta_rule_87_b200 as gdr
