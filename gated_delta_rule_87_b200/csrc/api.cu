@@ -594,23 +594,21 @@ bool io_aligned(const void *p, bool bf16) {
   return (reinterpret_cast<uintptr_t>(p) & (bf16 ? 1u : 3u)) == 0;
 }
 
-// Workspace of a scan: the status word, then what its tiles hand over.  Stripes
-// are counted at their narrowest (32 channels) and groups at their shortest.
+// Workspace of a scan: the status word and the ticket, the tiles that hold a
+// sequence's start or end, the words that tiles and groups of tiles hand over.
 struct GlrLayout {
-  int64_t tiles;
-  size_t flags, marks, map, carry, chunks, total;
+  int64_t tiles, pitch;
+  size_t marks, map, chunks, total;
 };
 GlrLayout glr_layout(int64_t tokens, int64_t D, bool own_chunks) {
   GlrLayout L{};
   L.tiles = (tokens + gdr::kGlrChunk - 1) / gdr::kGlrChunk;
-  const size_t per = (size_t)L.tiles * D * sizeof(float), stripes = (size_t)(D + 31) / 32;
+  L.pitch = D + (D & 1);
   const size_t groups = (size_t)L.tiles / gdr::kGlrShortestGroup + 1;
   size_t off = kStatusBytes;
-  L.flags = off; off = up256(off + (1 + (L.tiles + groups) * stripes) * sizeof(int32_t));
   L.marks = off; off = up256(off + (size_t)L.tiles * sizeof(int32_t));
-  L.map = off; off = up256(off + 2 * per);
-  L.carry = off; off = up256(off + groups * D * sizeof(float));
-  L.chunks = off; off = up256(off + (own_chunks ? per : 0));
+  L.map = off; off = up256(off + (L.tiles + groups) * L.pitch * sizeof(uint64_t));
+  L.chunks = off; off = up256(off + (own_chunks ? (size_t)L.tiles * D * sizeof(float) : 0));
   L.total = off;
   return L;
 }
@@ -657,10 +655,10 @@ kda_status_t check_glr(gdr::GlrArgs &a, int32_t B, glr_input_t input, kda_dtype_
   unsigned char *w = static_cast<unsigned char *>(workspace);
   a.tiles = L.tiles;
   a.status = reinterpret_cast<int32_t *>(w);
-  a.ticket = reinterpret_cast<int32_t *>(w + L.flags);
+  a.ticket = a.status + 32;
+  a.pitch = L.pitch;
   a.tile_marks = reinterpret_cast<int32_t *>(w + L.marks);
-  a.tile_map = reinterpret_cast<float *>(w + L.map);
-  a.carry = reinterpret_cast<float *>(w + L.carry);
+  a.tile_map = reinterpret_cast<uint64_t *>(w + L.map);
   if (a.own_chunks) a.chunk_states = reinterpret_cast<float *>(w + L.chunks);
   // a block a tile of 64 tokens x 32 channels at least
   if (a.tiles * ((a.D + 31) / 32) > INT32_MAX)

@@ -164,27 +164,31 @@ template <int V, int WARPS> struct TileShared {
 // timing.
 constexpr int kGroup = 16;
 static_assert(kGroup >= kGlrShortestGroup, "the workspace counts groups of at least this length");
-constexpr int kMapOpen = 1, kMapClosed = 2;
 constexpr uint32_t kMaxChainPolls = 1u << 20;  // about a second
 
-__device__ __forceinline__ int load_acquire(const int32_t *p) {
-  int v;
-  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
+// A channel's map goes through the workspace as one 64-bit word, which is its
+// own flag (no fence): H below, above it A with the sign bit set (A >= 0), or a
+// code for a closed span.  0: not there yet.
+constexpr uint32_t kClosedCode = 0xffbfffffu, kNanCode = 0xffffffffu;
+__device__ __forceinline__ uint64_t pack_map(float A, float H, bool closed) {
+  const uint32_t a = closed ? kClosedCode : A == A ? __float_as_uint(A) | 0x80000000u : kNanCode;
+  return (uint64_t)a << 32 | __float_as_uint(H);
 }
-__device__ __forceinline__ void store_release(int32_t *p, int v) {
-  asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
+__device__ __forceinline__ bool word_closed(uint64_t u) { return (uint32_t)(u >> 32) == kClosedCode; }
+__device__ __forceinline__ float word_A(uint64_t u) { return __uint_as_float((uint32_t)(u >> 32) & 0x7fffffffu); }
+__device__ __forceinline__ float word_H(uint64_t u) { return __uint_as_float((uint32_t)u); }
 
-// Waits for a flag; 0 if it gave up (or another block did: the status word says so).
-__device__ __forceinline__ int wait_flag(const GlrArgs &p, const int32_t *flag) {
-  for (uint32_t i = 0; i < kMaxChainPolls; ++i) {
-    const int v = load_acquire(flag);
-    if (v) return v;
-    if ((i & 1023) == 1023 && load_acquire(p.status) != KDA_DEVICE_OK) return 0;
-  }
-  *p.status = KDA_DEVICE_TIMEOUT;
-  return 0;
+template <int V> __device__ __forceinline__ void load_words(const uint64_t *p, uint64_t (&u)[V]) {
+  if constexpr (V == 2)
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(u[0]), "=l"(u[1]) : "l"(p) : "memory");
+  else
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(u[0]) : "l"(p) : "memory");
+}
+template <int V> __device__ __forceinline__ void store_words(uint64_t *p, const uint64_t (&u)[V]) {
+  if constexpr (V == 2)
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(u[0]), "l"(u[1]) : "memory");
+  else
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(u[0]) : "memory");
 }
 
 // The place of a ticket's tile in the chain (REV: from the last tile on).
@@ -203,78 +207,78 @@ template <bool REV> __device__ __forceinline__ Place place_of(const GlrArgs &p, 
   return q;
 }
 
-// Publishes a tile's map (one warp, the tile's 32 V channels).
+// Publishes a tile's map, or what leaves its group (one warp, the tile's 32 V channels).
 template <int V>
-__device__ __forceinline__ void publish_map(const GlrArgs &p, const Place &q, const Map<V> &m, int c,
-                                            bool on, int lane) {
+__device__ __forceinline__ void publish_map(const GlrArgs &p, const Place &q, const Map<V> &m, int c, bool on) {
   if (on && GDR_IN_BOUNDS(q.step < p.tiles && c + V <= p.D)) {
-    float2 *to = reinterpret_cast<float2 *>(p.tile_map) + (int64_t)q.step * p.D + c;
+    uint64_t u[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) __stcg(to + v, make_float2(m.A[v], m.H[v]));
+    for (int v = 0; v < V; ++v) u[v] = pack_map(m.A[v], m.H[v], m.closed);
+    store_words<V>(p.tile_map + (int64_t)q.step * p.pitch + c, u);
   }
-  __threadfence();
-  __syncwarp();
-  if (lane == 0)
-    store_release(p.tile_flag + (int64_t)q.step * p.stripes + q.stripe, m.closed ? kMapClosed : kMapOpen);
 }
 template <int V>
-__device__ __forceinline__ void publish_carry(const GlrArgs &p, const Place &q, const float (&h)[V],
-                                              int c, bool on, int lane) {
+__device__ __forceinline__ void publish_carry(const GlrArgs &p, const Place &q, const float (&h)[V], int c, bool on) {
   if (on && GDR_IN_BOUNDS(q.group < p.groups && c + V <= p.D)) {
+    uint64_t u[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) __stcg(p.carry + (int64_t)q.group * p.D + c + v, h[v]);
+    for (int v = 0; v < V; ++v) u[v] = pack_map(0.f, h[v], true);
+    store_words<V>(p.carry + (int64_t)q.group * p.pitch + c, u);
   }
-  __threadfence();
-  __syncwarp();
-  if (lane == 0) store_release(p.carry_flag + (int64_t)q.group * p.stripes + q.stripe, kMapOpen);
 }
 
-// What enters the tile.  Each warp joins its part of the group's earlier maps,
-// then all join the parts.  Every thread of the block takes part.  False: a wait gave up.
+// What enters the tile.  Each warp joins its part of the group's earlier maps
+// (the first warp's part starts from what enters the group, a closed word), then
+// all join the parts.  Every thread of the block takes part.  False: a wait gave up.
 template <int V, int WARPS>
 __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared<V, WARPS> &sh, const Place &q,
                                            int c, bool on, int w, int lane, float (&h)[V]) {
   constexpr int PER = kGroup / WARPS;  // maps a warp joins
-  Map<V> m;
-  m.identity();
   const int j0 = w * PER;
-  const int n = min(PER, q.in_group - j0);  // <= 0: none
-  const uint32_t first = q.group * kGroup + j0;
-  int flag = kMapOpen;
-  if (lane < n) flag = wait_flag(p, p.tile_flag + (int64_t)(first + lane) * p.stripes + q.stripe);
-  if (w == 0 && lane == 31 && q.group > 0)  // warp 0's part starts from what enters the group
-    flag = wait_flag(p, p.carry_flag + (int64_t)(q.group - 1) * p.stripes + q.stripe);
-  const bool ok = __all_sync(0xffffffffu, flag != 0);
-  const uint32_t closed = __ballot_sync(0xffffffffu, flag == kMapClosed);
-  if (ok) {
-    float2 t[PER][V];
-    float carry[V];
+  const int n = on ? min(PER, q.in_group - j0) : 0;  // <= 0: none
+  const bool start = on && w == 0 && q.group > 0;
+  const uint64_t *maps = p.tile_map + (int64_t)(q.group * kGroup + j0) * p.pitch + c;
+  const uint64_t *carry = p.carry + (int64_t)(q.group - 1) * p.pitch + c;
+  uint64_t t[PER][V], s[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = 0.f;
-    if (w == 0 && q.group > 0 && on && GDR_IN_BOUNDS(q.group <= p.groups && c + V <= p.D))
+  for (int v = 0; v < V; ++v) s[v] = 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = __ldcg(p.carry + (int64_t)(q.group - 1) * p.D + c + v);
+  for (int j = 0; j < PER; ++j)
+#pragma unroll
+    for (int v = 0; v < V; ++v) t[j][v] = 0;
+  bool ok = false;
+  for (uint32_t poll = 0; poll < kMaxChainPolls; ++poll) {
+    // loads what is missing; a lane's channels come and go together or not
+    bool have = true;
+    if (start && (s[0] == 0 || s[V - 1] == 0) && GDR_IN_BOUNDS(q.group <= p.groups && c + V <= p.D)) load_words<V>(carry, s);
 #pragma unroll
     for (int j = 0; j < PER; ++j)
+      if (j < n && (t[j][0] == 0 || t[j][V - 1] == 0) && GDR_IN_BOUNDS(q.step < p.tiles && c + V <= p.D))
+        load_words<V>(maps + (int64_t)j * p.pitch, t[j]);
+    if (start) have = s[0] != 0 && s[V - 1] != 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (j < n) have = have && t[j][0] != 0 && t[j][V - 1] != 0;
+    ok = __all_sync(0xffffffffu, have);
+    if (ok) break;
+    if ((poll & 1023) == 1023 && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK) break;
+    if (poll == kMaxChainPolls - 1) *p.status = KDA_DEVICE_TIMEOUT;
+  }
+  Map<V> m;
+  m.identity();
+#pragma unroll
+  for (int v = 0; v < V; ++v) m.H[v] = word_H(s[v]);
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (j < n) {
+      const bool shut = word_closed(t[j][0]);
+      m.closed |= shut;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        t[j][v] = make_float2(1.f, 0.f);
-        if (j < n && on && GDR_IN_BOUNDS(first + j < p.tiles && c + V <= p.D))
-          t[j][v] = __ldcg(reinterpret_cast<const float2 *>(p.tile_map) + (int64_t)(first + j) * p.D + c + v);
-      }
-#pragma unroll
-    for (int v = 0; v < V; ++v) m.H[v] = carry[v];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const bool shut = closed >> j & 1;
-      m.closed |= j < n && shut;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        m.H[v] = j < n && shut ? t[j][v].y : fmaf(t[j][v].x, m.H[v], t[j][v].y);
-        m.A[v] *= t[j][v].x;
+        m.H[v] = shut ? word_H(t[j][v]) : fmaf(word_A(t[j][v]), m.H[v], word_H(t[j][v]));
+        m.A[v] *= word_A(t[j][v]);
       }
     }
-  }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     sh.before_A[w][lane * V + v] = m.A[v];
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(128, 4) glr_scan_kernel(GlrArgs p) {
     }
     const bool group_end = q.in_group == kGroup - 1;
     if (p.chained && w == WARPS - 1 && !group_end)
-      publish_map<V>(p, q, map_before<V, WARPS, false>(sh, WARPS, lane), c, on, lane);
+      publish_map<V>(p, q, map_before<V, WARPS, false>(sh, WARPS, lane), c, on);
     const Map<V> before = map_before<V, WARPS, false>(sh, w, lane);
     float in[V];
 #pragma unroll
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(128, 4) glr_scan_kernel(GlrArgs p) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
         out[v] = m.first ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], h[v], sh.H[w][lane * V + v]);
-      publish_carry<V>(p, q, out, c, on, lane);
+      publish_carry<V>(p, q, out, c, on);
     }
     if (!STATES_ONLY) {
       IO *out = static_cast<IO *>(p.h) + (int64_t)t0 * p.D + c;
@@ -628,7 +632,7 @@ __global__ void __launch_bounds__(256, 2) glr_gradient_kernel(GlrArgs p) {
                                  : fmaf(sh.A[j][lane * V + v], h[v], state_H[j][lane * V + v]);
     const bool group_end = q.in_group == kGroup - 1;
     if (p.chained && w == 0 && !group_end)
-      publish_map<V>(p, q, map_before<V, WARPS, true>(sh, -1, lane), c, on, lane);
+      publish_map<V>(p, q, map_before<V, WARPS, true>(sh, -1, lane), c, on);
     const Map<V> after = map_before<V, WARPS, true>(sh, w, lane);
     float in[V];
 #pragma unroll
@@ -645,7 +649,7 @@ __global__ void __launch_bounds__(256, 2) glr_gradient_kernel(GlrArgs p) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
         out[v] = m.last ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], qv[v], sh.H[w][lane * V + v]);
-      publish_carry<V>(p, q, out, c, on, lane);
+      publish_carry<V>(p, q, out, c, on);
     }
     float before[TOK][V];  // h_{t-1}
 #pragma unroll
@@ -687,9 +691,9 @@ __global__ void __launch_bounds__(256, 2) glr_gradient_kernel(GlrArgs p) {
   }
 }
 
-// Before the scan kernels: zeroes the ticket and the flags, checks the packed
-// offsets, writes the status word and marks the tiles in which a sequence
-// begins or ends.
+// Before the scan kernels: zeroes the ticket and the chain's words, checks the
+// packed offsets, writes the status word and marks the tiles in which a
+// sequence begins or ends.
 __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words) {
   if (blockIdx.x == 0) {
     bool bad = false;
@@ -700,10 +704,14 @@ __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words
                (i < p.num_seqs && p.cu_seqlens[i + 1] < x);
       }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *p.status = bad ? KDA_DEVICE_BAD_CU_SEQLENS : KDA_DEVICE_OK;
+    if (threadIdx.x == 0) {
+      *p.status = bad ? KDA_DEVICE_BAD_CU_SEQLENS : KDA_DEVICE_OK;
+      *p.ticket = 0;
+    }
   }
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = at; i < words; i += step) p.ticket[i] = 0;
+  for (int64_t i = at; i < words / 2; i += step)  // (an even number, 16-byte aligned)
+    reinterpret_cast<uint4 *>(p.tile_map)[i] = make_uint4(0, 0, 0, 0);
   if (p.cu_seqlens && p.num_seqs > 0)
     for (int64_t tile = at; tile < p.tiles; tile += step) {
       const int64_t t = tile * kTile;
@@ -766,10 +774,10 @@ bool pairs_ok(const GlrArgs &p) {
 }
 
 cudaError_t launch_begin(const GlrArgs &p, cudaStream_t s) {
-  const int64_t words = p.chained ? 1 + (p.tiles + p.groups) * p.stripes : 0;
-  const int64_t most = words > p.tiles ? words : p.tiles, want = (most + 1023) / 1024;
+  const int64_t words = p.chained ? (p.tiles + p.groups) * p.pitch : 0;
+  const int64_t most = words > p.tiles ? words : p.tiles, want = (most + 2047) / 2048, cap = 4 * sm_count();
   TraceScope tr("glr_begin_kernel", s);
-  glr_begin_kernel<<<(unsigned)(want < 1 ? 1 : want > 148 ? 148 : want), 256, 0, s>>>(p, words);
+  glr_begin_kernel<<<(unsigned)(want < 1 ? 1 : want > cap ? cap : want), 256, 0, s>>>(p, words);
   return cudaGetLastError();
 }
 
@@ -787,8 +795,7 @@ template <int V> GlrArgs with_chain(const GlrArgs &a) {
   p.stripes = (p.D + 32 * V - 1) / (32 * V);
   p.chained = p.tiles > 1 && (p.cu_seqlens || p.T > kTile || kTile % p.T != 0);
   p.groups = (p.tiles + kGroup - 1) / kGroup;
-  p.tile_flag = p.ticket + 1;
-  p.carry_flag = p.tile_flag + p.tiles * p.stripes;
+  p.carry = p.tile_map + p.tiles * p.pitch;
   return p;
 }
 

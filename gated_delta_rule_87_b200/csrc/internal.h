@@ -123,12 +123,13 @@ struct GlrArgs {
   bool complement, bf16;
   // workspace
   int32_t *status;
-  int32_t *ticket;  // followed by the flags of the tiles, then of the groups
-  float *tile_map, *carry;
+  int32_t *ticket;
+  uint64_t *tile_map;   // [tiles][pitch], then the groups' words [groups][pitch]
+  int64_t pitch;        // D, rounded up to even
   int32_t *tile_marks;  // packed: whether a sequence begins or ends in the tile
   bool own_chunks;  // backward: chunk_states is workspace, to be filled first
   // set at the launch
-  int32_t *tile_flag, *carry_flag;
+  uint64_t *carry;
   int stripes;
   int64_t groups;
   bool chained;
