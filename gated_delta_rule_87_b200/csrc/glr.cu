@@ -15,57 +15,90 @@
 // A span that holds a sequence start (an end, for the gradient) is "closed":
 // what enters it does not reach what leaves it, whatever its value (an
 // infinity or NaN of one sequence stays in it).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 #include "internal.h"
+#include "tc_common.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kTile = kGlrChunk;  // tokens of a tile; a block's warps share them evenly
+constexpr int kCachedDevices = 64;
+constexpr int kTile = kGlrChunk;  // tokens of a tile
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kTok = kTile / kWarps;
+constexpr int kWide = 64;         // channels of a tile, two a lane
 
-// V adjacent channels of one token, as they are read.
-template <typename IO, int V> struct Raw;
-template <> struct Raw<float, 1> {
-  float r;
-  __device__ __forceinline__ void zero() { r = 0.f; }
-  __device__ __forceinline__ void load(const float *p) { r = __ldg(p); }
-  __device__ __forceinline__ float at(int) const { return r; }
-};
-template <> struct Raw<float, 2> {
-  float2 r;
-  __device__ __forceinline__ void zero() { r = make_float2(0.f, 0.f); }
-  __device__ __forceinline__ void load(const float *p) { r = __ldg(reinterpret_cast<const float2 *>(p)); }
-  __device__ __forceinline__ float at(int v) const { return v ? r.y : r.x; }
-};
-template <> struct Raw<__nv_bfloat16, 1> {
-  uint32_t r;
-  __device__ __forceinline__ void zero() { r = 0; }
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-    r = __ldg(reinterpret_cast<const unsigned short *>(p));
+// The two channels of a lane.  PAIRS: neighbours, rows and pointers aligned for
+// it (and for tensor-map copies); else 32 apart, any alignment.
+template <bool PAIRS> struct Lane {
+  int c;         // the first channel
+  bool on[2];    // which exist
+  __device__ __forceinline__ Lane(int stripe, int D) {
+    const int lane = threadIdx.x & 31;
+    c = stripe * kWide + (PAIRS ? 2 * lane : lane);
+    on[0] = c < D;
+    on[1] = c + step() < D;
   }
-  __device__ __forceinline__ float at(int) const { return bf16_lo(r); }
+  static __device__ __forceinline__ constexpr int step() { return PAIRS ? 1 : 32; }
+  __device__ __forceinline__ bool any() const { return on[0]; }
 };
-template <> struct Raw<__nv_bfloat16, 2> {
+
+// Two channels of one token as they are stored.
+template <typename IO> struct Raw;
+template <> struct Raw<float> {
+  float r[2];
+  __device__ __forceinline__ float at(int v) const { return r[v]; }
+};
+template <> struct Raw<__nv_bfloat16> {
   uint32_t r;
-  __device__ __forceinline__ void zero() { r = 0; }
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-    r = __ldg(reinterpret_cast<const unsigned int *>(p));
-  }
   __device__ __forceinline__ float at(int v) const { return v ? bf16_hi(r) : bf16_lo(r); }
 };
 
-template <typename IO, int V> __device__ __forceinline__ void store_row(IO *p, const float *x) {
-  if constexpr (V == 1) io<IO>::store(p, x[0]);
-  else if constexpr (sizeof(IO) == 4) *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
-  else *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(x[0], x[1]);
-}
-// States are read and written in place by some calls: plain (coherent) accesses.
-template <int V> __device__ __forceinline__ void load_state(const float *p, float *x) {
-  if constexpr (V == 1) {
-    x[0] = *p;
+// Shared memory: a lane's two channels of a row.
+template <bool PAIRS> __device__ __forceinline__ Raw<float> read_row(const float *row, int lane) {
+  Raw<float> x;
+  if constexpr (PAIRS) {
+    const float2 v = reinterpret_cast<const float2 *>(row)[lane];
+    x.r[0] = v.x; x.r[1] = v.y;
   } else {
-    const float2 v = *reinterpret_cast<const float2 *>(p);
+    x.r[0] = row[lane]; x.r[1] = row[lane + 32];
+  }
+  return x;
+}
+template <bool PAIRS> __device__ __forceinline__ Raw<__nv_bfloat16> read_row(const __nv_bfloat16 *row, int lane) {
+  Raw<__nv_bfloat16> x;
+  if constexpr (PAIRS) {
+    x.r = reinterpret_cast<const uint32_t *>(row)[lane];
+  } else {
+    const unsigned short *h = reinterpret_cast<const unsigned short *>(row);
+    x.r = (uint32_t)h[lane] | (uint32_t)h[lane + 32] << 16;
+  }
+  return x;
+}
+
+// Global memory: plain (coherent) accesses, states are updated in place by some calls.
+template <bool PAIRS> __device__ __forceinline__ void load2(const float *p, const Lane<PAIRS> &l, float (&x)[2]) {
+  if constexpr (PAIRS) {
+    const float2 v = *reinterpret_cast<const float2 *>(p + l.c);
     x[0] = v.x; x[1] = v.y;
+  } else {
+    x[0] = p[l.c];
+    x[1] = l.on[1] ? p[l.c + 32] : 0.f;
+  }
+}
+template <bool PAIRS, typename IO> __device__ __forceinline__ void store2(IO *p, const Lane<PAIRS> &l, const float (&x)[2]) {
+  if constexpr (!PAIRS) {
+    io<IO>::store(p + l.c, x[0]);
+    if (l.on[1]) io<IO>::store(p + l.c + 32, x[1]);
+  } else if constexpr (sizeof(IO) == 4) {
+    *reinterpret_cast<float2 *>(p + l.c) = make_float2(x[0], x[1]);
+  } else {
+    *reinterpret_cast<uint32_t *>(p + l.c) = pack_bf16x2(x[0], x[1]);
   }
 }
 
@@ -73,22 +106,44 @@ template <int V> __device__ __forceinline__ void load_state(const float *p, floa
 // (2^-22 of the value) enters the state of a span of at most 16 tokens only,
 // the decay of longer spans comes from the sum of their g.
 template <typename IO> __device__ __forceinline__ float decay(float g) {
-  if constexpr (sizeof(IO) == 2) return __expf(g);
-  else return expf(g);
+  if constexpr (sizeof(IO) == 2) {
+    float a;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(g * 1.44269504f));  // log2 e
+    return a;
+  } else {
+    return expf(g);
+  }
+}
+// 1 - a of one token.  With bf16 activations: near 0 the series of -expm1(g)
+// (its first term left out is below 2^-22 of the value), else the difference,
+// which then loses less than two bits.
+template <typename IO> __device__ __forceinline__ float fresh(float g, float a) {
+  if constexpr (sizeof(IO) == 2) {
+    float s = 1.f / 5040.f;
+    s = fmaf(s, g, 1.f / 720.f);
+    s = fmaf(s, g, 1.f / 120.f);
+    s = fmaf(s, g, 1.f / 24.f);
+    s = fmaf(s, g, 1.f / 6.f);
+    s = fmaf(s, g, 0.5f);
+    s = fmaf(s, g, 1.f);
+    return g > -0.5f ? -g * s : 1.f - a;
+  } else {
+    return -expm1f(g);
+  }
 }
 
-// Which of a warp's TOK tokens begin or end a sequence (bit i: token t0 + i), and,
+// Which of a warp's kTok tokens begin or end a sequence (bit i: token t0 + i), and,
 // in lane i, the sequence of token t0 + i.
 struct Marks {
   uint32_t first, last;
   int seq;
 };
-template <int TOK> __device__ __forceinline__ Marks find_marks(const GlrArgs &p, uint32_t t0, int lane) {
+__device__ __forceinline__ Marks find_marks(const GlrArgs &p, uint32_t t0, int lane) {
   Marks m;
   bool f = false, l = false;
   m.seq = 0;
   const uint32_t t = t0 + lane;
-  if (lane < TOK && t < (uint32_t)p.tokens) {
+  if (lane < kTok && t < (uint32_t)p.tokens) {
     if (p.cu_seqlens) {  // the last sequence that starts at or before t (empty ones start there too)
       int lo = 0, hi = p.num_seqs;
       while (hi - lo > 1) {
@@ -119,38 +174,39 @@ __device__ __forceinline__ int64_t state_row(const GlrArgs &p, int n) {
 }
 
 // The initial state of sequence n.
-template <int V>
-__device__ __forceinline__ void initial_of(const GlrArgs &p, int n, int c, bool on, float (&h0)[V]) {
-#pragma unroll
-  for (int v = 0; v < V; ++v) h0[v] = 0.f;
+template <bool PAIRS>
+__device__ __forceinline__ void initial_of(const GlrArgs &p, int n, const Lane<PAIRS> &l, float (&h0)[2]) {
+  h0[0] = h0[1] = 0.f;
   if (!p.initial_state) return;
   const int64_t r = state_row(p, n);
-  if (on && r >= 0 && GDR_IN_BOUNDS(n < p.num_seqs && r < p.num_slots && c + V <= p.D))
-    load_state<V>(p.initial_state + r * p.D + c, h0);
+  if (l.any() && r >= 0 && GDR_IN_BOUNDS(n < p.num_seqs && r < p.num_slots))
+    load2<PAIRS>(p.initial_state + r * p.D, l, h0);
 }
 
 __device__ __forceinline__ bool bad_offsets(const GlrArgs &p) {
   return p.cu_seqlens && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK;
 }
 
-// Affine map of a span of tokens, for V channels: out = A in + H, or out = H
-// where the span is closed.
-template <int V> struct Map {
-  float A[V], H[V];
-  bool closed;
-  __device__ __forceinline__ void identity() {
-    closed = false;
-#pragma unroll
-    for (int v = 0; v < V; ++v) { A[v] = 1.f; H[v] = 0.f; }
-  }
-  __device__ __forceinline__ float of(float in, int v) const { return closed ? H[v] : fmaf(A[v], in, H[v]); }
+// ---- maps of spans ------------------------------------------------------
+// A span of tokens takes what enters it, `in`, to A in + H, or to H where it is
+// closed.  A >= 0 is kept with its sign turned, a closed span as +1 in its place.
+struct Map {
+  float A, H;
 };
+constexpr float kClosed = 1.f;
+__device__ __forceinline__ float through(float A, float H, float in) { return A > 0.f ? H : fmaf(-A, in, H); }
+__device__ __forceinline__ void then(Map &m, float A, float H) {  // m, then the span (A, H)
+  m.H = through(A, H, m.H);
+  m.A = fmaxf(m.A, A) > 0.f ? kClosed : -(m.A * A);
+}
 
-template <int V, int WARPS> struct TileShared {
-  float G[WARPS][32 * V], A[WARPS][32 * V], H[WARPS][32 * V];     // per warp: sum of g, its exp, H
-  float before_A[WARPS][32 * V], before_H[WARPS][32 * V];         // earlier tiles, a part a warp
-  bool closed[WARPS], before_closed[WARPS];
-  uint32_t ticket;
+struct TileShared {
+  // the warps' maps; a tile's are read until its end, while the next one's are written
+  float A[2][kWarps][kWide], H[2][kWarps][kWide];
+  float before_A[kWarps][kWide], before_H[kWarps][kWide];  // of earlier tiles, a part a warp
+  uint64_t full[kWarps];                                   // a warp's copies have landed
+  uint32_t step;                                           // of the block's next tile
+  int stripe;
 };
 
 // ---- the chain of tiles -------------------------------------------------
@@ -162,178 +218,158 @@ template <int V, int WARPS> struct TileShared {
 // before it; the last tile of a group publishes what leaves the group.  Which
 // values are joined, and in which order, depends on the sizes alone, never on
 // timing.
-constexpr int kGroup = 16;
+//
+// A channel's map goes through the workspace as one 64-bit word (A above, H
+// below), which is its own flag: 0 is not there yet, and A is never +0.  So a
+// hand-over is one store and one polling load, without a fence.
+constexpr int kGroup = 16, kPart = kGroup / kWarps;
 static_assert(kGroup >= kGlrShortestGroup, "the workspace counts groups of at least this length");
 constexpr uint32_t kMaxChainPolls = 1u << 20;  // about a second
 
-// A channel's map goes through the workspace as one 64-bit word, which is its
-// own flag (no fence): H below, above it A with the sign bit set (A >= 0), or a
-// code for a closed span.  0: not there yet.
-constexpr uint32_t kClosedCode = 0xffbfffffu, kNanCode = 0xffffffffu;
-__device__ __forceinline__ uint64_t pack_map(float A, float H, bool closed) {
-  const uint32_t a = closed ? kClosedCode : A == A ? __float_as_uint(A) | 0x80000000u : kNanCode;
-  return (uint64_t)a << 32 | __float_as_uint(H);
+template <bool PAIRS> __device__ __forceinline__ void load_words(const uint64_t *p, const Lane<PAIRS> &l, uint64_t (&u)[2]) {
+  if constexpr (PAIRS) {
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(u[0]), "=l"(u[1]) : "l"(p + l.c) : "memory");
+  } else {
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(u[0]) : "l"(p + l.c) : "memory");
+    if (l.on[1]) asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(u[1]) : "l"(p + l.c + 32) : "memory");
+  }
 }
-__device__ __forceinline__ bool word_closed(uint64_t u) { return (uint32_t)(u >> 32) == kClosedCode; }
-__device__ __forceinline__ float word_A(uint64_t u) { return __uint_as_float((uint32_t)(u >> 32) & 0x7fffffffu); }
+template <bool PAIRS>
+__device__ __forceinline__ void store_words(uint64_t *p, const Lane<PAIRS> &l, const Map (&m)[2]) {
+  uint64_t u[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) u[v] = (uint64_t)__float_as_uint(m[v].A) << 32 | __float_as_uint(m[v].H);
+  if constexpr (PAIRS) {
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p + l.c), "l"(u[0]), "l"(u[1]) : "memory");
+  } else {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p + l.c), "l"(u[0]) : "memory");
+    if (l.on[1]) asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p + l.c + 32), "l"(u[1]) : "memory");
+  }
+}
+__device__ __forceinline__ float word_A(uint64_t u) { return __uint_as_float((uint32_t)(u >> 32)); }
 __device__ __forceinline__ float word_H(uint64_t u) { return __uint_as_float((uint32_t)u); }
 
-template <int V> __device__ __forceinline__ void load_words(const uint64_t *p, uint64_t (&u)[V]) {
-  if constexpr (V == 2)
-    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(u[0]), "=l"(u[1]) : "l"(p) : "memory");
-  else
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(u[0]) : "l"(p) : "memory");
-}
-template <int V> __device__ __forceinline__ void store_words(uint64_t *p, const uint64_t (&u)[V]) {
-  if constexpr (V == 2)
-    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(u[0]), "l"(u[1]) : "memory");
-  else
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(u[0]) : "memory");
-}
-
-// The place of a ticket's tile in the chain (REV: from the last tile on).
+// A tile's place in the chain (REV: from the last tile on).
 struct Place {
-  uint32_t tile, step;  // its number on the token axis, and in the chain
-  int stripe, in_group;
-  uint32_t group;
+  uint32_t step, tile;
+  int stripe;
+  __device__ __forceinline__ int in_group() const { return step % kGroup; }
+  __device__ __forceinline__ uint32_t group() const { return step / kGroup; }
 };
-template <bool REV> __device__ __forceinline__ Place place_of(const GlrArgs &p, uint32_t ticket) {
+
+// Takes the block's next tile (one thread).  Without a chain: `grid` tiles on.
+__device__ __forceinline__ uint32_t next_ticket(const GlrArgs &p, TileShared &sh, uint32_t last) {
+  const uint32_t t = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : last + gridDim.x;
+  sh.step = t / (uint32_t)p.stripes;
+  sh.stripe = (int)(t - sh.step * (uint32_t)p.stripes);
+  return t;
+}
+template <bool REV> __device__ __forceinline__ Place taken(const GlrArgs &p, const TileShared &sh) {
   Place q;
-  q.step = ticket / (uint32_t)p.stripes;
-  q.stripe = (int)(ticket - q.step * (uint32_t)p.stripes);
+  q.step = sh.step;
+  q.stripe = sh.stripe;
   q.tile = REV ? (uint32_t)p.tiles - 1 - q.step : q.step;
-  q.group = q.step / kGroup;
-  q.in_group = (int)(q.step % kGroup);
   return q;
 }
 
-// Publishes a tile's map, or what leaves its group (one warp, the tile's 32 V channels).
-template <int V>
-__device__ __forceinline__ void publish_map(const GlrArgs &p, const Place &q, const Map<V> &m, int c, bool on) {
-  if (on && GDR_IN_BOUNDS(q.step < p.tiles && c + V <= p.D)) {
-    uint64_t u[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) u[v] = pack_map(m.A[v], m.H[v], m.closed);
-    store_words<V>(p.tile_map + (int64_t)q.step * p.pitch + c, u);
-  }
-}
-template <int V>
-__device__ __forceinline__ void publish_carry(const GlrArgs &p, const Place &q, const float (&h)[V], int c, bool on) {
-  if (on && GDR_IN_BOUNDS(q.group < p.groups && c + V <= p.D)) {
-    uint64_t u[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) u[v] = pack_map(0.f, h[v], true);
-    store_words<V>(p.carry + (int64_t)q.group * p.pitch + c, u);
-  }
-}
-
 // What enters the tile.  Each warp joins its part of the group's earlier maps
-// (the first warp's part starts from what enters the group, a closed word), then
-// all join the parts.  Every thread of the block takes part.  False: a wait gave up.
-template <int V, int WARPS>
-__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared<V, WARPS> &sh, const Place &q,
-                                           int c, bool on, int w, int lane, float (&h)[V]) {
-  constexpr int PER = kGroup / WARPS;  // maps a warp joins
-  const int j0 = w * PER;
-  const int n = on ? min(PER, q.in_group - j0) : 0;  // <= 0: none
-  const bool start = on && w == 0 && q.group > 0;
-  const uint64_t *maps = p.tile_map + (int64_t)(q.group * kGroup + j0) * p.pitch + c;
-  const uint64_t *carry = p.carry + (int64_t)(q.group - 1) * p.pitch + c;
-  uint64_t t[PER][V], s[V];
+// (the first warp's part starts from what enters the group), then all join the
+// parts.  Every thread of the block takes part.  False: a wait gave up.
+template <bool PAIRS>
+__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, const Place &q, const Lane<PAIRS> &l,
+                                           int w, int lane, float (&in)[2]) {
+  const int at = q.in_group(), j0 = w * kPart;
+  const int n = l.any() && GDR_IN_BOUNDS(q.step < p.tiles) ? at - j0 : 0;  // maps to join (at most kPart)
+  const bool start = l.any() && w == 0 && q.step >= kGroup;
+  const uint64_t *maps = p.tile_map + (int64_t)(q.step - at + j0) * p.pitch;
+  const uint64_t *carry = p.carry + ((int64_t)q.group() - 1) * p.pitch;
+  uint64_t t[kPart][2], s[2] = {0, 0};
 #pragma unroll
-  for (int v = 0; v < V; ++v) s[v] = 0;
-#pragma unroll
-  for (int j = 0; j < PER; ++j)
-#pragma unroll
-    for (int v = 0; v < V; ++v) t[j][v] = 0;
+  for (int j = 0; j < kPart; ++j) t[j][0] = t[j][1] = 0;
   bool ok = false;
-  for (uint32_t poll = 0; poll < kMaxChainPolls; ++poll) {
-    // loads what is missing; a lane's channels come and go together or not
-    bool have = true;
-    if (start && (s[0] == 0 || s[V - 1] == 0) && GDR_IN_BOUNDS(q.group <= p.groups && c + V <= p.D)) load_words<V>(carry, s);
+  for (uint32_t poll = 0;; ++poll) {
+    bool have = true;  // loads what is missing
+    if (start && (s[0] == 0 || (l.on[1] && s[1] == 0))) load_words<PAIRS>(carry, l, s);
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (j < n && (t[j][0] == 0 || t[j][V - 1] == 0) && GDR_IN_BOUNDS(q.step < p.tiles && c + V <= p.D))
-        load_words<V>(maps + (int64_t)j * p.pitch, t[j]);
-    if (start) have = s[0] != 0 && s[V - 1] != 0;
+    for (int j = 0; j < kPart; ++j)
+      if (j < n && (t[j][0] == 0 || (l.on[1] && t[j][1] == 0))) load_words<PAIRS>(maps + (int64_t)j * p.pitch, l, t[j]);
+    if (start) have = s[0] != 0 && (!l.on[1] || s[1] != 0);
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (j < n) have = have && t[j][0] != 0 && t[j][V - 1] != 0;
+    for (int j = 0; j < kPart; ++j)
+      if (j < n) have = have && t[j][0] != 0 && (!l.on[1] || t[j][1] != 0);
     ok = __all_sync(0xffffffffu, have);
     if (ok) break;
     if ((poll & 1023) == 1023 && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK) break;
-    if (poll == kMaxChainPolls - 1) *p.status = KDA_DEVICE_TIMEOUT;
-  }
-  Map<V> m;
-  m.identity();
-#pragma unroll
-  for (int v = 0; v < V; ++v) m.H[v] = word_H(s[v]);
-#pragma unroll
-  for (int j = 0; j < PER; ++j)
-    if (j < n) {
-      const bool shut = word_closed(t[j][0]);
-      m.closed |= shut;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        m.H[v] = shut ? word_H(t[j][v]) : fmaf(word_A(t[j][v]), m.H[v], word_H(t[j][v]));
-        m.A[v] *= word_A(t[j][v]);
-      }
+    if (poll == kMaxChainPolls) {
+      *p.status = KDA_DEVICE_TIMEOUT;
+      break;
     }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sh.before_A[w][lane * V + v] = m.A[v];
-    sh.before_H[w][lane * V + v] = m.H[v];
   }
-  if (lane == 0) sh.before_closed[w] = m.closed;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    Map m{-1.f, word_H(s[v])};
+#pragma unroll
+    for (int j = 0; j < kPart; ++j)
+      if (j < n) then(m, word_A(t[j][v]), word_H(t[j][v]));
+    sh.before_A[w][2 * lane + v] = m.A;
+    sh.before_H[w][2 * lane + v] = m.H;
+  }
   if (__syncthreads_or(!ok)) return false;
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = sh.before_H[0][lane * V + v];
+  for (int v = 0; v < 2; ++v) in[v] = sh.before_H[0][2 * lane + v];
 #pragma unroll
-  for (int k = 1; k < WARPS; ++k)
-    if (k * PER < q.in_group) {
+  for (int k = 1; k < kWarps; ++k)
+    if (k * kPart < at)
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        h[v] = sh.before_closed[k] ? sh.before_H[k][lane * V + v]
-                                   : fmaf(sh.before_A[k][lane * V + v], h[v], sh.before_H[k][lane * V + v]);
-    }
+      for (int v = 0; v < 2; ++v) in[v] = through(sh.before_A[k][2 * lane + v], sh.before_H[k][2 * lane + v], in[v]);
   return true;
 }
 
-// The map of the tile's tokens before warp w's (after them, for REV) from what
-// the warps have shared.  Its decay is exp of the whole sum.
-template <int V, int WARPS, bool REV>
-__device__ __forceinline__ Map<V> map_before(const TileShared<V, WARPS> &sh, int w, int lane) {
-  Map<V> m;
-  m.identity();
-  float gs[V];
+// After the warps have shared their maps: the last one in the chain's direction
+// publishes the tile's, unless the tile ends its group.
+template <bool PAIRS, bool REV>
+__device__ __forceinline__ void publish_tile(const GlrArgs &p, const TileShared &sh, int buf, const Place &q,
+                                             const Lane<PAIRS> &l, int lane) {
+  Map m[2];
 #pragma unroll
-  for (int v = 0; v < V; ++v) gs[v] = 0.f;
+  for (int v = 0; v < 2; ++v) {
+    m[v] = Map{-1.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < WARPS; ++k) {
-    const int j = REV ? WARPS - 1 - k : k;
-    if (REV ? j > w : j < w) {
-      m.closed |= sh.closed[j];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gs[v] += sh.G[j][lane * V + v];
-        m.H[v] = sh.closed[j] ? sh.H[j][lane * V + v]
-                              : fmaf(sh.A[j][lane * V + v], m.H[v], sh.H[j][lane * V + v]);
-      }
+    for (int k = 0; k < kWarps; ++k) {
+      const int j = REV ? kWarps - 1 - k : k;
+      then(m[v], sh.A[buf][j][2 * lane + v], sh.H[buf][j][2 * lane + v]);
     }
   }
+  if (l.any() && GDR_IN_BOUNDS(q.step < p.tiles)) store_words<PAIRS>(p.tile_map + (int64_t)q.step * p.pitch, l, m);
+}
+// `x`, what enters the tile, becomes what enters warp w, and at the end of a
+// group what leaves the tile is published (by the last warp).
+template <bool PAIRS, bool REV>
+__device__ __forceinline__ void enter_warp(const GlrArgs &p, const TileShared &sh, int buf, const Place &q,
+                                           const Lane<PAIRS> &l, int w, int lane, float (&x)[2]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) m.A[v] = expf(gs[v]);
-  return m;
+  for (int k = 0; k < kWarps - 1; ++k) {
+    const int j = REV ? kWarps - 1 - k : k;
+    if (REV ? j > w : j < w)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) x[v] = through(sh.A[buf][j][2 * lane + v], sh.H[buf][j][2 * lane + v], x[v]);
+  }
+  if (p.chained && w == (REV ? 0 : kWarps - 1) && q.in_group() == kGroup - 1) {
+    Map m[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      m[v] = Map{kClosed, through(sh.A[buf][w][2 * lane + v], sh.H[buf][w][2 * lane + v], x[v])};
+    if (l.any() && GDR_IN_BOUNDS(q.group() < p.groups)) store_words<PAIRS>(p.carry + (int64_t)q.group() * p.pitch, l, m);
+  }
 }
 
 // Sequences without tokens, by the blocks of the first tile: what leaves them
 // is what enters them.
-template <int WARPS>
 __device__ __forceinline__ void pass_empty(const GlrArgs &p, const float *src, float *dst, bool pooled,
                                            int c0, int width) {
   if (!dst || !p.cu_seqlens) return;
   const int lane = threadIdx.x & 31;
-  for (int n0 = (threadIdx.x >> 5) * 32; n0 < p.num_seqs; n0 += WARPS * 32) {
+  for (int n0 = (threadIdx.x >> 5) * 32; n0 < p.num_seqs; n0 += kThreads) {
     const int n = n0 + lane;
     const bool empty = n < p.num_seqs && __ldg(p.cu_seqlens + n) == __ldg(p.cu_seqlens + n + 1);
     uint32_t todo = __ballot_sync(0xffffffffu, empty);
@@ -356,338 +392,348 @@ __device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
   return r == 0 || r + kTile >= (uint32_t)p.T;
 }
 
-// ---- forward ------------------------------------------------------------
-template <typename IO, int V, int TOK> struct Tokens {
-  Raw<IO, V> x[TOK];
-  Raw<float, V> g[TOK];
-  bool marked;
-  __device__ __forceinline__ void load(const GlrArgs &p, uint32_t tile, uint32_t t0, int c, bool on) {
-    const IO *x0 = static_cast<const IO *>(p.x) + (int64_t)t0 * p.ld_x + c;
-    const float *g0 = p.g + (int64_t)t0 * p.ld_g + c;
-    const int n = on ? (int)min((int64_t)TOK, p.tokens - t0) : 0;
-#pragma unroll
-    for (int i = 0; i < TOK; ++i) {
-      x[i].zero();
-      g[i].zero();
-      if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) {
-        x[i].load(x0 + i * p.ld_x);
-        g[i].load(g0 + i * p.ld_g);
-      }
-    }
-    marked = has_marks(p, tile);
-  }
+// ---- the kernels --------------------------------------------------------
+// Persistent blocks of four warps, 16 tokens and 64 channels a warp.  Each warp
+// copies its own rows to shared memory (a tensor-map copy a tensor, or lane by
+// lane where rows are not aligned) and waits for them alone.
+template <typename IO> struct WarpRows {
+  float g[kTok][kWide];
+  IO x[kTok][kWide];
+};
+template <typename IO> struct WarpRowsBwd : WarpRows<IO> {
+  IO dh[kTok][kWide];
+};
+struct GlrMaps {
+  CUtensorMap x, g, dh;
 };
 
-// Persistent blocks: the loads of a block's next tile are under way while this
-// one waits for what enters it and is written.  x and g are read once; the
-// tokens' a stays in registers in between.  STATES_ONLY: only the saved chunk
-// states are written.
-template <typename IO, int V, bool COMPLEMENT, bool STATES_ONLY>
-__global__ void __launch_bounds__(128, 4) glr_scan_kernel(GlrArgs p) {
-  constexpr int WARPS = 4, TOK = kTile / WARPS;
-  __shared__ TileShared<V, WARPS> sh;
+// Tokens of a warp that exist.
+__device__ __forceinline__ int tokens_of(const GlrArgs &p, uint32_t t0) {
+  const int64_t left = p.tokens - (int64_t)t0;
+  return left <= 0 ? 0 : left < kTok ? (int)left : kTok;
+}
+
+// Lane copies of one tensor's rows; zeros where nothing is.
+template <typename IO>
+__device__ __forceinline__ void copy_rows(const GlrArgs &p, IO (&to)[kTok][kWide], const void *from, int64_t ld,
+                                          uint32_t t0, const Lane<false> &l, int lane) {
+  const IO *src = static_cast<const IO *>(from);
+  const int n = tokens_of(p, t0);
+  int64_t off = (int64_t)t0 * ld + l.c;
+  if constexpr (sizeof(IO) == 4) {
+#pragma unroll
+    for (int i = 0; i < kTok; ++i, off += ld)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const bool ok = i < n && l.on[v] && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens && l.c + 32 * v < p.D);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&to[i][lane + 32 * v])),
+                     "l"(ok ? src + off + 32 * v : src), "r"(ok ? 4 : 0) : "memory");
+      }
+  } else {  // a single bf16 is too short for an asynchronous copy
+    IO t[kTok][2];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i, off += ld)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const bool ok = i < n && l.on[v] && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens && l.c + 32 * v < p.D);
+        t[i][v] = ok ? __ldg(src + off + 32 * v) : __float2bfloat16_rn(0.f);
+      }
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) to[i][lane + 32 * v] = t[i][v];
+  }
+}
+
+// Begins the copies of a warp's rows of a tile.
+template <typename IO, bool PAIRS, bool BWD, typename ROWS>
+__device__ __forceinline__ void begin_copies(const GlrArgs &p, const GlrMaps &maps, ROWS &rows, uint64_t *full,
+                                             const Place &q, int w, int lane) {
+  const uint32_t t0 = q.tile * kTile + w * kTok;
+  if constexpr (PAIRS) {
+    __syncwarp();  // the rows have been read by every lane
+    if (lane == 0) {
+      const int c0 = q.stripe * kWide;
+      tc::mbar_arrive_expect_tx(full, sizeof(ROWS));
+      tc::tma_load_2d(rows.g, &maps.g, c0, (int)t0, full);
+      tc::tma_load_2d(rows.x, &maps.x, c0, (int)t0, full);
+      if constexpr (BWD) tc::tma_load_2d(rows.dh, &maps.dh, c0, (int)t0, full);
+    }
+  } else {
+    const Lane<false> l(q.stripe, p.D);
+    copy_rows<float>(p, rows.g, p.g, p.ld_g, t0, l, lane);
+    copy_rows<IO>(p, rows.x, p.x, p.ld_x, t0, l, lane);
+    if constexpr (BWD) copy_rows<IO>(p, rows.dh, p.dh, p.ld_dh, t0, l, lane);
+  }
+}
+template <bool PAIRS>
+__device__ __forceinline__ bool copies_done(const GlrArgs &p, uint64_t *full, uint32_t parity) {
+  if constexpr (PAIRS) return tc::mbar_wait_warp(full, parity, p.status, KDA_DEVICE_TIMEOUT);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  return true;
+}
+__device__ __forceinline__ void init_barriers(TileShared &sh) {
+  if (threadIdx.x < kWarps) tc::mbar_init(&sh.full[threadIdx.x], 1);
+  tc::mbar_fence_init();
+}
+
+// Forward.  A tile's decays and inputs go to registers in the first pass over
+// it, so the next tile's copies run while this one waits for what enters it and
+// is written.  STATES_ONLY: only the saved chunk states are written.
+template <typename IO, bool PAIRS, bool COMPLEMENT, bool STATES_ONLY>
+__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 && !COMPLEMENT ? 5 : 4)
+glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
+  __shared__ TileShared sh;
+  extern __shared__ __align__(128) unsigned char tile_bytes[];
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const uint32_t total = (uint32_t)(p.tiles * p.stripes);
-  if (threadIdx.x == 0) sh.ticket = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : blockIdx.x;
+  auto &rows = reinterpret_cast<WarpRows<IO> *>(tile_bytes)[w];
+  uint32_t ticket = 0, parity = 0;
+  init_barriers(sh);
+  if (threadIdx.x == 0) ticket = next_ticket(p, sh, blockIdx.x - gridDim.x);
   __syncthreads();
-  uint32_t ticket = sh.ticket;
+  Place q = taken<false>(p, sh);
+  if (q.step >= p.tiles) return;
   __syncthreads();
-  if (ticket >= total) return;
-  Place q = place_of<false>(p, ticket);
-  Tokens<IO, V, TOK> k;
-  {
-    const int c = (q.stripe * 32 + lane) * V;
-    k.load(p, q.tile, q.tile * kTile + w * TOK, c, c < p.D);
-  }
+  begin_copies<IO, PAIRS, false>(p, maps, rows, &sh.full[w], q, w, lane);
+  bool marked = has_marks(p, q.tile);
   while (true) {
-    if (threadIdx.x == 0) sh.ticket = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : ticket + gridDim.x;
-    const uint32_t t0 = q.tile * kTile + w * TOK;
-    const int c = (q.stripe * 32 + lane) * V;
-    const bool on = c < p.D;
+    if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
+    const Lane<PAIRS> l(q.stripe, p.D);
+    const uint32_t t0 = q.tile * kTile + w * kTok;
     Marks m;
     m.first = m.last = 0;
     m.seq = 0;
-    if (k.marked) m = find_marks<TOK>(p, t0, lane);
-    // the span from zeros; b of a token is x, or (1 - a) x
-    float a[TOK][V], b[COMPLEMENT ? TOK : 1][V], gs[V], h[V];
-    Raw<IO, V> x[TOK];
+    if (marked) m = find_marks(p, t0, lane);
+    const bool landed = copies_done<PAIRS>(p, &sh.full[w], parity);
+    parity ^= 1;
+    // the span's map; b of a token is x, or (1 - a) x
+    float a[kTok][2], b[COMPLEMENT ? kTok : 1][2], gs[2] = {0.f, 0.f}, h[2] = {0.f, 0.f};
+    Raw<IO> x[COMPLEMENT ? 1 : kTok];
+    auto b_of = [&](int i, int v) { return COMPLEMENT ? b[COMPLEMENT ? i : 0][v] : x[COMPLEMENT ? 0 : i].at(v); };
 #pragma unroll
-    for (int v = 0; v < V; ++v) gs[v] = h[v] = 0.f;
+    for (int i = 0; i < kTok; ++i) {
+      const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+      const Raw<IO> xi = read_row<PAIRS>(rows.x[i], lane);
+      if (!COMPLEMENT) x[COMPLEMENT ? 0 : i] = xi;
 #pragma unroll
-    for (int i = 0; i < TOK; ++i) {
-      x[i] = k.x[i];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float g = k.g[i].at(v);
-        a[i][v] = decay<IO>(g);
-        if (COMPLEMENT) b[i][v] = -expm1f(g) * x[i].at(v);
-        gs[v] += g;
+      for (int v = 0; v < 2; ++v) {
+        a[i][v] = decay<IO>(g.at(v));
+        if (COMPLEMENT) b[COMPLEMENT ? i : 0][v] = fresh<IO>(g.at(v), a[i][v]) * xi.at(v);
+        gs[v] += g.at(v);
       }
     }
-    auto b_of = [&](int i, int v) { return COMPLEMENT ? b[COMPLEMENT ? i : 0][v] : x[i].at(v); };
     if (m.first == 0) {
 #pragma unroll
-      for (int i = 0; i < TOK; ++i)
+      for (int i = 0; i < kTok; ++i)
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+        for (int v = 0; v < 2; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
     } else {
 #pragma unroll
-      for (int i = 0; i < TOK; ++i) {
+      for (int i = 0; i < kTok; ++i) {
         if (m.first >> i & 1) {
-          // a start's state takes the place of its a: the initial state is read
+          // A start's state takes the place of its a: the initial state is read
           // once, before the map is published (the sequence's last tile may
-          // write the final state over it as soon as that is done)
-          float h0[V];
-          initial_of<V>(p, __shfl_sync(0xffffffffu, m.seq, i), c, on, h0);
+          // write the final state over it as soon as that is done).
+          float h0[2];
+          initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, h0);
 #pragma unroll
-          for (int v = 0; v < V; ++v) h[v] = a[i][v] = fmaf(a[i][v], h0[v], b_of(i, v));
+          for (int v = 0; v < 2; ++v) h[v] = a[i][v] = fmaf(a[i][v], h0[v], b_of(i, v));
         } else {
 #pragma unroll
-          for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+          for (int v = 0; v < 2; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
         }
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      sh.G[w][lane * V + v] = gs[v];
-      sh.A[w][lane * V + v] = expf(gs[v]);
-      sh.H[w][lane * V + v] = h[v];
+    for (int v = 0; v < 2; ++v) {
+      sh.A[parity][w][2 * lane + v] = m.first ? kClosed : -expf(gs[v]);
+      sh.H[parity][w][2 * lane + v] = h[v];
     }
-    if (lane == 0) sh.closed[w] = m.first != 0;
-    __syncthreads();
-    // the next tile's loads
-    const uint32_t next = sh.ticket;
-    const Place nq = place_of<false>(p, next < total ? next : 0);
-    {
-      const int nc = (nq.stripe * 32 + lane) * V;
-      k.load(p, nq.tile, nq.tile * kTile + w * TOK, nc, next < total && nc < p.D);
+    if (__syncthreads_or(!landed)) return;
+    if (p.chained && w == kWarps - 1 && q.in_group() != kGroup - 1) publish_tile<PAIRS, false>(p, sh, parity, q, l, lane);
+    const Place nq = taken<false>(p, sh);
+    const bool more = nq.step < p.tiles;
+    if (more) {
+      begin_copies<IO, PAIRS, false>(p, maps, rows, &sh.full[w], nq, w, lane);
+      marked = has_marks(p, nq.tile);
     }
-    const bool group_end = q.in_group == kGroup - 1;
-    if (p.chained && w == WARPS - 1 && !group_end)
-      publish_map<V>(p, q, map_before<V, WARPS, false>(sh, WARPS, lane), c, on);
-    const Map<V> before = map_before<V, WARPS, false>(sh, w, lane);
-    float in[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) in[v] = 0.f;
+    float in[2] = {0.f, 0.f};
     if (p.chained) {
-      if (!enter_tile<V, WARPS>(p, sh, q, c, on, w, lane, in)) return;
+      if (!enter_tile<PAIRS>(p, sh, q, l, w, lane, in)) {
+        if (more) copies_done<PAIRS>(p, &sh.full[w], parity);
+        return;
+      }
     } else {
-      __syncthreads();  // the maps are read before the next tile's are written
+      __syncthreads();  // the next ticket is read before it is replaced
     }
-    if (w == 0 && on && p.chunk_states && GDR_IN_BOUNDS(q.tile < p.tiles && c + V <= p.D))
-      store_row<float, V>(p.chunk_states + (int64_t)q.tile * p.D + c, in);
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = before.of(in[v], v);
-    if (p.chained && w == WARPS - 1 && group_end) {
-      float out[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        out[v] = m.first ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], h[v], sh.H[w][lane * V + v]);
-      publish_carry<V>(p, q, out, c, on);
-    }
+    if (w == 0 && l.any() && p.chunk_states && GDR_IN_BOUNDS(q.tile < p.tiles))
+      store2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, in);
+    h[0] = in[0]; h[1] = in[1];
+    enter_warp<PAIRS, false>(p, sh, parity, q, l, w, lane, h);
     if (!STATES_ONLY) {
-      IO *out = static_cast<IO *>(p.h) + (int64_t)t0 * p.D + c;
-      const int n = on ? (int)min((int64_t)TOK, p.tokens - t0) : 0;
+      IO *out = static_cast<IO *>(p.h) + (int64_t)t0 * p.D;
+      const int n = l.any() ? tokens_of(p, t0) : 0;
       if ((m.first | m.last) == 0) {
 #pragma unroll
-        for (int i = 0; i < TOK; ++i) {
+        for (int i = 0; i < kTok; ++i) {
 #pragma unroll
-          for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
-          if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) store_row<IO, V>(out + (int64_t)i * p.D, h);
+          for (int v = 0; v < 2; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+          if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) store2<PAIRS>(out + (int64_t)i * p.D, l, h);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < TOK; ++i) {
+        for (int i = 0; i < kTok; ++i) {
           const int s = __shfl_sync(0xffffffffu, m.seq, i);
 #pragma unroll
-          for (int v = 0; v < V; ++v) h[v] = m.first >> i & 1 ? a[i][v] : fmaf(a[i][v], h[v], b_of(i, v));
-          if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) store_row<IO, V>(out + (int64_t)i * p.D, h);
+          for (int v = 0; v < 2; ++v) h[v] = m.first >> i & 1 ? a[i][v] : fmaf(a[i][v], h[v], b_of(i, v));
+          if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) store2<PAIRS>(out + (int64_t)i * p.D, l, h);
           if ((m.last >> i & 1) && p.final_state) {
             const int64_t r = state_row(p, s);
-            if (on && r >= 0 && GDR_IN_BOUNDS(s < p.num_seqs && r < p.num_slots && c + V <= p.D))
-              store_row<float, V>(p.final_state + r * p.D + c, h);
+            if (l.any() && r >= 0 && GDR_IN_BOUNDS(s < p.num_seqs && r < p.num_slots))
+              store2<PAIRS>(p.final_state + r * p.D, l, h);
           }
         }
       }
-      if (q.tile == 0) pass_empty<WARPS>(p, p.initial_state, p.final_state, true, q.stripe * 32 * V, 32 * V);
+      if (q.tile == 0) pass_empty(p, p.initial_state, p.final_state, true, q.stripe * kWide, kWide);
     }
-    if (next >= total) return;
-    ticket = next;
+    if (!more) return;
     q = nq;
   }
 }
 
-// ---- backward -----------------------------------------------------------
-// The states again from what enters the tile (saved), the gradients from what
-// enters it from the tokens after it (chained): x, g and dh are read once.
-template <typename IO, int V, bool COMPLEMENT>
-__global__ void __launch_bounds__(256, 2) glr_gradient_kernel(GlrArgs p) {
-  constexpr int WARPS = 8, TOK = kTile / WARPS;
-  __shared__ TileShared<V, WARPS> sh;
-  __shared__ float state_H[WARPS][32 * V];
-  __shared__ bool state_closed[WARPS];
+// Backward: the states again from what enters the tile (saved), the gradients
+// from what enters it from the tokens after it (chained).  The rows stay in
+// shared memory until the second pass has read them; more blocks an SM take
+// the place of the early copies.
+template <typename IO, bool PAIRS, bool COMPLEMENT>
+__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 4)
+glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
+  __shared__ TileShared sh;
+  __shared__ float state_A[kWarps][kWide], state_H[kWarps][kWide];
+  extern __shared__ __align__(128) unsigned char tile_bytes[];
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const uint32_t total = (uint32_t)(p.tiles * p.stripes);
-  if (threadIdx.x == 0) sh.ticket = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : blockIdx.x;
+  auto &rows = reinterpret_cast<WarpRowsBwd<IO> *>(tile_bytes)[w];
+  uint32_t ticket = 0, parity = 0;
+  init_barriers(sh);
+  if (threadIdx.x == 0) ticket = next_ticket(p, sh, blockIdx.x - gridDim.x);
   __syncthreads();
-  uint32_t ticket = sh.ticket;
+  Place q = taken<true>(p, sh);
+  if (q.step >= p.tiles) return;
   __syncthreads();
-  if (ticket >= total) return;
-  Place q = place_of<true>(p, ticket);
-  Tokens<IO, V, TOK> k;
-  Raw<IO, V> kd[TOK];
-  float kh[V];
-  auto load = [&](const Place &at, bool live) {
-    const uint32_t t0 = at.tile * kTile + w * TOK;
-    const int c = (at.stripe * 32 + lane) * V;
-    const bool on = live && c < p.D;
-    k.load(p, at.tile, t0, c, on);
-    const IO *d0 = static_cast<const IO *>(p.dh) + (int64_t)t0 * p.ld_dh + c;
-    const int n = on ? (int)min((int64_t)TOK, p.tokens - t0) : 0;
-#pragma unroll
-    for (int i = 0; i < TOK; ++i) {
-      kd[i].zero();
-      if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) kd[i].load(d0 + i * p.ld_dh);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) kh[v] = 0.f;
-    if (on && GDR_IN_BOUNDS(at.tile < p.tiles && c + V <= p.D))
-      load_state<V>(p.chunk_states + (int64_t)at.tile * p.D + c, kh);
-  };
-  load(q, true);
+  begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], q, w, lane);
   while (true) {
-    if (threadIdx.x == 0) sh.ticket = p.chained ? (uint32_t)atomicAdd(p.ticket, 1) : ticket + gridDim.x;
-    const uint32_t t0 = q.tile * kTile + w * TOK;
-    const int c = (q.stripe * 32 + lane) * V;
-    const bool on = c < p.D;
+    if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
+    const Lane<PAIRS> l(q.stripe, p.D);
+    const uint32_t t0 = q.tile * kTile + w * kTok;
+    float h[2] = {0.f, 0.f}, s[2] = {0.f, 0.f}, r[2] = {0.f, 0.f}, gs[2] = {0.f, 0.f};
+    if (l.any() && GDR_IN_BOUNDS(q.tile < p.tiles)) load2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, h);
     Marks m;
     m.first = m.last = 0;
     m.seq = 0;
-    if (k.marked) m = find_marks<TOK>(p, t0, lane);
-    float a[TOK][V], u[COMPLEMENT ? TOK : 1][V], x[TOK][V], d[TOK][V], gs[V], s[V], qv[V], h[V];
+    if (has_marks(p, q.tile)) m = find_marks(p, t0, lane);
+    const bool landed = copies_done<PAIRS>(p, &sh.full[w], parity);
+    parity ^= 1;
+    float a[kTok][2];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      gs[v] = s[v] = qv[v] = 0.f;
-      h[v] = kh[v];
-    }
+    for (int i = 0; i < kTok; ++i) {
+      const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
 #pragma unroll
-    for (int i = 0; i < TOK; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float g = k.g[i].at(v);
-        a[i][v] = decay<IO>(g);
-        if (COMPLEMENT) u[i][v] = -expm1f(g);
-        x[i][v] = k.x[i].at(v);
-        d[i][v] = kd[i].at(v);
-        gs[v] += g;
+      for (int v = 0; v < 2; ++v) {
+        a[i][v] = decay<IO>(g.at(v));
+        gs[v] += g.at(v);
       }
-    auto b_of = [&](int i, int v) { return COMPLEMENT ? u[COMPLEMENT ? i : 0][v] * x[i][v] : x[i][v]; };
+    }
+    // the state y after token i; the gradient that a sequence's end brings
+    auto advance = [&](int i, float (&y)[2]) {
+      const Raw<IO> x = read_row<PAIRS>(rows.x[i], lane);
+      Raw<float> g;
+      if (COMPLEMENT) g = read_row<PAIRS>(rows.g[i], lane);
 #pragma unroll
-    for (int i = 0; i < TOK; ++i) {
-      if (m.first >> i & 1) initial_of<V>(p, __shfl_sync(0xffffffffu, m.seq, i), c, on, s);
+      for (int v = 0; v < 2; ++v)
+        y[v] = fmaf(a[i][v], y[v], COMPLEMENT ? fresh<IO>(g.at(v), a[i][v]) * x.at(v) : x.at(v));
+    };
+    auto end_gradient = [&](int i, float (&y)[2]) {
+      const int sq = __shfl_sync(0xffffffffu, m.seq, i);
+      y[0] = y[1] = 0.f;
+      if (p.dfinal && l.any() && GDR_IN_BOUNDS(sq < p.num_seqs)) load2<PAIRS>(p.dfinal + (int64_t)sq * p.D, l, y);
+    };
 #pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = fmaf(a[i][v], s[v], b_of(i, v));
+    for (int i = 0; i < kTok; ++i) {
+      if (m.first >> i & 1) initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, s);
+      advance(i, s);
     }
 #pragma unroll
-    for (int i = TOK - 1; i >= 0; --i) {
-      if (m.last >> i & 1) {  // the gradient of the sequence's final state enters here
-        const int n = __shfl_sync(0xffffffffu, m.seq, i);
-        float df[V];
+    for (int i = kTok - 1; i >= 0; --i) {
+      if (m.last >> i & 1) end_gradient(i, r);
+      const Raw<IO> dh = read_row<PAIRS>(rows.dh[i], lane);
 #pragma unroll
-        for (int v = 0; v < V; ++v) df[v] = 0.f;
-        if (p.dfinal && on && GDR_IN_BOUNDS(n < p.num_seqs && c + V <= p.D))
-          load_state<V>(p.dfinal + (int64_t)n * p.D + c, df);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          d[i][v] += df[v];
-          qv[v] = 0.f;
-        }
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) qv[v] = a[i][v] * (d[i][v] + qv[v]);
+      for (int v = 0; v < 2; ++v) r[v] = a[i][v] * (dh.at(v) + r[v]);
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      sh.G[w][lane * V + v] = gs[v];
-      sh.A[w][lane * V + v] = expf(gs[v]);
-      sh.H[w][lane * V + v] = qv[v];
-      state_H[w][lane * V + v] = s[v];
+    for (int v = 0; v < 2; ++v) {
+      const float A = -expf(gs[v]);
+      sh.A[parity][w][2 * lane + v] = m.last ? kClosed : A;
+      sh.H[parity][w][2 * lane + v] = r[v];
+      state_A[w][2 * lane + v] = m.first ? kClosed : A;
+      state_H[w][2 * lane + v] = s[v];
     }
-    if (lane == 0) {
-      sh.closed[w] = m.last != 0;
-      state_closed[w] = m.first != 0;
-    }
-    __syncthreads();
-    const uint32_t next = sh.ticket;
-    const Place nq = place_of<true>(p, next < total ? next : 0);
-    load(nq, next < total);
+    if (__syncthreads_or(!landed)) return;
+    if (p.chained && w == 0 && q.in_group() != kGroup - 1) publish_tile<PAIRS, true>(p, sh, parity, q, l, lane);
+    const Place nq = taken<true>(p, sh);
+    const bool more = nq.step < p.tiles;
 #pragma unroll
-    for (int j = 0; j < WARPS - 1; ++j)  // the state that enters the warp
+    for (int j = 0; j < kWarps - 1; ++j)  // the state that enters the warp
       if (j < w)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          h[v] = state_closed[j] ? state_H[j][lane * V + v]
-                                 : fmaf(sh.A[j][lane * V + v], h[v], state_H[j][lane * V + v]);
-    const bool group_end = q.in_group == kGroup - 1;
-    if (p.chained && w == 0 && !group_end)
-      publish_map<V>(p, q, map_before<V, WARPS, true>(sh, -1, lane), c, on);
-    const Map<V> after = map_before<V, WARPS, true>(sh, w, lane);
-    float in[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) in[v] = 0.f;
+        for (int v = 0; v < 2; ++v) h[v] = through(state_A[j][2 * lane + v], state_H[j][2 * lane + v], h[v]);
+    r[0] = r[1] = 0.f;
     if (p.chained) {
-      if (!enter_tile<V, WARPS>(p, sh, q, c, on, w, lane, in)) return;
+      if (!enter_tile<PAIRS>(p, sh, q, l, w, lane, r)) return;
     } else {
-      __syncthreads();  // the maps are read before the next tile's are written
+      __syncthreads();  // the next ticket is read before it is replaced
     }
+    enter_warp<PAIRS, true>(p, sh, parity, q, l, w, lane, r);
+    float before[kTok][2];  // h_{t-1}, less x_t for the complement
 #pragma unroll
-    for (int v = 0; v < V; ++v) qv[v] = after.of(in[v], v);
-    if (p.chained && w == 0 && group_end) {
-      float out[V];
+    for (int i = 0; i < kTok; ++i) {
+      if (m.first >> i & 1) initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, h);
+      const Raw<IO> x = read_row<PAIRS>(rows.x[i], lane);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        out[v] = m.last ? sh.H[w][lane * V + v] : fmaf(sh.A[w][lane * V + v], qv[v], sh.H[w][lane * V + v]);
-      publish_carry<V>(p, q, out, c, on);
+      for (int v = 0; v < 2; ++v) before[i][v] = COMPLEMENT ? h[v] - x.at(v) : h[v];
+      if (i < kTok - 1) advance(i, h);
     }
-    float before[TOK][V];  // h_{t-1}
+    IO *dx0 = static_cast<IO *>(p.dx) + (int64_t)t0 * p.D;
+    float *dg0 = p.dg + (int64_t)t0 * p.D;
+    const int n = l.any() ? tokens_of(p, t0) : 0;
 #pragma unroll
-    for (int i = 0; i < TOK; ++i) {
-      if (m.first >> i & 1) initial_of<V>(p, __shfl_sync(0xffffffffu, m.seq, i), c, on, h);
+    for (int i = kTok - 1; i >= 0; --i) {
+      float dx[2], dg[2];
+      if (m.last >> i & 1) end_gradient(i, r);
+      const Raw<IO> dh = read_row<PAIRS>(rows.dh[i], lane);
+      Raw<float> g;
+      if (COMPLEMENT) g = read_row<PAIRS>(rows.g[i], lane);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        before[i][v] = COMPLEMENT ? h[v] - x[i][v] : h[v];
-        h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+      for (int v = 0; v < 2; ++v) {
+        const float dt = dh.at(v) + r[v];
+        r[v] = a[i][v] * dt;
+        dx[v] = COMPLEMENT ? fresh<IO>(g.at(v), a[i][v]) * dt : dt;
+        dg[v] = r[v] * before[i][v];
       }
-    }
-    IO *dx0 = static_cast<IO *>(p.dx) + (int64_t)t0 * p.D + c;
-    float *dg0 = p.dg + (int64_t)t0 * p.D + c;
-    const int n = on ? (int)min((int64_t)TOK, p.tokens - t0) : 0;
-#pragma unroll
-    for (int i = TOK - 1; i >= 0; --i) {
-      float dx[V], dg[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float dt = m.last >> i & 1 ? d[i][v] : d[i][v] + qv[v];
-        qv[v] = a[i][v] * dt;
-        dx[v] = COMPLEMENT ? u[COMPLEMENT ? i : 0][v] * dt : dt;
-        dg[v] = qv[v] * before[i][v];
-      }
-      if (i < n && GDR_IN_BOUNDS(t0 + i < p.tokens && c + V <= p.D)) {
-        store_row<IO, V>(dx0 + (int64_t)i * p.D, dx);
-        store_row<float, V>(dg0 + (int64_t)i * p.D, dg);
+      if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) {
+        store2<PAIRS>(dx0 + (int64_t)i * p.D, l, dx);
+        store2<PAIRS>(dg0 + (int64_t)i * p.D, l, dg);
       }
       if (p.dinitial && (m.first >> i & 1)) {
         const int sq = __shfl_sync(0xffffffffu, m.seq, i);
-        if (on && GDR_IN_BOUNDS(sq < p.num_seqs && c + V <= p.D))
-          store_row<float, V>(p.dinitial + (int64_t)sq * p.D + c, qv);
+        if (l.any() && GDR_IN_BOUNDS(sq < p.num_seqs)) store2<PAIRS>(p.dinitial + (int64_t)sq * p.D, l, r);
       }
     }
-    if (q.tile == 0) pass_empty<WARPS>(p, p.dfinal, p.dinitial, false, q.stripe * 32 * V, 32 * V);
-    if (next >= total) return;
-    ticket = next;
+    if (q.tile == 0) pass_empty(p, p.dfinal, p.dinitial, false, q.stripe * kWide, kWide);
+    if (!more) return;
     q = nq;
+    begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], q, w, lane);
   }
 }
 
@@ -737,8 +783,9 @@ __global__ void __launch_bounds__(256) glr_no_tokens_kernel(GlrArgs p, bool back
 }
 
 // One token for each sequence, the state in place.
-template <typename IO, int V, bool COMPLEMENT>
+template <typename IO, bool PAIRS, bool COMPLEMENT>
 __global__ void __launch_bounds__(256) glr_step_kernel(GlrArgs p) {
+  constexpr int V = PAIRS ? 2 : 1;
   const int c = (blockIdx.x * 256 + threadIdx.x) * V;
   if (c >= p.D) return;
   for (int n = blockIdx.y; n < p.num_seqs; n += gridDim.y) {
@@ -747,30 +794,83 @@ __global__ void __launch_bounds__(256) glr_step_kernel(GlrArgs p) {
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = 0.f;
     if (r >= 0 && GDR_IN_BOUNDS(r < p.num_slots && c + V <= p.D)) {
-      Raw<IO, V> x;
-      Raw<float, V> g;
-      x.load(static_cast<const IO *>(p.x) + n * p.ld_x + c);
-      g.load(p.g + n * p.ld_g + c);
-      load_state<V>(p.final_state + r * p.D + c, h);
+      const IO *x = static_cast<const IO *>(p.x) + n * p.ld_x + c;
+      const float *g = p.g + n * p.ld_g + c;
+      float *s = p.final_state + r * p.D + c;
+      float xv[V], gv[V];
+      if constexpr (PAIRS) {
+        const float2 g2 = __ldg(reinterpret_cast<const float2 *>(g)), s2 = *reinterpret_cast<const float2 *>(s);
+        gv[0] = g2.x; gv[1] = g2.y;
+        h[0] = s2.x; h[1] = s2.y;
+        if constexpr (sizeof(IO) == 2) {
+          const uint32_t u = __ldg(reinterpret_cast<const unsigned int *>(x));
+          xv[0] = bf16_lo(u); xv[1] = bf16_hi(u);
+        } else {
+          const float2 x2 = __ldg(reinterpret_cast<const float2 *>(x));
+          xv[0] = x2.x; xv[1] = x2.y;
+        }
+      } else {
+        gv[0] = __ldg(g);
+        h[0] = *s;
+        xv[0] = io<IO>::load(x);
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        h[v] = fmaf(expf(g.at(v)), h[v], COMPLEMENT ? -expm1f(g.at(v)) * x.at(v) : x.at(v));
-      store_row<float, V>(p.final_state + r * p.D + c, h);
+        h[v] = fmaf(expf(gv[v]), h[v], COMPLEMENT ? -expm1f(gv[v]) * xv[v] : xv[v]);
+      if constexpr (PAIRS) *reinterpret_cast<float2 *>(s) = make_float2(h[0], h[1]);
+      else *s = h[0];
     }
-    if (GDR_IN_BOUNDS(c + V <= p.D)) store_row<IO, V>(static_cast<IO *>(p.h) + (int64_t)n * p.D + c, h);
+    if (GDR_IN_BOUNDS(c + V <= p.D)) {
+      IO *out = static_cast<IO *>(p.h) + (int64_t)n * p.D + c;
+      if constexpr (!PAIRS) io<IO>::store(out, h[0]);
+      else if constexpr (sizeof(IO) == 2) *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(h[0], h[1]);
+      else *reinterpret_cast<float2 *>(out) = make_float2(h[0], h[1]);
+    }
   }
 }
 
 bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
-// Two channels a lane where rows and pointers allow 2-channel accesses, else one.
+// Two neighbouring channels a lane where the outputs' rows and the states allow it ...
 bool pairs_ok(const GlrArgs &p) {
   const size_t e = p.bf16 ? 2 : 4;
   return p.D % 2 == 0 && p.ld_x % 2 == 0 && p.ld_g % 2 == 0 && p.ld_dh % 2 == 0 &&
          aligned_to(p.x, 2 * e) && aligned_to(p.h, 2 * e) && aligned_to(p.dh, 2 * e) &&
          aligned_to(p.dx, 2 * e) && aligned_to(p.g, 8) && aligned_to(p.dg, 8) &&
          aligned_to(p.initial_state, 8) && aligned_to(p.final_state, 8) &&
-         aligned_to(p.dinitial, 8) && aligned_to(p.chunk_states, 8);
+         aligned_to(p.dfinal, 8) && aligned_to(p.dinitial, 8) && aligned_to(p.chunk_states, 8);
+}
+// ... and the inputs' rows begin on 16 bytes, as tensor-map copies need.
+bool maps_ok(const GlrArgs &p) {
+  const int64_t v = p.bf16 ? 8 : 4;
+  return pairs_ok(p) && p.ld_x % v == 0 && p.ld_dh % v == 0 && p.ld_g % 4 == 0 && aligned_to(p.x, 16) &&
+         aligned_to(p.dh, 16) && aligned_to(p.g, 16);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) == cudaSuccess &&
+        r == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// A warp's rows of a [tokens, D] tensor: boxes of 16 tokens x 64 channels, zeros outside.
+bool make_map(CUtensorMap *m, const void *base, bool bf16, const GlrArgs &p, int64_t ld) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t e = bf16 ? 2 : 4;
+  cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.tokens}, strides[1] = {(cuuint64_t)ld * e};
+  cuuint32_t box[2] = {kWide, kTok}, estr[2] = {1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_begin(const GlrArgs &p, cudaStream_t s) {
@@ -790,76 +890,106 @@ cudaError_t launch_no_tokens(const GlrArgs &p, bool backward, cudaStream_t s) {
 
 // The stripes of a call, and whether its tiles wait for one another: not where
 // each begins with a sequence's first token.
-template <int V> GlrArgs with_chain(const GlrArgs &a) {
+GlrArgs with_chain(const GlrArgs &a) {
   GlrArgs p = a;
-  p.stripes = (p.D + 32 * V - 1) / (32 * V);
+  p.stripes = (p.D + kWide - 1) / kWide;
   p.chained = p.tiles > 1 && (p.cu_seqlens || p.T > kTile || kTile % p.T != 0);
   p.groups = (p.tiles + kGroup - 1) / kGroup;
   p.carry = p.tile_map + p.tiles * p.pitch;
   return p;
 }
 
-// As many blocks as run at once, or one a tile.
-unsigned persistent_grid(const GlrArgs &p, int per_sm) {
-  const int64_t tiles = p.tiles * p.stripes, most = (int64_t)sm_count() * per_sm;
-  return (unsigned)(tiles < most ? tiles : most);
+// Blocks of a scan kernel that run at once on the current device (asked once a device).
+template <typename K> cudaError_t resident_blocks(K kernel, std::atomic<int> *cache, size_t smem, int *blocks) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool keep = dev >= 0 && dev < kCachedDevices;
+  *blocks = keep ? cache[dev].load(std::memory_order_relaxed) : 0;
+  if (*blocks > 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  int per_sm = 0;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+  if (e != cudaSuccess) return e;
+  *blocks = sm_count() * (per_sm > 0 ? per_sm : 1);
+  if (keep) cache[dev].store(*blocks, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
-template <typename IO, int V, bool COMPLEMENT>
+// Launches a scan kernel with as many blocks as run at once, or one a tile.
+template <auto KERNEL>
+cudaError_t launch_tiles(const char *name, size_t smem, const GlrArgs &p, const GlrMaps &maps, cudaStream_t s) {
+  static std::atomic<int> cache[kCachedDevices];
+  int most = 0;
+  cudaError_t e = resident_blocks(KERNEL, cache, smem, &most);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = p.tiles * p.stripes;
+  TraceScope tr(name, s);
+  KERNEL<<<(unsigned)(tiles < most ? tiles : most), kThreads, smem, s>>>(p, maps);
+  return cudaGetLastError();
+}
+
+template <typename IO, bool PAIRS, bool COMPLEMENT>
 cudaError_t launch_fwd(const GlrArgs &a, cudaStream_t s) {
-  const GlrArgs p = with_chain<V>(a);
+  const GlrArgs p = with_chain(a);
   cudaError_t e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, false, s);
-  TraceScope tr("glr_scan_kernel", s);
-  glr_scan_kernel<IO, V, COMPLEMENT, false><<<persistent_grid(p, 4), 128, 0, s>>>(p);
-  return cudaGetLastError();
+  GlrMaps maps;
+  if (PAIRS && !(make_map(&maps.x, p.x, p.bf16, p, p.ld_x) && make_map(&maps.g, p.g, false, p, p.ld_g)))
+    return cudaErrorInvalidValue;
+  return launch_tiles<glr_scan_kernel<IO, PAIRS, COMPLEMENT, false>>("glr_scan_kernel", kWarps * sizeof(WarpRows<IO>),
+                                                                    p, maps, s);
 }
 
-template <typename IO, int V, bool COMPLEMENT>
+template <typename IO, bool PAIRS, bool COMPLEMENT>
 cudaError_t launch_bwd(const GlrArgs &a, cudaStream_t s) {
-  const GlrArgs p = with_chain<V>(a);
+  const GlrArgs p = with_chain(a);
   cudaError_t e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, true, s);
+  GlrMaps maps;
+  if (PAIRS && !(make_map(&maps.x, p.x, p.bf16, p, p.ld_x) && make_map(&maps.g, p.g, false, p, p.ld_g) &&
+                 make_map(&maps.dh, p.dh, p.bf16, p, p.ld_dh)))
+    return cudaErrorInvalidValue;
   if (p.own_chunks) {
-    {
-      TraceScope tr("glr_scan_kernel", s);
-      glr_scan_kernel<IO, V, COMPLEMENT, true><<<persistent_grid(p, 4), 128, 0, s>>>(p);
-    }
-    e = launch_begin(p, s);
+    e = launch_tiles<glr_scan_kernel<IO, PAIRS, COMPLEMENT, true>>("glr_scan_kernel", kWarps * sizeof(WarpRows<IO>), p,
+                                                                  maps, s);
+    if (e == cudaSuccess) e = launch_begin(p, s);
     if (e != cudaSuccess) return e;
   }
-  TraceScope tr("glr_gradient_kernel", s);
-  glr_gradient_kernel<IO, V, COMPLEMENT><<<persistent_grid(p, 2), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_tiles<glr_gradient_kernel<IO, PAIRS, COMPLEMENT>>("glr_gradient_kernel",
+                                                                 kWarps * sizeof(WarpRowsBwd<IO>), p, maps, s);
 }
 
-template <typename IO, int V, bool COMPLEMENT>
+template <typename IO, bool PAIRS, bool COMPLEMENT>
 cudaError_t launch_step(const GlrArgs &p, cudaStream_t s) {
   TraceScope tr("glr_step_kernel", s);
-  const dim3 grid((unsigned)((p.D + 256 * V - 1) / (256 * V)),
-                  (unsigned)(p.num_seqs < 65535 ? p.num_seqs : 65535));
-  glr_step_kernel<IO, V, COMPLEMENT><<<grid, 256, 0, s>>>(p);
+  const int wide = PAIRS ? 512 : 256;
+  const dim3 grid((unsigned)((p.D + wide - 1) / wide), (unsigned)(p.num_seqs < 65535 ? p.num_seqs : 65535));
+  glr_step_kernel<IO, PAIRS, COMPLEMENT><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-#define GDR_GLR_DISPATCH(fn)                                                            \
-  do {                                                                                  \
-    const bool two = pairs_ok(p);                                                       \
-    if (p.bf16)                                                                         \
-      return p.complement ? (two ? fn<__nv_bfloat16, 2, true>(p, s) : fn<__nv_bfloat16, 1, true>(p, s))   \
-                          : (two ? fn<__nv_bfloat16, 2, false>(p, s) : fn<__nv_bfloat16, 1, false>(p, s)); \
-    return p.complement ? (two ? fn<float, 2, true>(p, s) : fn<float, 1, true>(p, s))   \
-                        : (two ? fn<float, 2, false>(p, s) : fn<float, 1, false>(p, s)); \
+#define GDR_GLR_DISPATCH(fn, pairs)                                                      \
+  do {                                                                                   \
+    const bool two = pairs;                                                              \
+    if (p.bf16)                                                                          \
+      return p.complement ? (two ? fn<__nv_bfloat16, true, true>(p, s) : fn<__nv_bfloat16, false, true>(p, s))   \
+                          : (two ? fn<__nv_bfloat16, true, false>(p, s) : fn<__nv_bfloat16, false, false>(p, s)); \
+    return p.complement ? (two ? fn<float, true, true>(p, s) : fn<float, false, true>(p, s))   \
+                        : (two ? fn<float, true, false>(p, s) : fn<float, false, false>(p, s)); \
   } while (0)
 
 }  // namespace
 
 GDR_DEFINE_OOB_COUNTER(oob_count_glr)
 
-cudaError_t launch_glr_fwd(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_fwd); }
-cudaError_t launch_glr_bwd(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_bwd); }
-cudaError_t launch_glr_step(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_step); }
+cudaError_t launch_glr_fwd(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_fwd, maps_ok(p)); }
+cudaError_t launch_glr_bwd(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_bwd, maps_ok(p)); }
+cudaError_t launch_glr_step(const GlrArgs &p, cudaStream_t s) { GDR_GLR_DISPATCH(launch_step, pairs_ok(p)); }
 
 }  // namespace gdr
