@@ -272,94 +272,128 @@ template <bool REV> __device__ __forceinline__ Place taken(const GlrArgs &p, con
   return q;
 }
 
-// What enters the tile.  Each warp joins its part of the group's earlier maps
-// (the first warp's part starts from what enters the group), then all join the
-// parts.  Every thread of the block takes part.  False: a wait gave up.
-template <bool PAIRS>
-__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, const Place &q, const Lane<PAIRS> &l,
-                                           int w, int lane, float (&in)[2]) {
-  const int at = q.in_group(), j0 = w * kPart;
-  const int n = l.any() && GDR_IN_BOUNDS(q.step < p.tiles) ? at - j0 : 0;  // maps to join (at most kPart)
-  const bool start = l.any() && w == 0 && q.step >= kGroup;
-  const uint64_t *maps = p.tile_map + (int64_t)(q.step - at + j0) * p.pitch;
-  const uint64_t *carry = p.carry + ((int64_t)q.group() - 1) * p.pitch;
-  uint64_t t[kPart][2], s[2] = {0, 0};
-#pragma unroll
-  for (int j = 0; j < kPart; ++j) t[j][0] = t[j][1] = 0;
-  bool ok = false;
-  for (uint32_t poll = 0;; ++poll) {
-    bool have = true;  // loads what is missing
-    if (start && (s[0] == 0 || (l.on[1] && s[1] == 0))) load_words<PAIRS>(carry, l, s);
-#pragma unroll
-    for (int j = 0; j < kPart; ++j)
-      if (j < n && (t[j][0] == 0 || (l.on[1] && t[j][1] == 0))) load_words<PAIRS>(maps + (int64_t)j * p.pitch, l, t[j]);
-    if (start) have = s[0] != 0 && (!l.on[1] || s[1] != 0);
-#pragma unroll
-    for (int j = 0; j < kPart; ++j)
-      if (j < n) have = have && t[j][0] != 0 && (!l.on[1] || t[j][1] != 0);
-    ok = __all_sync(0xffffffffu, have);
-    if (ok) break;
-    if ((poll & 1023) == 1023 && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK) break;
-    if (poll == kMaxChainPolls) {
-      *p.status = KDA_DEVICE_TIMEOUT;
-      break;
-    }
+// A poll's verdict: false to go on, true to stop (the wait gave up, here or elsewhere).
+__device__ __forceinline__ bool give_up(const GlrArgs &p, uint32_t poll) {
+  if ((poll & 1023) == 1023 && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK) return true;
+  if (poll == kMaxChainPolls) {
+    *p.status = KDA_DEVICE_TIMEOUT;
+    return true;
   }
-#pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    Map m{-1.f, word_H(s[v])};
-#pragma unroll
-    for (int j = 0; j < kPart; ++j)
-      if (j < n) then(m, word_A(t[j][v]), word_H(t[j][v]));
-    sh.before_A[w][2 * lane + v] = m.A;
-    sh.before_H[w][2 * lane + v] = m.H;
-  }
-  if (__syncthreads_or(!ok)) return false;
-#pragma unroll
-  for (int v = 0; v < 2; ++v) in[v] = sh.before_H[0][2 * lane + v];
-#pragma unroll
-  for (int k = 1; k < kWarps; ++k)
-    if (k * kPart < at)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) in[v] = through(sh.before_A[k][2 * lane + v], sh.before_H[k][2 * lane + v], in[v]);
-  return true;
+  return false;
+}
+template <bool PAIRS> __device__ __forceinline__ bool here(const uint64_t (&u)[2], const Lane<PAIRS> &l) {
+  return u[0] != 0 && (!l.on[1] || u[1] != 0);
 }
 
-// After the warps have shared their maps: the last one in the chain's direction
-// publishes the tile's, unless the tile ends its group.
+// The map of a tile from the maps that its warps have shared.
+template <bool REV>
+__device__ __forceinline__ Map tile_map_of(const TileShared &sh, int buf, int at, Map m) {
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) {
+    const int j = REV ? kWarps - 1 - k : k;
+    then(m, sh.A[buf][j][at], sh.H[buf][j][at]);
+  }
+  return m;
+}
+
+// After the warps have shared their maps, one of them publishes the tile's,
+// unless the tile ends its group.
 template <bool PAIRS, bool REV>
 __device__ __forceinline__ void publish_tile(const GlrArgs &p, const TileShared &sh, int buf, const Place &q,
                                              const Lane<PAIRS> &l, int lane) {
   Map m[2];
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    m[v] = Map{-1.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      const int j = REV ? kWarps - 1 - k : k;
-      then(m[v], sh.A[buf][j][2 * lane + v], sh.H[buf][j][2 * lane + v]);
-    }
-  }
+  for (int v = 0; v < 2; ++v) m[v] = tile_map_of<REV>(sh, buf, 2 * lane + v, Map{-1.f, 0.f});
   if (l.any() && GDR_IN_BOUNDS(q.step < p.tiles)) store_words<PAIRS>(p.tile_map + (int64_t)q.step * p.pitch, l, m);
 }
-// `x`, what enters the tile, becomes what enters warp w, and at the end of a
-// group what leaves the tile is published (by the last warp).
+
+// What enters the tile.  Each warp joins its part of the group's earlier maps,
+// then all join the parts and wait for what enters the group.  That wait is the
+// serial part of the chain: the tile that ends a group has its own map joined to
+// the others by then, so a group costs one poll, one product-sum and one store.
+// Every thread of the block takes part.  False: a wait gave up.
 template <bool PAIRS, bool REV>
-__device__ __forceinline__ void enter_warp(const GlrArgs &p, const TileShared &sh, int buf, const Place &q,
-                                           const Lane<PAIRS> &l, int w, int lane, float (&x)[2]) {
+__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int buf, const Place &q,
+                                           const Lane<PAIRS> &l, int w, int lane, float (&in)[2]) {
+  const int at = q.in_group(), j0 = w * kPart;
+  const int n = l.any() && GDR_IN_BOUNDS(q.step < p.tiles) ? at - j0 : 0;  // maps to join (at most kPart)
+  bool ok = true;
+  if (at > j0) {
+    const uint64_t *maps = p.tile_map + (int64_t)(q.step - at + j0) * p.pitch;
+    uint64_t t[kPart][2];
+#pragma unroll
+    for (int j = 0; j < kPart; ++j) t[j][0] = t[j][1] = 0;
+    for (uint32_t poll = 0;; ++poll) {
+      bool have = true;  // loads what is missing
+#pragma unroll
+      for (int j = 0; j < kPart; ++j)
+        if (j < n && !here<PAIRS>(t[j], l)) load_words<PAIRS>(maps + (int64_t)j * p.pitch, l, t[j]);
+#pragma unroll
+      for (int j = 0; j < kPart; ++j)
+        if (j < n) have = have && here<PAIRS>(t[j], l);
+      if (__all_sync(0xffffffffu, have)) break;
+      if (give_up(p, poll)) {
+        ok = false;
+        break;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      Map m{word_A(t[0][v]), word_H(t[0][v])};
+#pragma unroll
+      for (int j = 1; j < kPart; ++j)
+        if (j < n) then(m, word_A(t[j][v]), word_H(t[j][v]));
+      sh.before_A[w][2 * lane + v] = m.A;
+      sh.before_H[w][2 * lane + v] = m.H;
+    }
+  }
+  if (__syncthreads_or(!ok)) return false;
+  Map before[2], out[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    before[v] = Map{-1.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k)
+      if (k * kPart < at) then(before[v], sh.before_A[k][2 * lane + v], sh.before_H[k][2 * lane + v]);
+  }
+  const bool publish = at == kGroup - 1 && w == (REV ? 0 : kWarps - 1);
+  if (publish)
+#pragma unroll
+    for (int v = 0; v < 2; ++v) out[v] = tile_map_of<REV>(sh, buf, 2 * lane + v, before[v]);
+  in[0] = in[1] = 0.f;
+  if (q.step >= kGroup) {
+    const uint64_t *carry = p.carry + ((int64_t)q.group() - 1) * p.pitch;
+    uint64_t u[2] = {0, 0};
+    for (uint32_t poll = 0;; ++poll) {
+      if (l.any() && GDR_IN_BOUNDS(q.group() <= p.groups)) load_words<PAIRS>(carry, l, u);
+      if (__all_sync(0xffffffffu, !l.any() || here<PAIRS>(u, l))) break;
+      if (give_up(p, poll)) {
+        ok = false;  // the block finds out at its next barrier
+        break;
+      }
+    }
+    in[0] = word_H(u[0]);
+    in[1] = word_H(u[1]);
+  }
+  if (publish && ok) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) out[v] = Map{kClosed, through(out[v].A, out[v].H, in[v])};
+    if (l.any() && GDR_IN_BOUNDS(q.group() < p.groups)) store_words<PAIRS>(p.carry + (int64_t)q.group() * p.pitch, l, out);
+  }
+#pragma unroll
+  for (int v = 0; v < 2; ++v) in[v] = through(before[v].A, before[v].H, in[v]);
+  return ok;
+}
+
+// `x`, what enters the tile, becomes what enters warp w.
+template <bool REV>
+__device__ __forceinline__ void enter_warp(const TileShared &sh, int buf, int w, int lane, float (&x)[2]) {
 #pragma unroll
   for (int k = 0; k < kWarps - 1; ++k) {
     const int j = REV ? kWarps - 1 - k : k;
     if (REV ? j > w : j < w)
 #pragma unroll
       for (int v = 0; v < 2; ++v) x[v] = through(sh.A[buf][j][2 * lane + v], sh.H[buf][j][2 * lane + v], x[v]);
-  }
-  if (p.chained && w == (REV ? 0 : kWarps - 1) && q.in_group() == kGroup - 1) {
-    Map m[2];
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-      m[v] = Map{kClosed, through(sh.A[buf][w][2 * lane + v], sh.H[buf][w][2 * lane + v], x[v])};
-    if (l.any() && GDR_IN_BOUNDS(q.group() < p.groups)) store_words<PAIRS>(p.carry + (int64_t)q.group() * p.pitch, l, m);
   }
 }
 
@@ -496,16 +530,17 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
   if (q.step >= p.tiles) return;
   __syncthreads();
   begin_copies<IO, PAIRS, false>(p, maps, rows, &sh.full[w], q, w, lane);
-  bool marked = has_marks(p, q.tile);
+  bool marked = has_marks(p, q.tile), alive = true;
   while (true) {
     if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
-    const Lane<PAIRS> l(q.stripe, p.D);
+    Lane<PAIRS> l(q.stripe, p.D);
     const uint32_t t0 = q.tile * kTile + w * kTok;
     Marks m;
     m.first = m.last = 0;
     m.seq = 0;
     if (marked) m = find_marks(p, t0, lane);
-    const bool landed = copies_done<PAIRS>(p, &sh.full[w], parity);
+    alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
+    const int buf = parity;
     parity ^= 1;
     // the span's map; b of a token is x, or (1 - a) x
     float a[kTok][2], b[COMPLEMENT ? kTok : 1][2], gs[2] = {0.f, 0.f}, h[2] = {0.f, 0.f};
@@ -547,11 +582,11 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-      sh.A[parity][w][2 * lane + v] = m.first ? kClosed : -expf(gs[v]);
-      sh.H[parity][w][2 * lane + v] = h[v];
+      sh.A[buf][w][2 * lane + v] = m.first ? kClosed : -expf(gs[v]);
+      sh.H[buf][w][2 * lane + v] = h[v];
     }
-    if (__syncthreads_or(!landed)) return;
-    if (p.chained && w == kWarps - 1 && q.in_group() != kGroup - 1) publish_tile<PAIRS, false>(p, sh, parity, q, l, lane);
+    if (__syncthreads_or(!alive)) return;  // a wait gave up; no copy is under way
+    if (p.chained && w == kWarps - 1 && q.in_group() != kGroup - 1) publish_tile<PAIRS, false>(p, sh, buf, q, l, lane);
     const Place nq = taken<false>(p, sh);
     const bool more = nq.step < p.tiles;
     if (more) {
@@ -560,17 +595,15 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     }
     float in[2] = {0.f, 0.f};
     if (p.chained) {
-      if (!enter_tile<PAIRS>(p, sh, q, l, w, lane, in)) {
-        if (more) copies_done<PAIRS>(p, &sh.full[w], parity);
-        return;
-      }
+      alive = enter_tile<PAIRS, false>(p, sh, buf, q, l, w, lane, in);
+      if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced
     }
     if (w == 0 && l.any() && p.chunk_states && GDR_IN_BOUNDS(q.tile < p.tiles))
       store2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, in);
     h[0] = in[0]; h[1] = in[1];
-    enter_warp<PAIRS, false>(p, sh, parity, q, l, w, lane, h);
+    enter_warp<false>(sh, buf, w, lane, h);
     if (!STATES_ONLY) {
       IO *out = static_cast<IO *>(p.h) + (int64_t)t0 * p.D;
       const int n = l.any() ? tokens_of(p, t0) : 0;
@@ -603,12 +636,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
 }
 
 // Backward: the states again from what enters the tile (saved), the gradients
-// from what enters it from the tokens after it (chained).  The rows stay in
-// shared memory until the second pass has read them; more blocks an SM take
-// the place of the early copies.
+// from what enters it from the tokens after it (chained).  EARLY: x and dh go to
+// registers too, and the next tile's copies run while this one waits; else (x
+// and dh too wide, or g needed again) the rows stay in shared memory until the
+// second pass has read them.
 template <typename IO, bool PAIRS, bool COMPLEMENT>
-__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 ? 5 : 4)
+__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 && !COMPLEMENT ? 3 : 4)
 glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
+  constexpr bool EARLY = sizeof(IO) == 2 && !COMPLEMENT;
   __shared__ TileShared sh;
   __shared__ float state_A[kWarps][kWide], state_H[kWarps][kWide];
   extern __shared__ __align__(128) unsigned char tile_bytes[];
@@ -623,66 +658,89 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
   if (q.step >= p.tiles) return;
   __syncthreads();
   begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], q, w, lane);
+  bool marked = has_marks(p, q.tile), alive = true;
   while (true) {
     if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
-    const Lane<PAIRS> l(q.stripe, p.D);
+    Lane<PAIRS> l(q.stripe, p.D);
     const uint32_t t0 = q.tile * kTile + w * kTok;
     float h[2] = {0.f, 0.f}, s[2] = {0.f, 0.f}, r[2] = {0.f, 0.f}, gs[2] = {0.f, 0.f};
     if (l.any() && GDR_IN_BOUNDS(q.tile < p.tiles)) load2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, h);
     Marks m;
     m.first = m.last = 0;
     m.seq = 0;
-    if (has_marks(p, q.tile)) m = find_marks(p, t0, lane);
-    const bool landed = copies_done<PAIRS>(p, &sh.full[w], parity);
+    if (marked) m = find_marks(p, t0, lane);
+    const bool plain = (m.first | m.last) == 0;
+    alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
+    const int buf = parity;
     parity ^= 1;
     float a[kTok][2];
+    Raw<IO> xk[EARLY ? kTok : 1], dk[EARLY ? kTok : 1];
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+      if (EARLY) {
+        xk[EARLY ? i : 0] = read_row<PAIRS>(rows.x[i], lane);
+        dk[EARLY ? i : 0] = read_row<PAIRS>(rows.dh[i], lane);
+      }
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         a[i][v] = decay<IO>(g.at(v));
         gs[v] += g.at(v);
       }
     }
-    // the state y after token i; the gradient that a sequence's end brings
+    auto x_of = [&](int i) { return EARLY ? xk[EARLY ? i : 0] : read_row<PAIRS>(rows.x[i], lane); };
+    auto d_of = [&](int i) { return EARLY ? dk[EARLY ? i : 0] : read_row<PAIRS>(rows.dh[i], lane); };
+    // 1 - a of a token; the state y after token i; the gradient that a sequence's end brings
+    auto fresh_of = [&](int i, int v) { return fresh<IO>(read_row<PAIRS>(rows.g[i], lane).at(v), a[i][v]); };
     auto advance = [&](int i, float (&y)[2]) {
-      const Raw<IO> x = read_row<PAIRS>(rows.x[i], lane);
-      Raw<float> g;
-      if (COMPLEMENT) g = read_row<PAIRS>(rows.g[i], lane);
+      const Raw<IO> x = x_of(i);
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
-        y[v] = fmaf(a[i][v], y[v], COMPLEMENT ? fresh<IO>(g.at(v), a[i][v]) * x.at(v) : x.at(v));
+      for (int v = 0; v < 2; ++v) y[v] = fmaf(a[i][v], y[v], COMPLEMENT ? fresh_of(i, v) * x.at(v) : x.at(v));
     };
+    auto start = [&](int i, float (&y)[2]) { initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, y); };
     auto end_gradient = [&](int i, float (&y)[2]) {
       const int sq = __shfl_sync(0xffffffffu, m.seq, i);
       y[0] = y[1] = 0.f;
       if (p.dfinal && l.any() && GDR_IN_BOUNDS(sq < p.num_seqs)) load2<PAIRS>(p.dfinal + (int64_t)sq * p.D, l, y);
     };
+    auto back = [&](int i) {
+      const Raw<IO> d = d_of(i);
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      if (m.first >> i & 1) initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, s);
-      advance(i, s);
-    }
+      for (int v = 0; v < 2; ++v) r[v] = a[i][v] * (d.at(v) + r[v]);
+    };
+    if (plain) {
 #pragma unroll
-    for (int i = kTok - 1; i >= 0; --i) {
-      if (m.last >> i & 1) end_gradient(i, r);
-      const Raw<IO> dh = read_row<PAIRS>(rows.dh[i], lane);
+      for (int i = 0; i < kTok; ++i) advance(i, s);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) r[v] = a[i][v] * (dh.at(v) + r[v]);
+      for (int i = kTok - 1; i >= 0; --i) back(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        if (m.first >> i & 1) start(i, s);
+        advance(i, s);
+      }
+#pragma unroll
+      for (int i = kTok - 1; i >= 0; --i) {
+        if (m.last >> i & 1) end_gradient(i, r);
+        back(i);
+      }
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
       const float A = -expf(gs[v]);
-      sh.A[parity][w][2 * lane + v] = m.last ? kClosed : A;
-      sh.H[parity][w][2 * lane + v] = r[v];
+      sh.A[buf][w][2 * lane + v] = m.last ? kClosed : A;
+      sh.H[buf][w][2 * lane + v] = r[v];
       state_A[w][2 * lane + v] = m.first ? kClosed : A;
       state_H[w][2 * lane + v] = s[v];
     }
-    if (__syncthreads_or(!landed)) return;
-    if (p.chained && w == 0 && q.in_group() != kGroup - 1) publish_tile<PAIRS, true>(p, sh, parity, q, l, lane);
+    if (__syncthreads_or(!alive)) return;  // a wait gave up; no copy is under way
+    if (p.chained && w == 0 && q.in_group() != kGroup - 1) publish_tile<PAIRS, true>(p, sh, buf, q, l, lane);
     const Place nq = taken<true>(p, sh);
     const bool more = nq.step < p.tiles;
+    if (more) {
+      if (EARLY) begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], nq, w, lane);
+      marked = has_marks(p, nq.tile);
+    }
 #pragma unroll
     for (int j = 0; j < kWarps - 1; ++j)  // the state that enters the warp
       if (j < w)
@@ -690,50 +748,61 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
         for (int v = 0; v < 2; ++v) h[v] = through(state_A[j][2 * lane + v], state_H[j][2 * lane + v], h[v]);
     r[0] = r[1] = 0.f;
     if (p.chained) {
-      if (!enter_tile<PAIRS>(p, sh, q, l, w, lane, r)) return;
+      alive = enter_tile<PAIRS, true>(p, sh, buf, q, l, w, lane, r);
+      if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced
     }
-    enter_warp<PAIRS, true>(p, sh, parity, q, l, w, lane, r);
+    enter_warp<true>(sh, buf, w, lane, r);
     float before[kTok][2];  // h_{t-1}, less x_t for the complement
+    auto keep = [&](int i) {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      if (m.first >> i & 1) initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, h);
-      const Raw<IO> x = read_row<PAIRS>(rows.x[i], lane);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) before[i][v] = COMPLEMENT ? h[v] - x.at(v) : h[v];
+      for (int v = 0; v < 2; ++v) before[i][v] = COMPLEMENT ? h[v] - x_of(i).at(v) : h[v];
       if (i < kTok - 1) advance(i, h);
-    }
+    };
     IO *dx0 = static_cast<IO *>(p.dx) + (int64_t)t0 * p.D;
     float *dg0 = p.dg + (int64_t)t0 * p.D;
     const int n = l.any() ? tokens_of(p, t0) : 0;
-#pragma unroll
-    for (int i = kTok - 1; i >= 0; --i) {
+    auto write = [&](int i) {
       float dx[2], dg[2];
-      if (m.last >> i & 1) end_gradient(i, r);
-      const Raw<IO> dh = read_row<PAIRS>(rows.dh[i], lane);
-      Raw<float> g;
-      if (COMPLEMENT) g = read_row<PAIRS>(rows.g[i], lane);
+      const Raw<IO> d = d_of(i);
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        const float dt = dh.at(v) + r[v];
+        const float dt = d.at(v) + r[v];
         r[v] = a[i][v] * dt;
-        dx[v] = COMPLEMENT ? fresh<IO>(g.at(v), a[i][v]) * dt : dt;
+        dx[v] = COMPLEMENT ? fresh_of(i, v) * dt : dt;
         dg[v] = r[v] * before[i][v];
       }
       if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) {
         store2<PAIRS>(dx0 + (int64_t)i * p.D, l, dx);
         store2<PAIRS>(dg0 + (int64_t)i * p.D, l, dg);
       }
-      if (p.dinitial && (m.first >> i & 1)) {
-        const int sq = __shfl_sync(0xffffffffu, m.seq, i);
-        if (l.any() && GDR_IN_BOUNDS(sq < p.num_seqs)) store2<PAIRS>(p.dinitial + (int64_t)sq * p.D, l, r);
+    };
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) keep(i);
+#pragma unroll
+      for (int i = kTok - 1; i >= 0; --i) write(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        if (m.first >> i & 1) start(i, h);
+        keep(i);
+      }
+#pragma unroll
+      for (int i = kTok - 1; i >= 0; --i) {
+        if (m.last >> i & 1) end_gradient(i, r);
+        write(i);
+        if (p.dinitial && (m.first >> i & 1)) {
+          const int sq = __shfl_sync(0xffffffffu, m.seq, i);
+          if (l.any() && GDR_IN_BOUNDS(sq < p.num_seqs)) store2<PAIRS>(p.dinitial + (int64_t)sq * p.D, l, r);
+        }
       }
     }
     if (q.tile == 0) pass_empty(p, p.dfinal, p.dinitial, false, q.stripe * kWide, kWide);
     if (!more) return;
     q = nq;
-    begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], q, w, lane);
+    if (!EARLY) begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], q, w, lane);
   }
 }
 
