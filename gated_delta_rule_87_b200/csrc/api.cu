@@ -603,7 +603,7 @@ struct GlrLayout {
 GlrLayout glr_layout(int64_t tokens, int64_t D, bool own_chunks) {
   GlrLayout L{};
   L.tiles = (tokens + gdr::kGlrChunk - 1) / gdr::kGlrChunk;
-  L.pitch = D + (D & 1);
+  L.pitch = (D + 63) / 64 * 64;  // whole tiles
   const size_t groups = (size_t)L.tiles / gdr::kGlrShortestGroup + 1;
   size_t off = kStatusBytes;
   L.marks = off; off = up256(off + (size_t)L.tiles * sizeof(int32_t));
@@ -660,8 +660,7 @@ kda_status_t check_glr(gdr::GlrArgs &a, int32_t B, glr_input_t input, kda_dtype_
   a.tile_marks = reinterpret_cast<int32_t *>(w + L.marks);
   a.tile_map = reinterpret_cast<uint64_t *>(w + L.map);
   if (a.own_chunks) a.chunk_states = reinterpret_cast<float *>(w + L.chunks);
-  // a block a tile of 64 tokens x 32 channels at least
-  if (a.tiles * ((a.D + 31) / 32) > INT32_MAX)
+  if (a.tiles * (a.pitch / 64) > INT32_MAX)  // tickets
     return fail(KDA_ERR_UNSUPPORTED, "too many tokens times channels for one call");
   return KDA_OK;
 }

@@ -190,22 +190,44 @@ __device__ __forceinline__ bool bad_offsets(const GlrArgs &p) {
 // ---- maps of spans ------------------------------------------------------
 // A span of tokens takes what enters it, `in`, to A in + H, or to H where it is
 // closed.  A >= 0 is kept with its sign turned, a closed span as +1 in its place.
-struct Map {
-  float A, H;
+// All channels of a span are closed or none.
+struct Map2 {  // of a lane's two channels
+  float A[2], H[2];
 };
 constexpr float kClosed = 1.f;
 __device__ __forceinline__ float through(float A, float H, float in) { return A > 0.f ? H : fmaf(-A, in, H); }
-__device__ __forceinline__ void then(Map &m, float A, float H) {  // m, then the span (A, H)
-  m.H = through(A, H, m.H);
-  m.A = fmaxf(m.A, A) > 0.f ? kClosed : -(m.A * A);
+__device__ __forceinline__ void through(const Map2 &m, float (&x)[2]) {
+  x[0] = through(m.A[0], m.H[0], x[0]);
+  x[1] = through(m.A[1], m.H[1], x[1]);
+}
+// The map of n spans one after the other (n known where it is unrolled).
+template <int N> __device__ __forceinline__ Map2 joined(const Map2 (&t)[N]) {
+  Map2 m = t[0];
+  bool closed = false;
+#pragma unroll
+  for (int j = 0; j < N; ++j) closed |= t[j].A[0] > 0.f;
+  if (!closed) {
+#pragma unroll
+    for (int j = 1; j < N; ++j)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        m.H[v] = fmaf(-t[j].A[v], m.H[v], t[j].H[v]);
+        m.A[v] = -(m.A[v] * t[j].A[v]);
+      }
+  } else {
+#pragma unroll
+    for (int j = 1; j < N; ++j) through(t[j], m.H);
+    m.A[0] = m.A[1] = kClosed;
+  }
+  return m;
 }
 
 struct TileShared {
   // the warps' maps; a tile's are read until its end, while the next one's are written
-  float A[2][kWarps][kWide], H[2][kWarps][kWide];
-  float before_A[kWarps][kWide], before_H[kWarps][kWide];  // of earlier tiles, a part a warp
-  uint64_t full[kWarps];                                   // a warp's copies have landed
-  uint32_t step;                                           // of the block's next tile
+  Map2 map[2][kWarps][32];
+  Map2 before[kWarps][32];  // of earlier tiles, a part a warp
+  uint64_t full[kWarps];    // a warp's copies have landed
+  uint32_t step;            // of the block's next tile
   int stripe;
 };
 
@@ -221,33 +243,44 @@ struct TileShared {
 //
 // A channel's map goes through the workspace as one 64-bit word (A above, H
 // below), which is its own flag: 0 is not there yet, and A is never +0.  So a
-// hand-over is one store and one polling load, without a fence.
+// hand-over is one store and one polling load, without a fence.  The rows of
+// words are as wide as the tiles (`pitch`), so every lane has its own.
 constexpr int kGroup = 16, kPart = kGroup / kWarps;
 static_assert(kGroup >= kGlrShortestGroup, "the workspace counts groups of at least this length");
 constexpr uint32_t kMaxChainPolls = 1u << 20;  // about a second
 
-template <bool PAIRS> __device__ __forceinline__ void load_words(const uint64_t *p, const Lane<PAIRS> &l, uint64_t (&u)[2]) {
+struct Words {
+  uint64_t u[2];
+  __device__ __forceinline__ bool here() const { return min((uint32_t)(u[0] >> 32), (uint32_t)(u[1] >> 32)) != 0; }
+  __device__ __forceinline__ Map2 map() const {
+    Map2 m;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      m.A[v] = __uint_as_float((uint32_t)(u[v] >> 32));
+      m.H[v] = __uint_as_float((uint32_t)u[v]);
+    }
+    return m;
+  }
+};
+template <bool PAIRS> __device__ __forceinline__ void load_words(const uint64_t *p, Words &w) {
   if constexpr (PAIRS) {
-    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(u[0]), "=l"(u[1]) : "l"(p + l.c) : "memory");
+    asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(w.u[0]), "=l"(w.u[1]) : "l"(p) : "memory");
   } else {
-    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(u[0]) : "l"(p + l.c) : "memory");
-    if (l.on[1]) asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(u[1]) : "l"(p + l.c + 32) : "memory");
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w.u[0]) : "l"(p) : "memory");
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w.u[1]) : "l"(p + 32) : "memory");
   }
 }
-template <bool PAIRS>
-__device__ __forceinline__ void store_words(uint64_t *p, const Lane<PAIRS> &l, const Map (&m)[2]) {
+template <bool PAIRS> __device__ __forceinline__ void store_words(uint64_t *p, const Map2 &m) {
   uint64_t u[2];
 #pragma unroll
-  for (int v = 0; v < 2; ++v) u[v] = (uint64_t)__float_as_uint(m[v].A) << 32 | __float_as_uint(m[v].H);
+  for (int v = 0; v < 2; ++v) u[v] = (uint64_t)__float_as_uint(m.A[v]) << 32 | __float_as_uint(m.H[v]);
   if constexpr (PAIRS) {
-    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p + l.c), "l"(u[0]), "l"(u[1]) : "memory");
+    asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(u[0]), "l"(u[1]) : "memory");
   } else {
-    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p + l.c), "l"(u[0]) : "memory");
-    if (l.on[1]) asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p + l.c + 32), "l"(u[1]) : "memory");
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(u[0]) : "memory");
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p + 32), "l"(u[1]) : "memory");
   }
 }
-__device__ __forceinline__ float word_A(uint64_t u) { return __uint_as_float((uint32_t)(u >> 32)); }
-__device__ __forceinline__ float word_H(uint64_t u) { return __uint_as_float((uint32_t)u); }
 
 // A tile's place in the chain (REV: from the last tile on).
 struct Place {
@@ -272,128 +305,110 @@ template <bool REV> __device__ __forceinline__ Place taken(const GlrArgs &p, con
   return q;
 }
 
-// A poll's verdict: false to go on, true to stop (the wait gave up, here or elsewhere).
+// Whether a wait gives up (here, or elsewhere: the status word says so).
 __device__ __forceinline__ bool give_up(const GlrArgs &p, uint32_t poll) {
-  if ((poll & 1023) == 1023 && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK) return true;
-  if (poll == kMaxChainPolls) {
-    *p.status = KDA_DEVICE_TIMEOUT;
-    return true;
-  }
-  return false;
-}
-template <bool PAIRS> __device__ __forceinline__ bool here(const uint64_t (&u)[2], const Lane<PAIRS> &l) {
-  return u[0] != 0 && (!l.on[1] || u[1] != 0);
-}
-
-// The map of a tile from the maps that its warps have shared.
-template <bool REV>
-__device__ __forceinline__ Map tile_map_of(const TileShared &sh, int buf, int at, Map m) {
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k) {
-    const int j = REV ? kWarps - 1 - k : k;
-    then(m, sh.A[buf][j][at], sh.H[buf][j][at]);
-  }
-  return m;
+  if ((poll & 1023) != 1023) return false;
+  if (*reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK) return true;
+  if (poll < kMaxChainPolls) return false;
+  *p.status = KDA_DEVICE_TIMEOUT;
+  return true;
 }
 
 // After the warps have shared their maps, one of them publishes the tile's,
 // unless the tile ends its group.
 template <bool PAIRS, bool REV>
 __device__ __forceinline__ void publish_tile(const GlrArgs &p, const TileShared &sh, int buf, const Place &q,
-                                             const Lane<PAIRS> &l, int lane) {
-  Map m[2];
+                                             int c, int lane) {
+  Map2 t[kWarps];
 #pragma unroll
-  for (int v = 0; v < 2; ++v) m[v] = tile_map_of<REV>(sh, buf, 2 * lane + v, Map{-1.f, 0.f});
-  if (l.any() && GDR_IN_BOUNDS(q.step < p.tiles)) store_words<PAIRS>(p.tile_map + (int64_t)q.step * p.pitch, l, m);
+  for (int k = 0; k < kWarps; ++k) t[k] = sh.map[buf][REV ? kWarps - 1 - k : k][lane];
+  if (GDR_IN_BOUNDS(q.step < p.tiles && c < p.pitch))
+    store_words<PAIRS>(p.tile_map + (int64_t)q.step * p.pitch + c, joined(t));
 }
 
 // What enters the tile.  Each warp joins its part of the group's earlier maps,
-// then all join the parts and wait for what enters the group.  That wait is the
-// serial part of the chain: the tile that ends a group has its own map joined to
-// the others by then, so a group costs one poll, one product-sum and one store.
-// Every thread of the block takes part.  False: a wait gave up.
+// then all wait for what enters the group and take it through the parts.  That
+// wait is the serial part of the chain: the tile that ends a group sends on
+// what leaves it at once.  Every thread of the block takes part.  False: a wait
+// gave up.
 template <bool PAIRS, bool REV>
-__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int buf, const Place &q,
-                                           const Lane<PAIRS> &l, int w, int lane, float (&in)[2]) {
-  const int at = q.in_group(), j0 = w * kPart;
-  const int n = l.any() && GDR_IN_BOUNDS(q.step < p.tiles) ? at - j0 : 0;  // maps to join (at most kPart)
+__device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int buf, const Place &q, int c, int w,
+                                           int lane, float (&in)[2]) {
+  const int at = q.in_group(), n = at - w * kPart;  // maps to join (at most kPart)
   bool ok = true;
-  if (at > j0) {
-    const uint64_t *maps = p.tile_map + (int64_t)(q.step - at + j0) * p.pitch;
-    uint64_t t[kPart][2];
+  if (n > 0 && GDR_IN_BOUNDS(q.step < p.tiles && c < p.pitch)) {
+    const uint64_t *from = p.tile_map + (int64_t)(q.step - n) * p.pitch + c;
+    Words t[kPart];
 #pragma unroll
-    for (int j = 0; j < kPart; ++j) t[j][0] = t[j][1] = 0;
+    for (int j = 0; j < kPart; ++j) {
+      t[j].u[0] = t[j].u[1] = (uint64_t)__float_as_uint(-1.f) << 32;  // nothing changes
+      if (j < n) load_words<PAIRS>(from + (int64_t)j * p.pitch, t[j]);
+    }
     for (uint32_t poll = 0;; ++poll) {
-      bool have = true;  // loads what is missing
+      bool have = true;
 #pragma unroll
-      for (int j = 0; j < kPart; ++j)
-        if (j < n && !here<PAIRS>(t[j], l)) load_words<PAIRS>(maps + (int64_t)j * p.pitch, l, t[j]);
-#pragma unroll
-      for (int j = 0; j < kPart; ++j)
-        if (j < n) have = have && here<PAIRS>(t[j], l);
+      for (int j = 0; j < kPart; ++j) have = have && t[j].here();
       if (__all_sync(0xffffffffu, have)) break;
       if (give_up(p, poll)) {
         ok = false;
         break;
       }
-    }
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      Map m{word_A(t[0][v]), word_H(t[0][v])};
-#pragma unroll
-      for (int j = 1; j < kPart; ++j)
-        if (j < n) then(m, word_A(t[j][v]), word_H(t[j][v]));
-      sh.before_A[w][2 * lane + v] = m.A;
-      sh.before_H[w][2 * lane + v] = m.H;
+      for (int j = 0; j < kPart; ++j)
+        if (!t[j].here()) load_words<PAIRS>(from + (int64_t)j * p.pitch, t[j]);
     }
+    Map2 m[kPart];
+#pragma unroll
+    for (int j = 0; j < kPart; ++j) m[j] = t[j].map();
+    sh.before[w][lane] = joined(m);
   }
   if (__syncthreads_or(!ok)) return false;
-  Map before[2], out[2];
+  Map2 part[kWarps];
+  bool closed = false;  // nothing to wait for where a sequence began since
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    before[v] = Map{-1.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k)
-      if (k * kPart < at) then(before[v], sh.before_A[k][2 * lane + v], sh.before_H[k][2 * lane + v]);
-  }
-  const bool publish = at == kGroup - 1 && w == (REV ? 0 : kWarps - 1);
-  if (publish)
-#pragma unroll
-    for (int v = 0; v < 2; ++v) out[v] = tile_map_of<REV>(sh, buf, 2 * lane + v, before[v]);
+  for (int k = 0; k < kWarps; ++k)
+    if (k * kPart < at) {
+      part[k] = sh.before[k][lane];
+      closed |= part[k].A[0] > 0.f;
+    }
   in[0] = in[1] = 0.f;
-  if (q.step >= kGroup) {
-    const uint64_t *carry = p.carry + ((int64_t)q.group() - 1) * p.pitch;
-    uint64_t u[2] = {0, 0};
+  if (q.step >= kGroup && !closed && GDR_IN_BOUNDS(q.group() <= p.groups && c < p.pitch)) {
+    const uint64_t *carry = p.carry + ((int64_t)q.group() - 1) * p.pitch + c;
+    Words u;
     for (uint32_t poll = 0;; ++poll) {
-      if (l.any() && GDR_IN_BOUNDS(q.group() <= p.groups)) load_words<PAIRS>(carry, l, u);
-      if (__all_sync(0xffffffffu, !l.any() || here<PAIRS>(u, l))) break;
+      load_words<PAIRS>(carry, u);
+      if (__all_sync(0xffffffffu, u.here())) break;
       if (give_up(p, poll)) {
         ok = false;  // the block finds out at its next barrier
         break;
       }
     }
-    in[0] = word_H(u[0]);
-    in[1] = word_H(u[1]);
-  }
-  if (publish && ok) {
-#pragma unroll
-    for (int v = 0; v < 2; ++v) out[v] = Map{kClosed, through(out[v].A, out[v].H, in[v])};
-    if (l.any() && GDR_IN_BOUNDS(q.group() < p.groups)) store_words<PAIRS>(p.carry + (int64_t)q.group() * p.pitch, l, out);
+    const Map2 m = u.map();
+    in[0] = m.H[0];
+    in[1] = m.H[1];
   }
 #pragma unroll
-  for (int v = 0; v < 2; ++v) in[v] = through(before[v].A, before[v].H, in[v]);
+  for (int k = 0; k < kWarps; ++k)
+    if (k * kPart < at) through(part[k], in);
+  if (ok && at == kGroup - 1 && w == (REV ? 0 : kWarps - 1) && GDR_IN_BOUNDS(q.group() < p.groups && c < p.pitch)) {
+    Map2 out;
+    out.H[0] = in[0];
+    out.H[1] = in[1];
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) through(sh.map[buf][REV ? kWarps - 1 - k : k][lane], out.H);
+    out.A[0] = out.A[1] = kClosed;
+    store_words<PAIRS>(p.carry + (int64_t)q.group() * p.pitch + c, out);
+  }
   return ok;
 }
 
 // `x`, what enters the tile, becomes what enters warp w.
 template <bool REV>
-__device__ __forceinline__ void enter_warp(const TileShared &sh, int buf, int w, int lane, float (&x)[2]) {
+__device__ __forceinline__ void enter_warp(const Map2 (&map)[kWarps][32], int w, int lane, float (&x)[2]) {
 #pragma unroll
   for (int k = 0; k < kWarps - 1; ++k) {
     const int j = REV ? kWarps - 1 - k : k;
-    if (REV ? j > w : j < w)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) x[v] = through(sh.A[buf][j][2 * lane + v], sh.H[buf][j][2 * lane + v], x[v]);
+    if (REV ? j > w : j < w) through(map[j][lane], x);
   }
 }
 
@@ -515,7 +530,7 @@ __device__ __forceinline__ void init_barriers(TileShared &sh) {
 // it, so the next tile's copies run while this one waits for what enters it and
 // is written.  STATES_ONLY: only the saved chunk states are written.
 template <typename IO, bool PAIRS, bool COMPLEMENT, bool STATES_ONLY>
-__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 && !COMPLEMENT ? 5 : 4)
+__global__ void __launch_bounds__(kThreads, 4)
 glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
   __shared__ TileShared sh;
   extern __shared__ __align__(128) unsigned char tile_bytes[];
@@ -580,13 +595,9 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
         }
       }
     }
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      sh.A[buf][w][2 * lane + v] = m.first ? kClosed : -expf(gs[v]);
-      sh.H[buf][w][2 * lane + v] = h[v];
-    }
+    sh.map[buf][w][lane] = {{m.first ? kClosed : -expf(gs[0]), m.first ? kClosed : -expf(gs[1])}, {h[0], h[1]}};
     if (__syncthreads_or(!alive)) return;  // a wait gave up; no copy is under way
-    if (p.chained && w == kWarps - 1 && q.in_group() != kGroup - 1) publish_tile<PAIRS, false>(p, sh, buf, q, l, lane);
+    if (p.chained && w == kWarps - 1 && q.in_group() != kGroup - 1) publish_tile<PAIRS, false>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<false>(p, sh);
     const bool more = nq.step < p.tiles;
     if (more) {
@@ -595,7 +606,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     }
     float in[2] = {0.f, 0.f};
     if (p.chained) {
-      alive = enter_tile<PAIRS, false>(p, sh, buf, q, l, w, lane, in);
+      alive = enter_tile<PAIRS, false>(p, sh, buf, q, l.c, w, lane, in);
       if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced
@@ -603,7 +614,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     if (w == 0 && l.any() && p.chunk_states && GDR_IN_BOUNDS(q.tile < p.tiles))
       store2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, in);
     h[0] = in[0]; h[1] = in[1];
-    enter_warp<false>(sh, buf, w, lane, h);
+    enter_warp<false>(sh.map[buf], w, lane, h);
     if (!STATES_ONLY) {
       IO *out = static_cast<IO *>(p.h) + (int64_t)t0 * p.D;
       const int n = l.any() ? tokens_of(p, t0) : 0;
@@ -645,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 && !COMPLEMENT ? 3 :
 glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
   constexpr bool EARLY = sizeof(IO) == 2 && !COMPLEMENT;
   __shared__ TileShared sh;
-  __shared__ float state_A[kWarps][kWide], state_H[kWarps][kWide];
+  __shared__ Map2 states[kWarps][32];  // the warps' maps of the states
   extern __shared__ __align__(128) unsigned char tile_bytes[];
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -725,35 +736,28 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
         back(i);
       }
     }
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const float A = -expf(gs[v]);
-      sh.A[buf][w][2 * lane + v] = m.last ? kClosed : A;
-      sh.H[buf][w][2 * lane + v] = r[v];
-      state_A[w][2 * lane + v] = m.first ? kClosed : A;
-      state_H[w][2 * lane + v] = s[v];
+    {
+      const float A[2] = {-expf(gs[0]), -expf(gs[1])};
+      sh.map[buf][w][lane] = {{m.last ? kClosed : A[0], m.last ? kClosed : A[1]}, {r[0], r[1]}};
+      states[w][lane] = {{m.first ? kClosed : A[0], m.first ? kClosed : A[1]}, {s[0], s[1]}};
     }
     if (__syncthreads_or(!alive)) return;  // a wait gave up; no copy is under way
-    if (p.chained && w == 0 && q.in_group() != kGroup - 1) publish_tile<PAIRS, true>(p, sh, buf, q, l, lane);
+    if (p.chained && w == 0 && q.in_group() != kGroup - 1) publish_tile<PAIRS, true>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<true>(p, sh);
     const bool more = nq.step < p.tiles;
     if (more) {
       if (EARLY) begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], nq, w, lane);
       marked = has_marks(p, nq.tile);
     }
-#pragma unroll
-    for (int j = 0; j < kWarps - 1; ++j)  // the state that enters the warp
-      if (j < w)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) h[v] = through(state_A[j][2 * lane + v], state_H[j][2 * lane + v], h[v]);
+    enter_warp<false>(states, w, lane, h);
     r[0] = r[1] = 0.f;
     if (p.chained) {
-      alive = enter_tile<PAIRS, true>(p, sh, buf, q, l, w, lane, r);
+      alive = enter_tile<PAIRS, true>(p, sh, buf, q, l.c, w, lane, r);
       if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced
     }
-    enter_warp<true>(sh, buf, w, lane, r);
+    enter_warp<true>(sh.map[buf], w, lane, r);
     float before[kTok][2];  // h_{t-1}, less x_t for the complement
     auto keep = [&](int i) {
 #pragma unroll

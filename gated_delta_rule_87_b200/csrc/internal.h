@@ -125,7 +125,7 @@ struct GlrArgs {
   int32_t *status;
   int32_t *ticket;
   uint64_t *tile_map;   // [tiles][pitch], then the groups' words [groups][pitch]
-  int64_t pitch;        // D, rounded up to even
+  int64_t pitch;        // D, rounded up to whole tiles
   int32_t *tile_marks;  // packed: whether a sequence begins or ends in the tile
   bool own_chunks;  // backward: chunk_states is workspace, to be filled first
   // set at the launch

@@ -380,8 +380,8 @@ KDA_API kda_status_t kda_chunk_fwd_host(const void *q, const void *k, const void
  * products and sums are fp32; only h is rounded to io_dtype.  A non-finite
  * value of one sequence never reaches another.  final_state may be the
  * buffer of initial_state.  An invalid cu_seqlens leaves every output
- * unwritten (kda_check_device_status on the workspace).  B T D / 2048 must fit
- * in int32 (else KDA_ERR_UNSUPPORTED).
+ * unwritten (kda_check_device_status on the workspace).  B T D / 4096 must
+ * fit in int32 (else KDA_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 typedef enum { GLR_INPUT_GIVEN = 0, GLR_INPUT_COMPLEMENT = 1 } glr_input_t;
 
