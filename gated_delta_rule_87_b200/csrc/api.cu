@@ -653,14 +653,14 @@ kda_status_t check_glr(gdr::GlrArgs &a, int32_t B, glr_input_t input, kda_dtype_
   if (workspace_bytes < L.total)
     return fail(KDA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, L.total);
   unsigned char *w = static_cast<unsigned char *>(workspace);
-  a.tiles = L.tiles;
+  a.chunks = L.tiles;
   a.status = reinterpret_cast<int32_t *>(w);
   a.ticket = a.status + 32;
   a.pitch = L.pitch;
   a.tile_marks = reinterpret_cast<int32_t *>(w + L.marks);
   a.tile_map = reinterpret_cast<uint64_t *>(w + L.map);
   if (a.own_chunks) a.chunk_states = reinterpret_cast<float *>(w + L.chunks);
-  if (a.tiles * (a.pitch / 64) > INT32_MAX)  // tickets
+  if (a.chunks * (a.pitch / 64) > INT32_MAX)  // tickets
     return fail(KDA_ERR_UNSUPPORTED, "too many tokens times channels for one call");
   return KDA_OK;
 }

@@ -29,8 +29,7 @@ namespace gdr {
 namespace {
 
 constexpr int kCachedDevices = 64;
-constexpr int kTile = kGlrChunk;  // tokens of a tile
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kTok = kTile / kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kWide = 64;         // channels of a tile, two a lane
 
 // The two channels of a lane.  PAIRS: neighbours, rows and pointers aligned for
@@ -81,6 +80,14 @@ template <bool PAIRS> __device__ __forceinline__ Raw<__nv_bfloat16> read_row(con
   return x;
 }
 
+template <bool PAIRS> __device__ __forceinline__ void write_row(float *row, int lane, const float (&x)[2]) {
+  if constexpr (PAIRS) {
+    reinterpret_cast<float2 *>(row)[lane] = make_float2(x[0], x[1]);
+  } else {
+    row[lane] = x[0]; row[lane + 32] = x[1];
+  }
+}
+
 // Global memory: plain (coherent) accesses, states are updated in place by some calls.
 template <bool PAIRS> __device__ __forceinline__ void load2(const float *p, const Lane<PAIRS> &l, float (&x)[2]) {
   if constexpr (PAIRS) {
@@ -114,36 +121,38 @@ template <typename IO> __device__ __forceinline__ float decay(float g) {
     return expf(g);
   }
 }
-// 1 - a of one token.  With bf16 activations: near 0 the series of -expm1(g)
-// (its first term left out is below 2^-22 of the value), else the difference,
+// 1 - a of one token: near 0 the series of -expm1(g), whose first term left out
+// is below 2^-22 of the value (bf16 activations) or 2^-28, else the difference,
 // which then loses less than two bits.
 template <typename IO> __device__ __forceinline__ float fresh(float g, float a) {
-  if constexpr (sizeof(IO) == 2) {
-    float s = 1.f / 5040.f;
-    s = fmaf(s, g, 1.f / 720.f);
-    s = fmaf(s, g, 1.f / 120.f);
-    s = fmaf(s, g, 1.f / 24.f);
-    s = fmaf(s, g, 1.f / 6.f);
-    s = fmaf(s, g, 0.5f);
-    s = fmaf(s, g, 1.f);
-    return g > -0.5f ? -g * s : 1.f - a;
-  } else {
-    return -expm1f(g);
+  float s = 1.f / 5040.f;
+  if constexpr (sizeof(IO) == 4) {
+    s = 1.f / 362880.f;
+    s = fmaf(s, g, 1.f / 40320.f);
+    s = fmaf(s, g, 1.f / 5040.f);
   }
+  s = fmaf(s, g, 1.f / 720.f);
+  s = fmaf(s, g, 1.f / 120.f);
+  s = fmaf(s, g, 1.f / 24.f);
+  s = fmaf(s, g, 1.f / 6.f);
+  s = fmaf(s, g, 0.5f);
+  s = fmaf(s, g, 1.f);
+  return g > -0.5f ? -g * s : 1.f - a;
 }
 
-// Which of a warp's kTok tokens begin or end a sequence (bit i: token t0 + i), and,
+// Which of a warp's TOK tokens begin or end a sequence (bit i: token t0 + i), and,
 // in lane i, the sequence of token t0 + i.
 struct Marks {
   uint32_t first, last;
   int seq;
 };
-__device__ __forceinline__ Marks find_marks(const GlrArgs &p, uint32_t t0, int lane) {
+template <int TOK> __device__ __forceinline__ Marks find_marks(const GlrArgs &p, uint32_t t0, int lane) {
+  static_assert(TOK <= 32, "a lane a token");
   Marks m;
   bool f = false, l = false;
   m.seq = 0;
   const uint32_t t = t0 + lane;
-  if (lane < kTok && t < (uint32_t)p.tokens) {
+  if (lane < TOK && t < (uint32_t)p.tokens) {
     if (p.cu_seqlens) {  // the last sequence that starts at or before t (empty ones start there too)
       int lo = 0, hi = p.num_seqs;
       while (hi - lo > 1) {
@@ -336,6 +345,12 @@ __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int
                                            int lane, float (&in)[2]) {
   const int at = q.in_group(), n = at - w * kPart;  // maps to join (at most kPart)
   bool ok = true;
+  // (the carry of a group begun long ago is there by now, or looked at again below)
+  const bool behind = q.step >= kGroup && GDR_IN_BOUNDS(q.group() <= p.groups && c < p.pitch);
+  const uint64_t *carry = p.carry + ((int64_t)q.group() - 1) * p.pitch + c;
+  Words u;
+  u.u[0] = u.u[1] = 0;
+  if (behind) load_words<PAIRS>(carry, u);
   if (n > 0 && GDR_IN_BOUNDS(q.step < p.tiles && c < p.pitch)) {
     const uint64_t *from = p.tile_map + (int64_t)(q.step - n) * p.pitch + c;
     Words t[kPart];
@@ -372,16 +387,13 @@ __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int
       closed |= part[k].A[0] > 0.f;
     }
   in[0] = in[1] = 0.f;
-  if (q.step >= kGroup && !closed && GDR_IN_BOUNDS(q.group() <= p.groups && c < p.pitch)) {
-    const uint64_t *carry = p.carry + ((int64_t)q.group() - 1) * p.pitch + c;
-    Words u;
-    for (uint32_t poll = 0;; ++poll) {
-      load_words<PAIRS>(carry, u);
-      if (__all_sync(0xffffffffu, u.here())) break;
+  if (behind && !closed) {
+    for (uint32_t poll = 0; !__all_sync(0xffffffffu, u.here()); ++poll) {
       if (give_up(p, poll)) {
         ok = false;  // the block finds out at its next barrier
         break;
       }
+      load_words<PAIRS>(carry, u);
     }
     const Map2 m = u.map();
     in[0] = m.H[0];
@@ -437,41 +449,48 @@ __device__ __forceinline__ void pass_empty(const GlrArgs &p, const float *src, f
 // the path without marks).
 __device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
   if (p.cu_seqlens) return __ldg(p.tile_marks + tile) != 0;
-  const uint32_t t = tile * kTile, r = t % (uint32_t)p.T;
-  return r == 0 || r + kTile >= (uint32_t)p.T;
+  const uint32_t t = tile * p.tile_tokens, r = t % (uint32_t)p.T;
+  return r == 0 || r + p.tile_tokens >= (uint32_t)p.T;
 }
 
 // ---- the kernels --------------------------------------------------------
-// Persistent blocks of four warps, 16 tokens and 64 channels a warp.  Each warp
-// copies its own rows to shared memory (a tensor-map copy a tensor, or lane by
-// lane where rows are not aligned) and waits for them alone.
-template <typename IO> struct WarpRows {
-  float g[kTok][kWide];
-  IO x[kTok][kWide];
+// Persistent blocks of four warps; a tile is TOK tokens a warp and 64 channels.
+// Each warp copies its own rows to shared memory (a tensor-map copy a tensor, or
+// lane by lane where rows are not aligned) and waits for them alone.  In the
+// first pass over a tile its rows go to registers, so that the next tile's
+// copies run while this one waits for what enters it and is written: one read
+// of each input.  What an SM moves is what its blocks hold (registers and the
+// copies under way) over the time a tile takes, two or three L2 round trips.
+//
+// A tile in which a sequence begins or ends takes rolled loops instead, over the
+// rows in shared memory, and its block's next copies begin after it.
+template <typename IO, int TOK> struct WarpRows {
+  float g[TOK][kWide];
+  IO x[TOK][kWide];
 };
-template <typename IO> struct WarpRowsBwd : WarpRows<IO> {
-  IO dh[kTok][kWide];
+template <typename IO, int TOK> struct WarpRowsBwd : WarpRows<IO, TOK> {
+  IO dh[TOK][kWide];
 };
 struct GlrMaps {
   CUtensorMap x, g, dh;
 };
 
 // Tokens of a warp that exist.
-__device__ __forceinline__ int tokens_of(const GlrArgs &p, uint32_t t0) {
+template <int TOK> __device__ __forceinline__ int tokens_of(const GlrArgs &p, uint32_t t0) {
   const int64_t left = p.tokens - (int64_t)t0;
-  return left <= 0 ? 0 : left < kTok ? (int)left : kTok;
+  return left <= 0 ? 0 : left < TOK ? (int)left : TOK;
 }
 
 // Lane copies of one tensor's rows; zeros where nothing is.
-template <typename IO>
-__device__ __forceinline__ void copy_rows(const GlrArgs &p, IO (&to)[kTok][kWide], const void *from, int64_t ld,
+template <typename IO, int TOK>
+__device__ __forceinline__ void copy_rows(const GlrArgs &p, IO (&to)[TOK][kWide], const void *from, int64_t ld,
                                           uint32_t t0, const Lane<false> &l, int lane) {
   const IO *src = static_cast<const IO *>(from);
-  const int n = tokens_of(p, t0);
+  const int n = tokens_of<TOK>(p, t0);
   int64_t off = (int64_t)t0 * ld + l.c;
   if constexpr (sizeof(IO) == 4) {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i, off += ld)
+    for (int i = 0; i < TOK; ++i, off += ld)
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const bool ok = i < n && l.on[v] && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens && l.c + 32 * v < p.D);
@@ -479,26 +498,26 @@ __device__ __forceinline__ void copy_rows(const GlrArgs &p, IO (&to)[kTok][kWide
                      "l"(ok ? src + off + 32 * v : src), "r"(ok ? 4 : 0) : "memory");
       }
   } else {  // a single bf16 is too short for an asynchronous copy
-    IO t[kTok][2];
+    IO t[TOK][2];
 #pragma unroll
-    for (int i = 0; i < kTok; ++i, off += ld)
+    for (int i = 0; i < TOK; ++i, off += ld)
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const bool ok = i < n && l.on[v] && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens && l.c + 32 * v < p.D);
         t[i][v] = ok ? __ldg(src + off + 32 * v) : __float2bfloat16_rn(0.f);
       }
 #pragma unroll
-    for (int i = 0; i < kTok; ++i)
+    for (int i = 0; i < TOK; ++i)
 #pragma unroll
       for (int v = 0; v < 2; ++v) to[i][lane + 32 * v] = t[i][v];
   }
 }
 
 // Begins the copies of a warp's rows of a tile.
-template <typename IO, bool PAIRS, bool BWD, typename ROWS>
+template <typename IO, bool PAIRS, bool BWD, int TOK, typename ROWS>
 __device__ __forceinline__ void begin_copies(const GlrArgs &p, const GlrMaps &maps, ROWS &rows, uint64_t *full,
                                              const Place &q, int w, int lane) {
-  const uint32_t t0 = q.tile * kTile + w * kTok;
+  const uint32_t t0 = q.tile * (kWarps * TOK) + w * TOK;
   if constexpr (PAIRS) {
     __syncwarp();  // the rows have been read by every lane
     if (lane == 0) {
@@ -510,9 +529,9 @@ __device__ __forceinline__ void begin_copies(const GlrArgs &p, const GlrMaps &ma
     }
   } else {
     const Lane<false> l(q.stripe, p.D);
-    copy_rows<float>(p, rows.g, p.g, p.ld_g, t0, l, lane);
-    copy_rows<IO>(p, rows.x, p.x, p.ld_x, t0, l, lane);
-    if constexpr (BWD) copy_rows<IO>(p, rows.dh, p.dh, p.ld_dh, t0, l, lane);
+    copy_rows<float, TOK>(p, rows.g, p.g, p.ld_g, t0, l, lane);
+    copy_rows<IO, TOK>(p, rows.x, p.x, p.ld_x, t0, l, lane);
+    if constexpr (BWD) copy_rows<IO, TOK>(p, rows.dh, p.dh, p.ld_dh, t0, l, lane);
   }
 }
 template <bool PAIRS>
@@ -526,17 +545,32 @@ __device__ __forceinline__ void init_barriers(TileShared &sh) {
   tc::mbar_fence_init();
 }
 
-// Forward.  A tile's decays and inputs go to registers in the first pass over
-// it, so the next tile's copies run while this one waits for what enters it and
-// is written.  STATES_ONLY: only the saved chunk states are written.
+// Tokens a warp, and blocks an SM by their registers.  The chain and the barriers
+// cost about as much for a long tile as for a short one, so a tile is as long as
+// the registers allow: forward in bf16, 32 tokens a warp (a and the packed x in
+// 96 registers, three blocks) against 16 (four blocks).
+template <typename IO, bool PAIRS, bool COMPLEMENT> struct FwdShape {
+  static constexpr bool kLong = PAIRS && sizeof(IO) == 2 && !COMPLEMENT;
+  static constexpr int kTok = kLong ? 32 : 16, kBlocks = kLong ? 3 : 4;
+};
+// Backward: in bf16 x and dh go to registers as well; else (x and dh too wide, or
+// g needed again) they are read from shared memory in both passes, and the next
+// copies begin after the second.
+template <typename IO, bool COMPLEMENT> struct BwdShape {
+  static constexpr bool kEarly = sizeof(IO) == 2 && !COMPLEMENT;
+  static constexpr int kTok = 16, kBlocks = kEarly ? 3 : 4;
+};
+
+// Forward.  STATES_ONLY: only the saved chunk states are written.
 template <typename IO, bool PAIRS, bool COMPLEMENT, bool STATES_ONLY>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, (FwdShape<IO, PAIRS, COMPLEMENT>::kBlocks))
 glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
+  constexpr int TOK = FwdShape<IO, PAIRS, COMPLEMENT>::kTok;
   __shared__ TileShared sh;
   extern __shared__ __align__(128) unsigned char tile_bytes[];
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  auto &rows = reinterpret_cast<WarpRows<IO> *>(tile_bytes)[w];
+  auto &rows = reinterpret_cast<WarpRows<IO, TOK> *>(tile_bytes)[w];
   uint32_t ticket = 0, parity = 0;
   init_barriers(sh);
   if (threadIdx.x == 0) ticket = next_ticket(p, sh, blockIdx.x - gridDim.x);
@@ -544,55 +578,59 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
   Place q = taken<false>(p, sh);
   if (q.step >= p.tiles) return;
   __syncthreads();
-  begin_copies<IO, PAIRS, false>(p, maps, rows, &sh.full[w], q, w, lane);
+  begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], q, w, lane);
   bool marked = has_marks(p, q.tile), alive = true;
   while (true) {
     if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
     Lane<PAIRS> l(q.stripe, p.D);
-    const uint32_t t0 = q.tile * kTile + w * kTok;
+    const uint32_t t0 = q.tile * (kWarps * TOK) + w * TOK;
     Marks m;
     m.first = m.last = 0;
     m.seq = 0;
-    if (marked) m = find_marks(p, t0, lane);
+    if (marked) m = find_marks<TOK>(p, t0, lane);
     alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
     const int buf = parity;
     parity ^= 1;
-    // the span's map; b of a token is x, or (1 - a) x
-    float a[kTok][2], b[COMPLEMENT ? kTok : 1][2], gs[2] = {0.f, 0.f}, h[2] = {0.f, 0.f};
-    Raw<IO> x[COMPLEMENT ? 1 : kTok];
+    // the map of the warp's tokens; b of a token is x, or (1 - a) x
+    float a[TOK][2], b[COMPLEMENT ? TOK : 1][2], gs[2] = {0.f, 0.f}, h[2] = {0.f, 0.f};
+    Raw<IO> x[COMPLEMENT ? 1 : TOK];
     auto b_of = [&](int i, int v) { return COMPLEMENT ? b[COMPLEMENT ? i : 0][v] : x[COMPLEMENT ? 0 : i].at(v); };
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
+    auto rolled = [&](int i) {  // the state h after token i, from shared memory
       const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
       const Raw<IO> xi = read_row<PAIRS>(rows.x[i], lane);
-      if (!COMPLEMENT) x[COMPLEMENT ? 0 : i] = xi;
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        a[i][v] = decay<IO>(g.at(v));
-        if (COMPLEMENT) b[COMPLEMENT ? i : 0][v] = fresh<IO>(g.at(v), a[i][v]) * xi.at(v);
+        const float ai = decay<IO>(g.at(v));
+        h[v] = fmaf(ai, h[v], COMPLEMENT ? fresh<IO>(g.at(v), ai) * xi.at(v) : xi.at(v));
         gs[v] += g.at(v);
       }
-    }
-    if (m.first == 0) {
+    };
+    if (!marked) {
 #pragma unroll
-      for (int i = 0; i < kTok; ++i)
+      for (int i = 0; i < TOK; ++i) {
+        const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+        const Raw<IO> xi = read_row<PAIRS>(rows.x[i], lane);
+        if (!COMPLEMENT) x[COMPLEMENT ? 0 : i] = xi;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          a[i][v] = decay<IO>(g.at(v));
+          if (COMPLEMENT) b[COMPLEMENT ? i : 0][v] = fresh<IO>(g.at(v), a[i][v]) * xi.at(v);
+          gs[v] += g.at(v);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < TOK; ++i)
 #pragma unroll
         for (int v = 0; v < 2; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
     } else {
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (m.first >> i & 1) {
-          // A start's state takes the place of its a: the initial state is read
-          // once, before the map is published (the sequence's last tile may
-          // write the final state over it as soon as that is done).
-          float h0[2];
-          initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, h0);
-#pragma unroll
-          for (int v = 0; v < 2; ++v) h[v] = a[i][v] = fmaf(a[i][v], h0[v], b_of(i, v));
-        } else {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
-        }
+      // The state after a start takes the place of its g: the initial state is
+      // read once, before the map is published (the sequence's last tile may
+      // write the final state over it as soon as that is done).
+      for (int i = 0; i < TOK; ++i) {
+        const bool start = m.first >> i & 1;
+        if (start) initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, h);
+        rolled(i);
+        if (start) write_row<PAIRS>(rows.g[i], lane, h);
       }
     }
     sh.map[buf][w][lane] = {{m.first ? kClosed : -expf(gs[0]), m.first ? kClosed : -expf(gs[1])}, {h[0], h[1]}};
@@ -600,38 +638,40 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     if (p.chained && w == kWarps - 1 && q.in_group() != kGroup - 1) publish_tile<PAIRS, false>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<false>(p, sh);
     const bool more = nq.step < p.tiles;
-    if (more) {
-      begin_copies<IO, PAIRS, false>(p, maps, rows, &sh.full[w], nq, w, lane);
-      marked = has_marks(p, nq.tile);
-    }
-    float in[2] = {0.f, 0.f};
+    if (more && !marked) begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    const bool next_marked = more && has_marks(p, nq.tile);
+    h[0] = h[1] = 0.f;
     if (p.chained) {
-      alive = enter_tile<PAIRS, false>(p, sh, buf, q, l.c, w, lane, in);
+      alive = enter_tile<PAIRS, false>(p, sh, buf, q, l.c, w, lane, h);
       if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced
     }
-    if (w == 0 && l.any() && p.chunk_states && GDR_IN_BOUNDS(q.tile < p.tiles))
-      store2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, in);
-    h[0] = in[0]; h[1] = in[1];
     enter_warp<false>(sh.map[buf], w, lane, h);
+    // (a chunk of 64 tokens begins with every warp of 64, 32 or 16 tokens that divides it)
+    if (p.chunk_states && t0 % kGlrChunk == 0 && l.any() && t0 < p.tokens && GDR_IN_BOUNDS(t0 / kGlrChunk < p.chunks))
+      store2<PAIRS>(p.chunk_states + (int64_t)(t0 / kGlrChunk) * p.D, l, h);
     if (!STATES_ONLY) {
       IO *out = static_cast<IO *>(p.h) + (int64_t)t0 * p.D;
-      const int n = l.any() ? tokens_of(p, t0) : 0;
-      if ((m.first | m.last) == 0) {
+      const int n = l.any() ? tokens_of<TOK>(p, t0) : 0;
+      if (!marked) {
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) {
+        for (int i = 0; i < TOK; ++i) {
 #pragma unroll
           for (int v = 0; v < 2; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
           if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) store2<PAIRS>(out + (int64_t)i * p.D, l, h);
         }
       } else {
-#pragma unroll
-        for (int i = 0; i < kTok; ++i) {
-          const int s = __shfl_sync(0xffffffffu, m.seq, i);
-#pragma unroll
-          for (int v = 0; v < 2; ++v) h[v] = m.first >> i & 1 ? a[i][v] : fmaf(a[i][v], h[v], b_of(i, v));
+        for (int i = 0; i < TOK; ++i) {
+          if (m.first >> i & 1) {
+            const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+            h[0] = g.at(0);
+            h[1] = g.at(1);
+          } else {
+            rolled(i);
+          }
           if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) store2<PAIRS>(out + (int64_t)i * p.D, l, h);
+          const int s = __shfl_sync(0xffffffffu, m.seq, i);
           if ((m.last >> i & 1) && p.final_state) {
             const int64_t r = state_row(p, s);
             if (l.any() && r >= 0 && GDR_IN_BOUNDS(s < p.num_seqs && r < p.num_slots))
@@ -642,25 +682,26 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
       if (q.tile == 0) pass_empty(p, p.initial_state, p.final_state, true, q.stripe * kWide, kWide);
     }
     if (!more) return;
+    if (marked) begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    marked = next_marked;
     q = nq;
   }
 }
 
 // Backward: the states again from what enters the tile (saved), the gradients
-// from what enters it from the tokens after it (chained).  EARLY: x and dh go to
-// registers too, and the next tile's copies run while this one waits; else (x
-// and dh too wide, or g needed again) the rows stay in shared memory until the
-// second pass has read them.
+// from what enters it from the tokens after it (chained).
 template <typename IO, bool PAIRS, bool COMPLEMENT>
-__global__ void __launch_bounds__(kThreads, sizeof(IO) == 2 && !COMPLEMENT ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, (BwdShape<IO, COMPLEMENT>::kBlocks))
 glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
-  constexpr bool EARLY = sizeof(IO) == 2 && !COMPLEMENT;
+  constexpr bool EARLY = BwdShape<IO, COMPLEMENT>::kEarly;
+  constexpr int TOK = BwdShape<IO, COMPLEMENT>::kTok;
+  static_assert(kWarps * TOK == kGlrChunk, "a tile is a chunk: its saved state enters it");
   __shared__ TileShared sh;
   __shared__ Map2 states[kWarps][32];  // the warps' maps of the states
   extern __shared__ __align__(128) unsigned char tile_bytes[];
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  auto &rows = reinterpret_cast<WarpRowsBwd<IO> *>(tile_bytes)[w];
+  auto &rows = reinterpret_cast<WarpRowsBwd<IO, TOK> *>(tile_bytes)[w];
   uint32_t ticket = 0, parity = 0;
   init_barriers(sh);
   if (threadIdx.x == 0) ticket = next_ticket(p, sh, blockIdx.x - gridDim.x);
@@ -668,72 +709,90 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
   Place q = taken<true>(p, sh);
   if (q.step >= p.tiles) return;
   __syncthreads();
-  begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], q, w, lane);
+  begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], q, w, lane);
   bool marked = has_marks(p, q.tile), alive = true;
   while (true) {
     if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
     Lane<PAIRS> l(q.stripe, p.D);
-    const uint32_t t0 = q.tile * kTile + w * kTok;
+    const uint32_t t0 = q.tile * (kWarps * TOK) + w * TOK;
     float h[2] = {0.f, 0.f}, s[2] = {0.f, 0.f}, r[2] = {0.f, 0.f}, gs[2] = {0.f, 0.f};
-    if (l.any() && GDR_IN_BOUNDS(q.tile < p.tiles)) load2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, h);
+    if (l.any() && GDR_IN_BOUNDS(q.tile < p.chunks)) load2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, h);
     Marks m;
     m.first = m.last = 0;
     m.seq = 0;
-    if (marked) m = find_marks(p, t0, lane);
-    const bool plain = (m.first | m.last) == 0;
+    if (marked) m = find_marks<TOK>(p, t0, lane);
     alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
     const int buf = parity;
     parity ^= 1;
-    float a[kTok][2];
-    Raw<IO> xk[EARLY ? kTok : 1], dk[EARLY ? kTok : 1];
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
-      if (EARLY) {
-        xk[EARLY ? i : 0] = read_row<PAIRS>(rows.x[i], lane);
-        dk[EARLY ? i : 0] = read_row<PAIRS>(rows.dh[i], lane);
-      }
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        a[i][v] = decay<IO>(g.at(v));
-        gs[v] += g.at(v);
-      }
-    }
+    float a[TOK][2];
+    Raw<IO> xk[EARLY ? TOK : 1], dk[EARLY ? TOK : 1];
     auto x_of = [&](int i) { return EARLY ? xk[EARLY ? i : 0] : read_row<PAIRS>(rows.x[i], lane); };
     auto d_of = [&](int i) { return EARLY ? dk[EARLY ? i : 0] : read_row<PAIRS>(rows.dh[i], lane); };
-    // 1 - a of a token; the state y after token i; the gradient that a sequence's end brings
     auto fresh_of = [&](int i, int v) { return fresh<IO>(read_row<PAIRS>(rows.g[i], lane).at(v), a[i][v]); };
-    auto advance = [&](int i, float (&y)[2]) {
+    auto advance = [&](int i, float (&y)[2]) {  // the state y after token i
       const Raw<IO> x = x_of(i);
 #pragma unroll
       for (int v = 0; v < 2; ++v) y[v] = fmaf(a[i][v], y[v], COMPLEMENT ? fresh_of(i, v) * x.at(v) : x.at(v));
     };
+    // the same for the rolled loops, from shared memory; their a and 1 - a of a token
     auto start = [&](int i, float (&y)[2]) { initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, y); };
-    auto end_gradient = [&](int i, float (&y)[2]) {
+    auto rolled_decay = [&](int i, float (&ai)[2], float (&ui)[2]) {
+      const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        ai[v] = decay<IO>(g.at(v));
+        ui[v] = COMPLEMENT ? fresh<IO>(g.at(v), ai[v]) : 1.f;
+      }
+    };
+    auto rolled = [&](int i, float (&y)[2]) {
+      float ai[2], ui[2];
+      rolled_decay(i, ai, ui);
+      const Raw<IO> x = read_row<PAIRS>(rows.x[i], lane);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) y[v] = fmaf(ai[v], y[v], COMPLEMENT ? ui[v] * x.at(v) : x.at(v));
+    };
+    auto end_gradient = [&](int i, float (&y)[2]) {  // what the end of a sequence brings
       const int sq = __shfl_sync(0xffffffffu, m.seq, i);
       y[0] = y[1] = 0.f;
       if (p.dfinal && l.any() && GDR_IN_BOUNDS(sq < p.num_seqs)) load2<PAIRS>(p.dfinal + (int64_t)sq * p.D, l, y);
     };
-    auto back = [&](int i) {
-      const Raw<IO> d = d_of(i);
+    if (!marked) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) r[v] = a[i][v] * (d.at(v) + r[v]);
-    };
-    if (plain) {
+      for (int i = 0; i < TOK; ++i) {
+        const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+        if (EARLY) {
+          xk[EARLY ? i : 0] = read_row<PAIRS>(rows.x[i], lane);
+          dk[EARLY ? i : 0] = read_row<PAIRS>(rows.dh[i], lane);
+        }
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) advance(i, s);
-#pragma unroll
-      for (int i = kTok - 1; i >= 0; --i) back(i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (m.first >> i & 1) start(i, s);
-        advance(i, s);
+        for (int v = 0; v < 2; ++v) {
+          a[i][v] = decay<IO>(g.at(v));
+          gs[v] += g.at(v);
+        }
       }
 #pragma unroll
-      for (int i = kTok - 1; i >= 0; --i) {
+      for (int i = 0; i < TOK; ++i) advance(i, s);
+#pragma unroll
+      for (int i = TOK - 1; i >= 0; --i) {
+        const Raw<IO> d = d_of(i);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) r[v] = a[i][v] * (d.at(v) + r[v]);
+      }
+    } else {
+      for (int i = 0; i < TOK; ++i) {
+        if (m.first >> i & 1) start(i, s);
+        rolled(i, s);
+        const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+        gs[0] += g.at(0);
+        gs[1] += g.at(1);
+      }
+      for (int i = TOK - 1; i >= 0; --i) {
         if (m.last >> i & 1) end_gradient(i, r);
-        back(i);
+        float ai[2], ui[2];
+        rolled_decay(i, ai, ui);
+        const Raw<IO> d = read_row<PAIRS>(rows.dh[i], lane);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) r[v] = ai[v] * (d.at(v) + r[v]);
       }
     }
     {
@@ -745,10 +804,8 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     if (p.chained && w == 0 && q.in_group() != kGroup - 1) publish_tile<PAIRS, true>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<true>(p, sh);
     const bool more = nq.step < p.tiles;
-    if (more) {
-      if (EARLY) begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], nq, w, lane);
-      marked = has_marks(p, nq.tile);
-    }
+    if (EARLY && more && !marked) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    const bool next_marked = more && has_marks(p, nq.tile);
     enter_warp<false>(states, w, lane, h);
     r[0] = r[1] = 0.f;
     if (p.chained) {
@@ -758,55 +815,66 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
       __syncthreads();  // the next ticket is read before it is replaced
     }
     enter_warp<true>(sh.map[buf], w, lane, r);
-    float before[kTok][2];  // h_{t-1}, less x_t for the complement
-    auto keep = [&](int i) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v) before[i][v] = COMPLEMENT ? h[v] - x_of(i).at(v) : h[v];
-      if (i < kTok - 1) advance(i, h);
-    };
     IO *dx0 = static_cast<IO *>(p.dx) + (int64_t)t0 * p.D;
     float *dg0 = p.dg + (int64_t)t0 * p.D;
-    const int n = l.any() ? tokens_of(p, t0) : 0;
-    auto write = [&](int i) {
+    const int n = l.any() ? tokens_of<TOK>(p, t0) : 0;
+    // from the carry r: dx, dg and the carry of the token before; `u` is 1 - a,
+    // `past` h_{t-1}, less x_t for the complement
+    auto write = [&](int i, const Raw<IO> &d, const float (&ai)[2], const float (&u)[2], const float (&past)[2]) {
       float dx[2], dg[2];
-      const Raw<IO> d = d_of(i);
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const float dt = d.at(v) + r[v];
-        r[v] = a[i][v] * dt;
-        dx[v] = COMPLEMENT ? fresh_of(i, v) * dt : dt;
-        dg[v] = r[v] * before[i][v];
+        r[v] = ai[v] * dt;
+        dx[v] = COMPLEMENT ? u[v] * dt : dt;
+        dg[v] = r[v] * past[v];
       }
       if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) {
         store2<PAIRS>(dx0 + (int64_t)i * p.D, l, dx);
         store2<PAIRS>(dg0 + (int64_t)i * p.D, l, dg);
       }
     };
-    if (plain) {
+    if (!marked) {
+      float past[TOK][2];
 #pragma unroll
-      for (int i = 0; i < kTok; ++i) keep(i);
+      for (int i = 0; i < TOK; ++i) {
 #pragma unroll
-      for (int i = kTok - 1; i >= 0; --i) write(i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (m.first >> i & 1) start(i, h);
-        keep(i);
+        for (int v = 0; v < 2; ++v) past[i][v] = COMPLEMENT ? h[v] - x_of(i).at(v) : h[v];
+        if (i < TOK - 1) advance(i, h);
       }
 #pragma unroll
-      for (int i = kTok - 1; i >= 0; --i) {
-        if (m.last >> i & 1) end_gradient(i, r);
-        write(i);
-        if (p.dinitial && (m.first >> i & 1)) {
-          const int sq = __shfl_sync(0xffffffffu, m.seq, i);
-          if (l.any() && GDR_IN_BOUNDS(sq < p.num_seqs)) store2<PAIRS>(p.dinitial + (int64_t)sq * p.D, l, r);
+      for (int i = TOK - 1; i >= 0; --i) {
+        float u[2] = {1.f, 1.f};
+        if (COMPLEMENT) {
+          u[0] = fresh_of(i, 0);
+          u[1] = fresh_of(i, 1);
         }
+        write(i, d_of(i), a[i], u, past[i]);
+      }
+    } else {
+      float past[TOK][2];  // (indexed by a running i: local memory)
+      for (int i = 0; i < TOK; ++i) {
+        if (m.first >> i & 1) start(i, h);
+        const Raw<IO> x = read_row<PAIRS>(rows.x[i], lane);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) past[i][v] = COMPLEMENT ? h[v] - x.at(v) : h[v];
+        rolled(i, h);
+      }
+      for (int i = TOK - 1; i >= 0; --i) {
+        if (m.last >> i & 1) end_gradient(i, r);
+        float ai[2], ui[2];
+        rolled_decay(i, ai, ui);
+        write(i, read_row<PAIRS>(rows.dh[i], lane), ai, ui, past[i]);
+        const int sq = __shfl_sync(0xffffffffu, m.seq, i);
+        if (p.dinitial && (m.first >> i & 1) && l.any() && GDR_IN_BOUNDS(sq < p.num_seqs))
+          store2<PAIRS>(p.dinitial + (int64_t)sq * p.D, l, r);
       }
     }
     if (q.tile == 0) pass_empty(p, p.dfinal, p.dinitial, false, q.stripe * kWide, kWide);
     if (!more) return;
+    if (!EARLY || marked) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    marked = next_marked;
     q = nq;
-    if (!EARLY) begin_copies<IO, PAIRS, true>(p, maps, rows, &sh.full[w], q, w, lane);
   }
 }
 
@@ -833,14 +901,14 @@ __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words
     reinterpret_cast<uint4 *>(p.tile_map)[i] = make_uint4(0, 0, 0, 0);
   if (p.cu_seqlens && p.num_seqs > 0)
     for (int64_t tile = at; tile < p.tiles; tile += step) {
-      const int64_t t = tile * kTile;
+      const int64_t t = tile * p.tile_tokens;
       int lo = 0, hi = p.num_seqs;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.cu_seqlens[mid] <= t) lo = mid;
         else hi = mid;
       }
-      p.tile_marks[tile] = p.cu_seqlens[lo] == t || p.cu_seqlens[lo + 1] <= t + kTile;
+      p.tile_marks[tile] = p.cu_seqlens[lo] == t || p.cu_seqlens[lo + 1] <= t + p.tile_tokens;
     }
 }
 
@@ -933,13 +1001,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A warp's rows of a [tokens, D] tensor: boxes of 16 tokens x 64 channels, zeros outside.
-bool make_map(CUtensorMap *m, const void *base, bool bf16, const GlrArgs &p, int64_t ld) {
+// A warp's rows of a [tokens, D] tensor: boxes of `tok` tokens x 64 channels, zeros outside.
+bool make_map(CUtensorMap *m, const void *base, bool bf16, const GlrArgs &p, int64_t ld, int tok) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t e = bf16 ? 2 : 4;
   cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.tokens}, strides[1] = {(cuuint64_t)ld * e};
-  cuuint32_t box[2] = {kWide, kTok}, estr[2] = {1, 1};
+  cuuint32_t box[2] = {kWide, (cuuint32_t)tok}, estr[2] = {1, 1};
   return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
             const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -961,12 +1029,14 @@ cudaError_t launch_no_tokens(const GlrArgs &p, bool backward, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The stripes of a call, and whether its tiles wait for one another: not where
-// each begins with a sequence's first token.
-GlrArgs with_chain(const GlrArgs &a) {
+// The tiles of a launch with `tok` tokens a warp, and whether they wait for one
+// another: not where each begins with a sequence's first token.
+GlrArgs with_tiles(const GlrArgs &a, int tok) {
   GlrArgs p = a;
+  p.tile_tokens = kWarps * tok;
+  p.tiles = (p.tokens + p.tile_tokens - 1) / p.tile_tokens;
   p.stripes = (p.D + kWide - 1) / kWide;
-  p.chained = p.tiles > 1 && (p.cu_seqlens || p.T > kTile || kTile % p.T != 0);
+  p.chained = p.tiles > 1 && (p.cu_seqlens || p.T > p.tile_tokens || p.tile_tokens % p.T != 0);
   p.groups = (p.tiles + kGroup - 1) / kGroup;
   p.carry = p.tile_map + p.tiles * p.pitch;
   return p;
@@ -1005,37 +1075,40 @@ cudaError_t launch_tiles(const char *name, size_t smem, const GlrArgs &p, const 
   return cudaGetLastError();
 }
 
-template <typename IO, bool PAIRS, bool COMPLEMENT>
-cudaError_t launch_fwd(const GlrArgs &a, cudaStream_t s) {
-  const GlrArgs p = with_chain(a);
+template <typename IO, bool PAIRS, bool COMPLEMENT, bool STATES_ONLY>
+cudaError_t launch_scan(const GlrArgs &a, cudaStream_t s) {
+  constexpr int TOK = FwdShape<IO, PAIRS, COMPLEMENT>::kTok;
+  const GlrArgs p = with_tiles(a, TOK);
   cudaError_t e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, false, s);
   GlrMaps maps;
-  if (PAIRS && !(make_map(&maps.x, p.x, p.bf16, p, p.ld_x) && make_map(&maps.g, p.g, false, p, p.ld_g)))
+  if (PAIRS && !(make_map(&maps.x, p.x, p.bf16, p, p.ld_x, TOK) && make_map(&maps.g, p.g, false, p, p.ld_g, TOK)))
     return cudaErrorInvalidValue;
-  return launch_tiles<glr_scan_kernel<IO, PAIRS, COMPLEMENT, false>>("glr_scan_kernel", kWarps * sizeof(WarpRows<IO>),
-                                                                    p, maps, s);
+  return launch_tiles<glr_scan_kernel<IO, PAIRS, COMPLEMENT, STATES_ONLY>>(
+      "glr_scan_kernel", kWarps * sizeof(WarpRows<IO, TOK>), p, maps, s);
+}
+
+template <typename IO, bool PAIRS, bool COMPLEMENT>
+cudaError_t launch_fwd(const GlrArgs &a, cudaStream_t s) {
+  return launch_scan<IO, PAIRS, COMPLEMENT, false>(a, s);
 }
 
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 cudaError_t launch_bwd(const GlrArgs &a, cudaStream_t s) {
-  const GlrArgs p = with_chain(a);
-  cudaError_t e = launch_begin(p, s);
+  constexpr int TOK = BwdShape<IO, COMPLEMENT>::kTok;
+  const GlrArgs p = with_tiles(a, TOK);
+  cudaError_t e = cudaSuccess;
+  if (p.own_chunks && p.tiles > 0) e = launch_scan<IO, PAIRS, COMPLEMENT, true>(a, s);
+  if (e == cudaSuccess) e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, true, s);
   GlrMaps maps;
-  if (PAIRS && !(make_map(&maps.x, p.x, p.bf16, p, p.ld_x) && make_map(&maps.g, p.g, false, p, p.ld_g) &&
-                 make_map(&maps.dh, p.dh, p.bf16, p, p.ld_dh)))
+  if (PAIRS && !(make_map(&maps.x, p.x, p.bf16, p, p.ld_x, TOK) && make_map(&maps.g, p.g, false, p, p.ld_g, TOK) &&
+                 make_map(&maps.dh, p.dh, p.bf16, p, p.ld_dh, TOK)))
     return cudaErrorInvalidValue;
-  if (p.own_chunks) {
-    e = launch_tiles<glr_scan_kernel<IO, PAIRS, COMPLEMENT, true>>("glr_scan_kernel", kWarps * sizeof(WarpRows<IO>), p,
-                                                                  maps, s);
-    if (e == cudaSuccess) e = launch_begin(p, s);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_tiles<glr_gradient_kernel<IO, PAIRS, COMPLEMENT>>("glr_gradient_kernel",
-                                                                 kWarps * sizeof(WarpRowsBwd<IO>), p, maps, s);
+  return launch_tiles<glr_gradient_kernel<IO, PAIRS, COMPLEMENT>>(
+      "glr_gradient_kernel", kWarps * sizeof(WarpRowsBwd<IO, TOK>), p, maps, s);
 }
 
 template <typename IO, bool PAIRS, bool COMPLEMENT>

@@ -99,7 +99,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);
 // Gated linear recurrence over a vector state.  Tokens are numbered along one
 // axis (sequence b of a dense batch begins at b T).
 constexpr int kGlrChunk = 64;         // tokens between two saved states
-constexpr int kGlrShortestGroup = 8;  // tiles of a group of the chain, at least
+constexpr int kGlrShortestGroup = 8;  // tiles of a group of the chain, at least (tiles are a chunk or longer)
 
 struct GlrArgs {
   const void *x;
@@ -110,7 +110,7 @@ struct GlrArgs {
   float *final_state;          // glr_step: the states, updated in place
   const int32_t *state_slots;  // device [num_seqs] pool slots, or nullptr
   int64_t num_slots;
-  float *chunk_states;  // [tiles, D]: the state that enters each chunk
+  float *chunk_states;  // [chunks, D]: the state that enters each chunk
   // backward
   const void *dh;
   int64_t ld_dh;
@@ -119,7 +119,7 @@ struct GlrArgs {
   float *dg, *dinitial;
   const int32_t *cu_seqlens;  // device [num_seqs + 1], or nullptr (dense)
   int num_seqs, T, D;
-  int64_t tokens, tiles;
+  int64_t tokens, chunks;
   bool complement, bf16;
   // workspace
   int32_t *status;
@@ -130,8 +130,8 @@ struct GlrArgs {
   bool own_chunks;  // backward: chunk_states is workspace, to be filled first
   // set at the launch
   uint64_t *carry;
-  int stripes;
-  int64_t groups;
+  int stripes, tile_tokens;
+  int64_t tiles, groups;
   bool chained;
 };
 
