@@ -47,112 +47,123 @@ template <bool PAIRS> struct Lane {
   __device__ __forceinline__ bool any() const { return on[0]; }
 };
 
+// A lane's two channels.  Plain arithmetic: two chains of dependent product-sums
+// that run side by side; the packed forms, which keep the pair in neighbouring
+// registers, spilled here and were slower (177 against 189 us, 32768 x 4096
+// bf16).  Long independent series (`fresh`) use them.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Two channels of one token as they are stored.
 template <typename IO> struct Raw;
 template <> struct Raw<float> {
-  float r[2];
-  __device__ __forceinline__ float at(int v) const { return r[v]; }
+  float2 r;
+  __device__ __forceinline__ float2 value() const { return r; }
 };
 template <> struct Raw<__nv_bfloat16> {
   uint32_t r;
-  __device__ __forceinline__ float at(int v) const { return v ? bf16_hi(r) : bf16_lo(r); }
+  __device__ __forceinline__ float2 value() const { return make_float2(bf16_lo(r), bf16_hi(r)); }
 };
 
 // Shared memory: a lane's two channels of a row.
 template <bool PAIRS> __device__ __forceinline__ Raw<float> read_row(const float *row, int lane) {
-  Raw<float> x;
-  if constexpr (PAIRS) {
-    const float2 v = reinterpret_cast<const float2 *>(row)[lane];
-    x.r[0] = v.x; x.r[1] = v.y;
-  } else {
-    x.r[0] = row[lane]; x.r[1] = row[lane + 32];
-  }
-  return x;
+  if constexpr (PAIRS) return {reinterpret_cast<const float2 *>(row)[lane]};
+  else return {make_float2(row[lane], row[lane + 32])};
 }
 template <bool PAIRS> __device__ __forceinline__ Raw<__nv_bfloat16> read_row(const __nv_bfloat16 *row, int lane) {
-  Raw<__nv_bfloat16> x;
-  if constexpr (PAIRS) {
-    x.r = reinterpret_cast<const uint32_t *>(row)[lane];
-  } else {
-    const unsigned short *h = reinterpret_cast<const unsigned short *>(row);
-    x.r = (uint32_t)h[lane] | (uint32_t)h[lane + 32] << 16;
-  }
-  return x;
+  if constexpr (PAIRS) return {reinterpret_cast<const uint32_t *>(row)[lane]};
+  const unsigned short *h = reinterpret_cast<const unsigned short *>(row);
+  return {(uint32_t)h[lane] | (uint32_t)h[lane + 32] << 16};
 }
-
-template <bool PAIRS> __device__ __forceinline__ void write_row(float *row, int lane, const float (&x)[2]) {
+template <bool PAIRS> __device__ __forceinline__ void write_row(float *row, int lane, float2 x) {
   if constexpr (PAIRS) {
-    reinterpret_cast<float2 *>(row)[lane] = make_float2(x[0], x[1]);
+    reinterpret_cast<float2 *>(row)[lane] = x;
   } else {
-    row[lane] = x[0]; row[lane + 32] = x[1];
+    row[lane] = x.x; row[lane + 32] = x.y;
   }
 }
 
 // Global memory: plain (coherent) accesses, states are updated in place by some calls.
-template <bool PAIRS> __device__ __forceinline__ void load2(const float *p, const Lane<PAIRS> &l, float (&x)[2]) {
-  if constexpr (PAIRS) {
-    const float2 v = *reinterpret_cast<const float2 *>(p + l.c);
-    x[0] = v.x; x[1] = v.y;
-  } else {
-    x[0] = p[l.c];
-    x[1] = l.on[1] ? p[l.c + 32] : 0.f;
-  }
+template <bool PAIRS> __device__ __forceinline__ float2 load2(const float *p, const Lane<PAIRS> &l) {
+  if constexpr (PAIRS) return *reinterpret_cast<const float2 *>(p + l.c);
+  else return make_float2(p[l.c], l.on[1] ? p[l.c + 32] : 0.f);
 }
-template <bool PAIRS, typename IO> __device__ __forceinline__ void store2(IO *p, const Lane<PAIRS> &l, const float (&x)[2]) {
+template <bool PAIRS, typename IO> __device__ __forceinline__ void store2(IO *p, const Lane<PAIRS> &l, float2 x) {
   if constexpr (!PAIRS) {
-    io<IO>::store(p + l.c, x[0]);
-    if (l.on[1]) io<IO>::store(p + l.c + 32, x[1]);
+    io<IO>::store(p + l.c, x.x);
+    if (l.on[1]) io<IO>::store(p + l.c + 32, x.y);
   } else if constexpr (sizeof(IO) == 4) {
-    *reinterpret_cast<float2 *>(p + l.c) = make_float2(x[0], x[1]);
+    *reinterpret_cast<float2 *>(p + l.c) = x;
   } else {
-    *reinterpret_cast<uint32_t *>(p + l.c) = pack_bf16x2(x[0], x[1]);
+    *reinterpret_cast<uint32_t *>(p + l.c) = pack_bf16x2(x.x, x.y);
   }
 }
 
 // The decay of one token.  With bf16 activations the fast exponential: its error
-// (2^-22 of the value) enters the state of a span of at most 16 tokens only,
+// (2^-22 of the value) enters the state of a span of at most 32 tokens only,
 // the decay of longer spans comes from the sum of their g.
-template <typename IO> __device__ __forceinline__ float decay(float g) {
+template <typename IO> __device__ __forceinline__ float2 decay(float2 g) {
   if constexpr (sizeof(IO) == 2) {
-    float a;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(g * 1.44269504f));  // log2 e
+    const float2 t = mul2(g, both(1.44269504f));  // log2 e
+    float2 a;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a.y) : "f"(t.y));
     return a;
   } else {
-    return expf(g);
+    return make_float2(expf(g.x), expf(g.y));
   }
 }
 // 1 - a of one token: near 0 the series of -expm1(g), whose first term left out
 // is below 2^-22 of the value (bf16 activations) or 2^-28, else the difference,
 // which then loses less than two bits.
-template <typename IO> __device__ __forceinline__ float fresh(float g, float a) {
-  float s = 1.f / 5040.f;
+template <typename IO> __device__ __forceinline__ float2 fresh(float2 g, float2 a) {
+  float2 s = both(1.f / 5040.f);
   if constexpr (sizeof(IO) == 4) {
-    s = 1.f / 362880.f;
-    s = fmaf(s, g, 1.f / 40320.f);
-    s = fmaf(s, g, 1.f / 5040.f);
+    s = both(1.f / 362880.f);
+    s = __ffma2_rn(s, g, both(1.f / 40320.f));
+    s = __ffma2_rn(s, g, both(1.f / 5040.f));
   }
-  s = fmaf(s, g, 1.f / 720.f);
-  s = fmaf(s, g, 1.f / 120.f);
-  s = fmaf(s, g, 1.f / 24.f);
-  s = fmaf(s, g, 1.f / 6.f);
-  s = fmaf(s, g, 0.5f);
-  s = fmaf(s, g, 1.f);
-  return g > -0.5f ? -g * s : 1.f - a;
+  s = __ffma2_rn(s, g, both(1.f / 720.f));
+  s = __ffma2_rn(s, g, both(1.f / 120.f));
+  s = __ffma2_rn(s, g, both(1.f / 24.f));
+  s = __ffma2_rn(s, g, both(1.f / 6.f));
+  s = __ffma2_rn(s, g, both(0.5f));
+  s = __ffma2_rn(s, g, both(1.f));
+  const float2 near = mul2(make_float2(-g.x, -g.y), s), far = fma2(a, both(-1.f), both(1.f));
+  return make_float2(g.x > -0.5f ? near.x : far.x, g.y > -0.5f ? near.y : far.y);
+}
+// What a token adds to the state: x, or (1 - a) x.
+template <typename IO, bool COMPLEMENT> __device__ __forceinline__ float2 input(float2 g, float2 a, float2 x) {
+  if constexpr (COMPLEMENT) return mul2(fresh<IO>(g, a), x);
+  else return x;
+}
+
+// Row of sequence n's state in the states or the pool, or -1 (no slot).
+__device__ __forceinline__ int state_row(const GlrArgs &p, int n) {
+  if (!p.state_slots) return n;
+  const int s = __ldg(p.state_slots + n);
+  return s >= 0 && s < p.num_slots ? s : -1;
 }
 
 // Which of a warp's TOK tokens begin or end a sequence (bit i: token t0 + i), and,
-// in lane i, the sequence of token t0 + i.
+// in lane i where token t0 + i does, the row of that sequence's states (or -1).
 struct Marks {
   uint32_t first, last;
-  int seq;
+  int row;
+  __device__ __forceinline__ int row_of(int i) const { return __shfl_sync(0xffffffffu, row, i); }
 };
 template <int TOK> __device__ __forceinline__ Marks find_marks(const GlrArgs &p, uint32_t t0, int lane) {
   static_assert(TOK <= 32, "a lane a token");
   Marks m;
   bool f = false, l = false;
-  m.seq = 0;
+  m.row = -1;
   const uint32_t t = t0 + lane;
   if (lane < TOK && t < (uint32_t)p.tokens) {
+    int seq;
     if (p.cu_seqlens) {  // the last sequence that starts at or before t (empty ones start there too)
       int lo = 0, hi = p.num_seqs;
       while (hi - lo > 1) {
@@ -160,36 +171,30 @@ template <int TOK> __device__ __forceinline__ Marks find_marks(const GlrArgs &p,
         if ((uint32_t)__ldg(p.cu_seqlens + mid) <= t) lo = mid;
         else hi = mid;
       }
-      m.seq = lo;
+      seq = lo;
       f = (uint32_t)__ldg(p.cu_seqlens + lo) == t;
       l = (uint32_t)__ldg(p.cu_seqlens + lo + 1) == t + 1;
     } else {
-      m.seq = (int)(t / (uint32_t)p.T);
-      const uint32_t r = t - (uint32_t)m.seq * (uint32_t)p.T;
+      seq = (int)(t / (uint32_t)p.T);
+      const uint32_t r = t - (uint32_t)seq * (uint32_t)p.T;
       f = r == 0;
       l = r == (uint32_t)p.T - 1;
     }
+    if ((f || l) && GDR_IN_BOUNDS(seq < p.num_seqs)) m.row = state_row(p, seq);
   }
   m.first = __ballot_sync(0xffffffffu, f);
   m.last = __ballot_sync(0xffffffffu, l);
   return m;
 }
 
-// Row of sequence n's state in the states or the pool, or -1 (no slot).
-__device__ __forceinline__ int64_t state_row(const GlrArgs &p, int n) {
-  if (!p.state_slots) return n;
-  const int64_t s = __ldg(p.state_slots + n);
-  return s >= 0 && s < p.num_slots ? s : -1;
-}
-
-// The initial state of sequence n.
+// Row `r` of a [rows, D] array of states; zeros where there is none.
 template <bool PAIRS>
-__device__ __forceinline__ void initial_of(const GlrArgs &p, int n, const Lane<PAIRS> &l, float (&h0)[2]) {
-  h0[0] = h0[1] = 0.f;
-  if (!p.initial_state) return;
-  const int64_t r = state_row(p, n);
-  if (l.any() && r >= 0 && GDR_IN_BOUNDS(n < p.num_seqs && r < p.num_slots))
-    load2<PAIRS>(p.initial_state + r * p.D, l, h0);
+__device__ __forceinline__ float2 load_row(const GlrArgs &p, const float *states, int r, const Lane<PAIRS> &l) {
+  return states && l.any() && r >= 0 && GDR_IN_BOUNDS(r < p.num_slots) ? load2<PAIRS>(states + (int64_t)r * p.D, l) : both(0.f);
+}
+template <bool PAIRS>
+__device__ __forceinline__ void store_state(const GlrArgs &p, float *states, int r, const Lane<PAIRS> &l, float2 x) {
+  if (states && l.any() && r >= 0 && GDR_IN_BOUNDS(r < p.num_slots)) store2<PAIRS>(states + (int64_t)r * p.D, l, x);
 }
 
 __device__ __forceinline__ bool bad_offsets(const GlrArgs &p) {
@@ -198,35 +203,33 @@ __device__ __forceinline__ bool bad_offsets(const GlrArgs &p) {
 
 // ---- maps of spans ------------------------------------------------------
 // A span of tokens takes what enters it, `in`, to A in + H, or to H where it is
-// closed.  A >= 0 is kept with its sign turned, a closed span as +1 in its place.
-// All channels of a span are closed or none.
+// closed: A = -1 (a decay is never below 0).  All channels of a span are closed
+// or none.
 struct Map2 {  // of a lane's two channels
-  float A[2], H[2];
+  float2 A, H;
+  __device__ __forceinline__ bool closed() const { return A.x < 0.f; }
+  __device__ __forceinline__ float2 of(float2 in) const {
+    const float2 t = fma2(A, in, H);
+    return closed() ? H : t;
+  }
 };
-constexpr float kClosed = 1.f;
-__device__ __forceinline__ float through(float A, float H, float in) { return A > 0.f ? H : fmaf(-A, in, H); }
-__device__ __forceinline__ void through(const Map2 &m, float (&x)[2]) {
-  x[0] = through(m.A[0], m.H[0], x[0]);
-  x[1] = through(m.A[1], m.H[1], x[1]);
-}
-// The map of n spans one after the other (n known where it is unrolled).
+constexpr float kClosed = -1.f;
+// The map of n spans one after the other.
 template <int N> __device__ __forceinline__ Map2 joined(const Map2 (&t)[N]) {
   Map2 m = t[0];
   bool closed = false;
 #pragma unroll
-  for (int j = 0; j < N; ++j) closed |= t[j].A[0] > 0.f;
+  for (int j = 0; j < N; ++j) closed |= t[j].closed();
   if (!closed) {
 #pragma unroll
-    for (int j = 1; j < N; ++j)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        m.H[v] = fmaf(-t[j].A[v], m.H[v], t[j].H[v]);
-        m.A[v] = -(m.A[v] * t[j].A[v]);
-      }
+    for (int j = 1; j < N; ++j) {
+      m.H = fma2(t[j].A, m.H, t[j].H);
+      m.A = mul2(m.A, t[j].A);
+    }
   } else {
 #pragma unroll
-    for (int j = 1; j < N; ++j) through(t[j], m.H);
-    m.A[0] = m.A[1] = kClosed;
+    for (int j = 1; j < N; ++j) m.H = t[j].of(m.H);
+    m.A = both(kClosed);
   }
   return m;
 }
@@ -244,31 +247,32 @@ struct TileShared {
 // Blocks take tiles in order of a ticket, each its own in rising order, so
 // every tile that another waits for is done or in the hands of a block that
 // waits for earlier ones only: the lowest open ticket always proceeds.  In
-// groups of kGroup tiles a tile publishes its map as soon as it has it; what
+// groups of tiles a tile publishes its map as soon as it has it; what
 // enters a tile is what enters its group, through the maps of the group's tiles
 // before it; the last tile of a group publishes what leaves the group.  Which
 // values are joined, and in which order, depends on the sizes alone, never on
 // timing.
 //
-// A channel's map goes through the workspace as one 64-bit word (A above, H
-// below), which is its own flag: 0 is not there yet, and A is never +0.  So a
-// hand-over is one store and one polling load, without a fence.  The rows of
-// words are as wide as the tiles (`pitch`), so every lane has its own.
-constexpr int kGroup = 16, kPart = kGroup / kWarps;
-static_assert(kGroup >= kGlrShortestGroup, "the workspace counts groups of at least this length");
+// A channel's map goes through the workspace as one 64-bit word (A with its sign
+// turned above, H below), which is its own flag: 0 is not there yet, and no map
+// is 0.  So a hand-over is one store and one polling load, without a fence.  The
+// rows of words are as wide as the tiles (`pitch`), so every lane has its own.
+template <int TOK> struct Chain {
+  static constexpr int kGroup = 16, kPart = kGroup / kWarps;
+  static_assert(kGroup >= kGlrShortestGroup, "the workspace counts groups of at least this length");
+};
 constexpr uint32_t kMaxChainPolls = 1u << 20;  // about a second
 
 struct Words {
   uint64_t u[2];
   __device__ __forceinline__ bool here() const { return min((uint32_t)(u[0] >> 32), (uint32_t)(u[1] >> 32)) != 0; }
+  static __device__ __forceinline__ uint64_t pack(float A, float H) {
+    return (uint64_t)(__float_as_uint(A) ^ 0x80000000u) << 32 | __float_as_uint(H);
+  }
+  static __device__ __forceinline__ float A(uint64_t u) { return __uint_as_float((uint32_t)(u >> 32) ^ 0x80000000u); }
+  static __device__ __forceinline__ float H(uint64_t u) { return __uint_as_float((uint32_t)u); }
   __device__ __forceinline__ Map2 map() const {
-    Map2 m;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      m.A[v] = __uint_as_float((uint32_t)(u[v] >> 32));
-      m.H[v] = __uint_as_float((uint32_t)u[v]);
-    }
-    return m;
+    return {make_float2(A(u[0]), A(u[1])), make_float2(H(u[0]), H(u[1]))};
   }
 };
 template <bool PAIRS> __device__ __forceinline__ void load_words(const uint64_t *p, Words &w) {
@@ -280,9 +284,7 @@ template <bool PAIRS> __device__ __forceinline__ void load_words(const uint64_t 
   }
 }
 template <bool PAIRS> __device__ __forceinline__ void store_words(uint64_t *p, const Map2 &m) {
-  uint64_t u[2];
-#pragma unroll
-  for (int v = 0; v < 2; ++v) u[v] = (uint64_t)__float_as_uint(m.A[v]) << 32 | __float_as_uint(m.H[v]);
+  const uint64_t u[2] = {Words::pack(m.A.x, m.H.x), Words::pack(m.A.y, m.H.y)};
   if constexpr (PAIRS) {
     asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(u[0]), "l"(u[1]) : "memory");
   } else {
@@ -295,8 +297,6 @@ template <bool PAIRS> __device__ __forceinline__ void store_words(uint64_t *p, c
 struct Place {
   uint32_t step, tile;
   int stripe;
-  __device__ __forceinline__ int in_group() const { return step % kGroup; }
-  __device__ __forceinline__ uint32_t group() const { return step / kGroup; }
 };
 
 // Takes the block's next tile (one thread).  Without a chain: `grid` tiles on.
@@ -340,14 +340,16 @@ __device__ __forceinline__ void publish_tile(const GlrArgs &p, const TileShared 
 // wait is the serial part of the chain: the tile that ends a group sends on
 // what leaves it at once.  Every thread of the block takes part.  False: a wait
 // gave up.
-template <bool PAIRS, bool REV>
+template <int TOK, bool PAIRS, bool REV>
 __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int buf, const Place &q, int c, int w,
-                                           int lane, float (&in)[2]) {
-  const int at = q.in_group(), n = at - w * kPart;  // maps to join (at most kPart)
+                                           int lane, float2 &in) {
+  constexpr int kGroup = Chain<TOK>::kGroup, kPart = Chain<TOK>::kPart;
+  const uint32_t group = q.step / kGroup;
+  const int at = q.step % kGroup, n = at - w * kPart;  // maps to join (at most kPart)
   bool ok = true;
   // (the carry of a group begun long ago is there by now, or looked at again below)
-  const bool behind = q.step >= kGroup && GDR_IN_BOUNDS(q.group() <= p.groups && c < p.pitch);
-  const uint64_t *carry = p.carry + ((int64_t)q.group() - 1) * p.pitch + c;
+  const bool behind = q.step >= kGroup && GDR_IN_BOUNDS(group <= p.groups && c < p.pitch);
+  const uint64_t *carry = p.carry + ((int64_t)group - 1) * p.pitch + c;
   Words u;
   u.u[0] = u.u[1] = 0;
   if (behind) load_words<PAIRS>(carry, u);
@@ -356,7 +358,7 @@ __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int
     Words t[kPart];
 #pragma unroll
     for (int j = 0; j < kPart; ++j) {
-      t[j].u[0] = t[j].u[1] = (uint64_t)__float_as_uint(-1.f) << 32;  // nothing changes
+      t[j].u[0] = t[j].u[1] = Words::pack(1.f, 0.f);  // nothing changes
       if (j < n) load_words<PAIRS>(from + (int64_t)j * p.pitch, t[j]);
     }
     for (uint32_t poll = 0;; ++poll) {
@@ -384,9 +386,9 @@ __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int
   for (int k = 0; k < kWarps; ++k)
     if (k * kPart < at) {
       part[k] = sh.before[k][lane];
-      closed |= part[k].A[0] > 0.f;
+      closed |= part[k].closed();
     }
-  in[0] = in[1] = 0.f;
+  in = both(0.f);
   if (behind && !closed) {
     for (uint32_t poll = 0; !__all_sync(0xffffffffu, u.here()); ++poll) {
       if (give_up(p, poll)) {
@@ -395,32 +397,27 @@ __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int
       }
       load_words<PAIRS>(carry, u);
     }
-    const Map2 m = u.map();
-    in[0] = m.H[0];
-    in[1] = m.H[1];
+    in = u.map().H;
   }
 #pragma unroll
   for (int k = 0; k < kWarps; ++k)
-    if (k * kPart < at) through(part[k], in);
-  if (ok && at == kGroup - 1 && w == (REV ? 0 : kWarps - 1) && GDR_IN_BOUNDS(q.group() < p.groups && c < p.pitch)) {
-    Map2 out;
-    out.H[0] = in[0];
-    out.H[1] = in[1];
+    if (k * kPart < at) in = part[k].of(in);
+  if (ok && at == kGroup - 1 && w == (REV ? 0 : kWarps - 1) && GDR_IN_BOUNDS(group < p.groups && c < p.pitch)) {
+    Map2 out = {both(kClosed), in};
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) through(sh.map[buf][REV ? kWarps - 1 - k : k][lane], out.H);
-    out.A[0] = out.A[1] = kClosed;
-    store_words<PAIRS>(p.carry + (int64_t)q.group() * p.pitch + c, out);
+    for (int k = 0; k < kWarps; ++k) out.H = sh.map[buf][REV ? kWarps - 1 - k : k][lane].of(out.H);
+    store_words<PAIRS>(p.carry + (int64_t)group * p.pitch + c, out);
   }
   return ok;
 }
 
 // `x`, what enters the tile, becomes what enters warp w.
 template <bool REV>
-__device__ __forceinline__ void enter_warp(const Map2 (&map)[kWarps][32], int w, int lane, float (&x)[2]) {
+__device__ __forceinline__ void enter_warp(const Map2 (&map)[kWarps][32], int w, int lane, float2 &x) {
 #pragma unroll
   for (int k = 0; k < kWarps - 1; ++k) {
     const int j = REV ? kWarps - 1 - k : k;
-    if (REV ? j > w : j < w) through(map[j][lane], x);
+    if (REV ? j > w : j < w) x = map[j][lane].of(x);
   }
 }
 
@@ -485,32 +482,39 @@ template <int TOK> __device__ __forceinline__ int tokens_of(const GlrArgs &p, ui
 template <typename IO, int TOK>
 __device__ __forceinline__ void copy_rows(const GlrArgs &p, IO (&to)[TOK][kWide], const void *from, int64_t ld,
                                           uint32_t t0, const Lane<false> &l, int lane) {
-  const IO *src = static_cast<const IO *>(from);
   const int n = tokens_of<TOK>(p, t0);
-  int64_t off = (int64_t)t0 * ld + l.c;
+  const bool whole = n == TOK && l.c - lane + kWide <= p.D && GDR_IN_BOUNDS((int64_t)t0 + TOK <= p.tokens);
+  const IO *src = static_cast<const IO *>(from) + (int64_t)t0 * ld + l.c;
   if constexpr (sizeof(IO) == 4) {
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < TOK; ++i, off += ld)
+      for (int i = 0; i < TOK; ++i, src += ld)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const bool ok = i < n && l.on[v] && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens && l.c + 32 * v < p.D);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&to[i][lane + 32 * v])),
-                     "l"(ok ? src + off + 32 * v : src), "r"(ok ? 4 : 0) : "memory");
-      }
-  } else {  // a single bf16 is too short for an asynchronous copy
+        for (int v = 0; v < 2; ++v)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(&to[i][lane + 32 * v])),
+                       "l"(src + 32 * v) : "memory");
+      return;
+    }
+  } else if (whole) {  // a single bf16 is too short for an asynchronous copy
     IO t[TOK][2];
 #pragma unroll
-    for (int i = 0; i < TOK; ++i, off += ld)
+    for (int i = 0; i < TOK; ++i, src += ld)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const bool ok = i < n && l.on[v] && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens && l.c + 32 * v < p.D);
-        t[i][v] = ok ? __ldg(src + off + 32 * v) : __float2bfloat16_rn(0.f);
-      }
+      for (int v = 0; v < 2; ++v) t[i][v] = __ldg(src + 32 * v);
 #pragma unroll
     for (int i = 0; i < TOK; ++i)
 #pragma unroll
       for (int v = 0; v < 2; ++v) to[i][lane + 32 * v] = t[i][v];
+    return;
   }
+  for (int i = 0; i < TOK; ++i, src += ld)
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const bool ok = i < n && l.on[v] && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens && l.c + 32 * v < p.D);
+      IO x = IO(0.f);
+      if (ok) x = __ldg(src + 32 * v);
+      to[i][lane + 32 * v] = x;
+    }
 }
 
 // Begins the copies of a warp's rows of a tile.
@@ -547,11 +551,11 @@ __device__ __forceinline__ void init_barriers(TileShared &sh) {
 
 // Tokens a warp, and blocks an SM by their registers.  The chain and the barriers
 // cost about as much for a long tile as for a short one, so a tile is as long as
-// the registers allow: forward in bf16, 32 tokens a warp (a and the packed x in
-// 96 registers, three blocks) against 16 (four blocks).
+// the registers allow: forward in bf16, 32 tokens a warp (a and the packed x in 96
+// registers, three blocks), else 16 (four blocks).
 template <typename IO, bool PAIRS, bool COMPLEMENT> struct FwdShape {
-  static constexpr bool kLong = PAIRS && sizeof(IO) == 2 && !COMPLEMENT;
-  static constexpr int kTok = kLong ? 32 : 16, kBlocks = kLong ? 3 : 4;
+  static constexpr bool kLong = PAIRS && sizeof(IO) == 2;
+  static constexpr int kTok = kLong ? 32 : 16, kBlocks = kLong ? COMPLEMENT ? 2 : 3 : 4;
 };
 // Backward: in bf16 x and dh go to registers as well; else (x and dh too wide, or
 // g needed again) they are read from shared memory in both passes, and the next
@@ -586,69 +590,72 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     const uint32_t t0 = q.tile * (kWarps * TOK) + w * TOK;
     Marks m;
     m.first = m.last = 0;
-    m.seq = 0;
+    m.row = -1;
     if (marked) m = find_marks<TOK>(p, t0, lane);
     alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
     const int buf = parity;
     parity ^= 1;
-    // the map of the warp's tokens; b of a token is x, or (1 - a) x
-    float a[TOK][2], b[COMPLEMENT ? TOK : 1][2], gs[2] = {0.f, 0.f}, h[2] = {0.f, 0.f};
+    // the map of the warp's tokens
+    float2 a[TOK], b[COMPLEMENT ? TOK : 1], gs = both(0.f), h = both(0.f);
     Raw<IO> x[COMPLEMENT ? 1 : TOK];
-    auto b_of = [&](int i, int v) { return COMPLEMENT ? b[COMPLEMENT ? i : 0][v] : x[COMPLEMENT ? 0 : i].at(v); };
-    auto rolled = [&](int i) {  // the state h after token i, from shared memory
-      const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
-      const Raw<IO> xi = read_row<PAIRS>(rows.x[i], lane);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const float ai = decay<IO>(g.at(v));
-        h[v] = fmaf(ai, h[v], COMPLEMENT ? fresh<IO>(g.at(v), ai) * xi.at(v) : xi.at(v));
-        gs[v] += g.at(v);
-      }
+    auto b_of = [&](int i) { return COMPLEMENT ? b[COMPLEMENT ? i : 0] : x[COMPLEMENT ? 0 : i].value(); };
+    auto g_row = [&](int i) { return read_row<PAIRS>(rows.g[i], lane).value(); };
+    auto rolled = [&](int i, float2 g, float2 y) {  // the state after y by token i
+      const float2 ai = decay<IO>(g);
+      return fma2(ai, y, input<IO, COMPLEMENT>(g, ai, read_row<PAIRS>(rows.x[i], lane).value()));
     };
     if (!marked) {
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
-        const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+        const float2 g = g_row(i);
         const Raw<IO> xi = read_row<PAIRS>(rows.x[i], lane);
-        if (!COMPLEMENT) x[COMPLEMENT ? 0 : i] = xi;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          a[i][v] = decay<IO>(g.at(v));
-          if (COMPLEMENT) b[COMPLEMENT ? i : 0][v] = fresh<IO>(g.at(v), a[i][v]) * xi.at(v);
-          gs[v] += g.at(v);
-        }
+        a[i] = decay<IO>(g);
+        if (COMPLEMENT) b[COMPLEMENT ? i : 0] = input<IO, COMPLEMENT>(g, a[i], xi.value());
+        else x[COMPLEMENT ? 0 : i] = xi;
+        gs = add2(gs, g);
       }
 #pragma unroll
-      for (int i = 0; i < TOK; ++i)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+      for (int i = 0; i < TOK; ++i) h = fma2(a[i], h, b_of(i));
     } else {
       // The state after a start takes the place of its g: the initial state is
       // read once, before the map is published (the sequence's last tile may
-      // write the final state over it as soon as that is done).
+      // write the final state over it as soon as that is done).  Four at a time.
+      for (uint32_t todo = m.first; todo;) {
+        int at[4];
+        float2 h0[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          at[k] = __ffs(todo) - 1;
+          todo &= todo - 1;
+          if (at[k] >= 0) h0[k] = load_row<PAIRS>(p, p.initial_state, m.row_of(at[k]), l);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (at[k] >= 0) write_row<PAIRS>(rows.g[at[k]], lane, rolled(at[k], g_row(at[k]), h0[k]));
+      }
+#pragma unroll 4
       for (int i = 0; i < TOK; ++i) {
-        const bool start = m.first >> i & 1;
-        if (start) initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, h);
-        rolled(i);
-        if (start) write_row<PAIRS>(rows.g[i], lane, h);
+        const float2 g = g_row(i), t = rolled(i, g, h);
+        h = m.first >> i & 1 ? g : t;
+        gs = add2(gs, g);  // (of no use in a closed span)
       }
     }
-    sh.map[buf][w][lane] = {{m.first ? kClosed : -expf(gs[0]), m.first ? kClosed : -expf(gs[1])}, {h[0], h[1]}};
+    sh.map[buf][w][lane] = {m.first ? both(kClosed) : make_float2(expf(gs.x), expf(gs.y)), h};
     if (__syncthreads_or(!alive)) return;  // a wait gave up; no copy is under way
-    if (p.chained && w == kWarps - 1 && q.in_group() != kGroup - 1) publish_tile<PAIRS, false>(p, sh, buf, q, l.c, lane);
+    if (p.chained && w == kWarps - 1 && (q.step + 1) % Chain<TOK>::kGroup != 0) publish_tile<PAIRS, false>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<false>(p, sh);
     const bool more = nq.step < p.tiles;
     if (more && !marked) begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
     const bool next_marked = more && has_marks(p, nq.tile);
-    h[0] = h[1] = 0.f;
+    h = both(0.f);
     if (p.chained) {
-      alive = enter_tile<PAIRS, false>(p, sh, buf, q, l.c, w, lane, h);
+      alive = enter_tile<TOK, PAIRS, false>(p, sh, buf, q, l.c, w, lane, h);
       if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced
     }
     enter_warp<false>(sh.map[buf], w, lane, h);
-    // (a chunk of 64 tokens begins with every warp of 64, 32 or 16 tokens that divides it)
+    // (a chunk's first token is a warp's)
     if (p.chunk_states && t0 % kGlrChunk == 0 && l.any() && t0 < p.tokens && GDR_IN_BOUNDS(t0 / kGlrChunk < p.chunks))
       store2<PAIRS>(p.chunk_states + (int64_t)(t0 / kGlrChunk) * p.D, l, h);
     if (!STATES_ONLY) {
@@ -657,26 +664,16 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
       if (!marked) {
 #pragma unroll
         for (int i = 0; i < TOK; ++i) {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) h[v] = fmaf(a[i][v], h[v], b_of(i, v));
+          h = fma2(a[i], h, b_of(i));
           if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) store2<PAIRS>(out + (int64_t)i * p.D, l, h);
         }
       } else {
+#pragma unroll 4
         for (int i = 0; i < TOK; ++i) {
-          if (m.first >> i & 1) {
-            const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
-            h[0] = g.at(0);
-            h[1] = g.at(1);
-          } else {
-            rolled(i);
-          }
+          const float2 g = g_row(i), t = rolled(i, g, h);
+          h = m.first >> i & 1 ? g : t;
           if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) store2<PAIRS>(out + (int64_t)i * p.D, l, h);
-          const int s = __shfl_sync(0xffffffffu, m.seq, i);
-          if ((m.last >> i & 1) && p.final_state) {
-            const int64_t r = state_row(p, s);
-            if (l.any() && r >= 0 && GDR_IN_BOUNDS(s < p.num_seqs && r < p.num_slots))
-              store2<PAIRS>(p.final_state + r * p.D, l, h);
-          }
+          if (m.last >> i & 1) store_state<PAIRS>(p, p.final_state, m.row_of(i), l, h);
         }
       }
       if (q.tile == 0) pass_empty(p, p.initial_state, p.final_state, true, q.stripe * kWide, kWide);
@@ -715,101 +712,73 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
     Lane<PAIRS> l(q.stripe, p.D);
     const uint32_t t0 = q.tile * (kWarps * TOK) + w * TOK;
-    float h[2] = {0.f, 0.f}, s[2] = {0.f, 0.f}, r[2] = {0.f, 0.f}, gs[2] = {0.f, 0.f};
-    if (l.any() && GDR_IN_BOUNDS(q.tile < p.chunks)) load2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l, h);
+    float2 h = both(0.f), s = both(0.f), r = both(0.f), gs = both(0.f);
+    if (l.any() && GDR_IN_BOUNDS(q.tile < p.chunks)) h = load2<PAIRS>(p.chunk_states + (int64_t)q.tile * p.D, l);
     Marks m;
     m.first = m.last = 0;
-    m.seq = 0;
+    m.row = -1;
     if (marked) m = find_marks<TOK>(p, t0, lane);
     alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
     const int buf = parity;
     parity ^= 1;
-    float a[TOK][2];
+    float2 a[TOK];
     Raw<IO> xk[EARLY ? TOK : 1], dk[EARLY ? TOK : 1];
-    auto x_of = [&](int i) { return EARLY ? xk[EARLY ? i : 0] : read_row<PAIRS>(rows.x[i], lane); };
-    auto d_of = [&](int i) { return EARLY ? dk[EARLY ? i : 0] : read_row<PAIRS>(rows.dh[i], lane); };
-    auto fresh_of = [&](int i, int v) { return fresh<IO>(read_row<PAIRS>(rows.g[i], lane).at(v), a[i][v]); };
-    auto advance = [&](int i, float (&y)[2]) {  // the state y after token i
-      const Raw<IO> x = x_of(i);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) y[v] = fmaf(a[i][v], y[v], COMPLEMENT ? fresh_of(i, v) * x.at(v) : x.at(v));
+    auto g_row = [&](int i) { return read_row<PAIRS>(rows.g[i], lane).value(); };
+    auto x_row = [&](int i) { return read_row<PAIRS>(rows.x[i], lane).value(); };
+    auto d_row = [&](int i) { return read_row<PAIRS>(rows.dh[i], lane).value(); };
+    auto x_of = [&](int i) { return EARLY ? xk[EARLY ? i : 0].value() : x_row(i); };
+    auto d_of = [&](int i) { return EARLY ? dk[EARLY ? i : 0].value() : d_row(i); };
+    // the state after y by token i
+    auto advance = [&](int i, float2 x, float2 y) {
+      return fma2(a[i], y, COMPLEMENT ? input<IO, COMPLEMENT>(g_row(i), a[i], x) : x);
     };
-    // the same for the rolled loops, from shared memory; their a and 1 - a of a token
-    auto start = [&](int i, float (&y)[2]) { initial_of<PAIRS>(p, __shfl_sync(0xffffffffu, m.seq, i), l, y); };
-    auto rolled_decay = [&](int i, float (&ai)[2], float (&ui)[2]) {
-      const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        ai[v] = decay<IO>(g.at(v));
-        ui[v] = COMPLEMENT ? fresh<IO>(g.at(v), ai[v]) : 1.f;
-      }
-    };
-    auto rolled = [&](int i, float (&y)[2]) {
-      float ai[2], ui[2];
-      rolled_decay(i, ai, ui);
-      const Raw<IO> x = read_row<PAIRS>(rows.x[i], lane);
-#pragma unroll
-      for (int v = 0; v < 2; ++v) y[v] = fmaf(ai[v], y[v], COMPLEMENT ? ui[v] * x.at(v) : x.at(v));
-    };
-    auto end_gradient = [&](int i, float (&y)[2]) {  // what the end of a sequence brings
-      const int sq = __shfl_sync(0xffffffffu, m.seq, i);
-      y[0] = y[1] = 0.f;
-      if (p.dfinal && l.any() && GDR_IN_BOUNDS(sq < p.num_seqs)) load2<PAIRS>(p.dfinal + (int64_t)sq * p.D, l, y);
+    auto rolled = [&](int i, float2 y) {
+      const float2 g = g_row(i), ai = decay<IO>(g);
+      return fma2(ai, y, input<IO, COMPLEMENT>(g, ai, x_row(i)));
     };
     if (!marked) {
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
-        const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
+        const float2 g = g_row(i);
         if (EARLY) {
           xk[EARLY ? i : 0] = read_row<PAIRS>(rows.x[i], lane);
           dk[EARLY ? i : 0] = read_row<PAIRS>(rows.dh[i], lane);
         }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          a[i][v] = decay<IO>(g.at(v));
-          gs[v] += g.at(v);
-        }
+        a[i] = decay<IO>(g);
+        gs = add2(gs, g);
       }
 #pragma unroll
-      for (int i = 0; i < TOK; ++i) advance(i, s);
+      for (int i = 0; i < TOK; ++i) s = advance(i, x_of(i), s);
 #pragma unroll
-      for (int i = TOK - 1; i >= 0; --i) {
-        const Raw<IO> d = d_of(i);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) r[v] = a[i][v] * (d.at(v) + r[v]);
-      }
+      for (int i = TOK - 1; i >= 0; --i) r = mul2(a[i], add2(d_of(i), r));
     } else {
+#pragma unroll 2
       for (int i = 0; i < TOK; ++i) {
-        if (m.first >> i & 1) start(i, s);
-        rolled(i, s);
-        const Raw<float> g = read_row<PAIRS>(rows.g[i], lane);
-        gs[0] += g.at(0);
-        gs[1] += g.at(1);
+        if (m.first >> i & 1) s = load_row<PAIRS>(p, p.initial_state, m.row_of(i), l);
+        s = rolled(i, s);
+        gs = add2(gs, g_row(i));
       }
-      for (int i = TOK - 1; i >= 0; --i) {
-        if (m.last >> i & 1) end_gradient(i, r);
-        float ai[2], ui[2];
-        rolled_decay(i, ai, ui);
-        const Raw<IO> d = read_row<PAIRS>(rows.dh[i], lane);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) r[v] = ai[v] * (d.at(v) + r[v]);
+#pragma unroll 2
+      for (int i = TOK - 1; i >= 0; --i) {  // the end of a sequence brings its final state's gradient
+        if (m.last >> i & 1) r = load_row<PAIRS>(p, p.dfinal, m.row_of(i), l);
+        r = mul2(decay<IO>(g_row(i)), add2(d_row(i), r));
       }
     }
     {
-      const float A[2] = {-expf(gs[0]), -expf(gs[1])};
-      sh.map[buf][w][lane] = {{m.last ? kClosed : A[0], m.last ? kClosed : A[1]}, {r[0], r[1]}};
-      states[w][lane] = {{m.first ? kClosed : A[0], m.first ? kClosed : A[1]}, {s[0], s[1]}};
+      const float2 A = make_float2(expf(gs.x), expf(gs.y));
+      sh.map[buf][w][lane] = {m.last ? both(kClosed) : A, r};
+      states[w][lane] = {m.first ? both(kClosed) : A, s};
     }
     if (__syncthreads_or(!alive)) return;  // a wait gave up; no copy is under way
-    if (p.chained && w == 0 && q.in_group() != kGroup - 1) publish_tile<PAIRS, true>(p, sh, buf, q, l.c, lane);
+    if (p.chained && w == 0 && (q.step + 1) % Chain<TOK>::kGroup != 0) publish_tile<PAIRS, true>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<true>(p, sh);
     const bool more = nq.step < p.tiles;
     if (EARLY && more && !marked) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
     const bool next_marked = more && has_marks(p, nq.tile);
     enter_warp<false>(states, w, lane, h);
-    r[0] = r[1] = 0.f;
+    r = both(0.f);
     if (p.chained) {
-      alive = enter_tile<PAIRS, true>(p, sh, buf, q, l.c, w, lane, r);
+      alive = enter_tile<TOK, PAIRS, true>(p, sh, buf, q, l.c, w, lane, r);
       if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced
@@ -818,56 +787,40 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     IO *dx0 = static_cast<IO *>(p.dx) + (int64_t)t0 * p.D;
     float *dg0 = p.dg + (int64_t)t0 * p.D;
     const int n = l.any() ? tokens_of<TOK>(p, t0) : 0;
-    // from the carry r: dx, dg and the carry of the token before; `u` is 1 - a,
-    // `past` h_{t-1}, less x_t for the complement
-    auto write = [&](int i, const Raw<IO> &d, const float (&ai)[2], const float (&u)[2], const float (&past)[2]) {
-      float dx[2], dg[2];
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const float dt = d.at(v) + r[v];
-        r[v] = ai[v] * dt;
-        dx[v] = COMPLEMENT ? u[v] * dt : dt;
-        dg[v] = r[v] * past[v];
-      }
+    // from the carry r: dx, dg and the carry of the token before; `past` is
+    // h_{t-1}, less x_t for the complement
+    auto write = [&](int i, float2 d, float2 ai, float2 past) {
+      const float2 dt = add2(d, r);
+      r = mul2(ai, dt);
       if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) {
-        store2<PAIRS>(dx0 + (int64_t)i * p.D, l, dx);
-        store2<PAIRS>(dg0 + (int64_t)i * p.D, l, dg);
+        store2<PAIRS>(dx0 + (int64_t)i * p.D, l, COMPLEMENT ? mul2(fresh<IO>(g_row(i), ai), dt) : dt);
+        store2<PAIRS>(dg0 + (int64_t)i * p.D, l, mul2(r, past));
       }
     };
+    auto less = [&](float2 y, float2 x) { return COMPLEMENT ? fma2(x, both(-1.f), y) : y; };
     if (!marked) {
-      float past[TOK][2];
+      float2 past[TOK];
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) past[i][v] = COMPLEMENT ? h[v] - x_of(i).at(v) : h[v];
-        if (i < TOK - 1) advance(i, h);
+        const float2 x = x_of(i);
+        past[i] = less(h, x);
+        if (i < TOK - 1) h = advance(i, x, h);
       }
 #pragma unroll
-      for (int i = TOK - 1; i >= 0; --i) {
-        float u[2] = {1.f, 1.f};
-        if (COMPLEMENT) {
-          u[0] = fresh_of(i, 0);
-          u[1] = fresh_of(i, 1);
-        }
-        write(i, d_of(i), a[i], u, past[i]);
-      }
+      for (int i = TOK - 1; i >= 0; --i) write(i, d_of(i), a[i], past[i]);
     } else {
-      float past[TOK][2];  // (indexed by a running i: local memory)
+      float2 past[TOK];  // (indexed by a running i: local memory)
+#pragma unroll 2
       for (int i = 0; i < TOK; ++i) {
-        if (m.first >> i & 1) start(i, h);
-        const Raw<IO> x = read_row<PAIRS>(rows.x[i], lane);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) past[i][v] = COMPLEMENT ? h[v] - x.at(v) : h[v];
-        rolled(i, h);
+        if (m.first >> i & 1) h = load_row<PAIRS>(p, p.initial_state, m.row_of(i), l);
+        past[i] = less(h, x_row(i));
+        h = rolled(i, h);
       }
+#pragma unroll 2
       for (int i = TOK - 1; i >= 0; --i) {
-        if (m.last >> i & 1) end_gradient(i, r);
-        float ai[2], ui[2];
-        rolled_decay(i, ai, ui);
-        write(i, read_row<PAIRS>(rows.dh[i], lane), ai, ui, past[i]);
-        const int sq = __shfl_sync(0xffffffffu, m.seq, i);
-        if (p.dinitial && (m.first >> i & 1) && l.any() && GDR_IN_BOUNDS(sq < p.num_seqs))
-          store2<PAIRS>(p.dinitial + (int64_t)sq * p.D, l, r);
+        if (m.last >> i & 1) r = load_row<PAIRS>(p, p.dfinal, m.row_of(i), l);
+        write(i, d_row(i), decay<IO>(g_row(i)), past[i]);
+        if (m.first >> i & 1) store_state<PAIRS>(p, p.dinitial, m.row_of(i), l, r);
       }
     }
     if (q.tile == 0) pass_empty(p, p.dfinal, p.dinitial, false, q.stripe * kWide, kWide);
@@ -1029,15 +982,15 @@ cudaError_t launch_no_tokens(const GlrArgs &p, bool backward, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The tiles of a launch with `tok` tokens a warp, and whether they wait for one
+// The tiles of a launch with TOK tokens a warp, and whether they wait for one
 // another: not where each begins with a sequence's first token.
-GlrArgs with_tiles(const GlrArgs &a, int tok) {
+template <int TOK> GlrArgs with_tiles(const GlrArgs &a) {
   GlrArgs p = a;
-  p.tile_tokens = kWarps * tok;
+  p.tile_tokens = kWarps * TOK;
   p.tiles = (p.tokens + p.tile_tokens - 1) / p.tile_tokens;
   p.stripes = (p.D + kWide - 1) / kWide;
   p.chained = p.tiles > 1 && (p.cu_seqlens || p.T > p.tile_tokens || p.tile_tokens % p.T != 0);
-  p.groups = (p.tiles + kGroup - 1) / kGroup;
+  p.groups = (p.tiles + Chain<TOK>::kGroup - 1) / Chain<TOK>::kGroup;
   p.carry = p.tile_map + p.tiles * p.pitch;
   return p;
 }
@@ -1078,7 +1031,7 @@ cudaError_t launch_tiles(const char *name, size_t smem, const GlrArgs &p, const 
 template <typename IO, bool PAIRS, bool COMPLEMENT, bool STATES_ONLY>
 cudaError_t launch_scan(const GlrArgs &a, cudaStream_t s) {
   constexpr int TOK = FwdShape<IO, PAIRS, COMPLEMENT>::kTok;
-  const GlrArgs p = with_tiles(a, TOK);
+  const GlrArgs p = with_tiles<TOK>(a);
   cudaError_t e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, false, s);
@@ -1097,7 +1050,7 @@ cudaError_t launch_fwd(const GlrArgs &a, cudaStream_t s) {
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 cudaError_t launch_bwd(const GlrArgs &a, cudaStream_t s) {
   constexpr int TOK = BwdShape<IO, COMPLEMENT>::kTok;
-  const GlrArgs p = with_tiles(a, TOK);
+  const GlrArgs p = with_tiles<TOK>(a);
   cudaError_t e = cudaSuccess;
   if (p.own_chunks && p.tiles > 0) e = launch_scan<IO, PAIRS, COMPLEMENT, true>(a, s);
   if (e == cudaSuccess) e = launch_begin(p, s);
