@@ -145,7 +145,9 @@ def lib() -> ctypes.CDLL:
     """Load ``libgated_delta.so`` (raises if it has not been built), or the
     library selected by :func:`use_library`."""
     global _lib
-    L = _load(_active_path)
+    L = _libs.get(_active_path)
+    if L is None:
+        L = _load(_active_path)
     if _active_path == library_path:
         _lib = L
     return L
@@ -476,36 +478,33 @@ def gdn_decode_step(q, k, v, g, beta, state, *, o=None, stream=None):
 # --------------------------------------------------------------------------- #
 # gated linear recurrence and the norms around a mixer block
 # --------------------------------------------------------------------------- #
-def _take(dev, **tensors):
-    """Every tensor given lives on ``dev``."""
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must live on {dev}, got {t.device}")
-
-
-def _dense(t, shape, dtype, name):
-    """Pointer of a contiguous tensor of this shape and type, or None."""
+# These calls are small next to their launches' cost on the host: arguments are
+# looked at once, in plain code.
+def _dense(t, shape, dtype, name, dev):
+    """Pointer of a contiguous tensor of this shape, type and device, or None."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return _ptr(t)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on CUDA device {dev}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _rows(t, shape, dtype, name, inner=1):
+def _rows(t, shape, dtype, name, dev, inner=1):
     """(pointer, elements from one row to the next) of a tensor whose last
     ``inner`` axes are contiguous and whose leading axes step evenly."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("tensors must live on a CUDA device")
-    width = 1
-    for n in shape[len(shape) - inner:]:
-        width *= n
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on CUDA device {dev}")
+    width = shape[-1] if inner == 1 else shape[-1] * shape[-2]
     if t.is_contiguous():
         return t.data_ptr(), width
     step, strides = 1, t.stride()
@@ -530,15 +529,39 @@ def _rows(t, shape, dtype, name, inner=1):
     return t.data_ptr(), ld
 
 
-@contextlib.contextmanager
-def _on(dev):
-    """The device current, where it is not."""
-    torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        yield
-    else:
-        with torch.cuda.device(dev):
-            yield
+def _bytes(t, name, dev):
+    """Pointer and size of a workspace."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must live on CUDA device {dev}")
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def _device_of(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    return dev
+
+
+def _current(torch, dev) -> bool:
+    return torch.cuda.current_device() == dev
+
+
+def _stream_of(torch, stream, dev) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 1.3 us less than the Stream object
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _like(torch, t):
+    """An empty contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _done(status, what):
+    if status:
+        _check(status, what)
 
 
 def _glr_input(name) -> int:
@@ -547,19 +570,25 @@ def _glr_input(name) -> int:
     return _GLR_INPUT[name]
 
 
-def _glr_common(x, g, cu_seqlens):
-    torch = _torch()
+def _glr_shape(torch, x, cu_seqlens, dev):
+    """(B, T, D, sequences, pointer of cu_seqlens)."""
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
-    io = _dtype_code(x)
     B, T, D = x.shape
-    if cu_seqlens is not None:
-        if cu_seqlens.dtype != torch.int32:
-            raise TypeError("cu_seqlens must be int32")
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("cu_seqlens must be [N + 1]")
-        return io, B, T, D, cu_seqlens.numel() - 1
-    return io, B, T, D, B
+    if cu_seqlens is None:
+        return B, T, D, B, None
+    if cu_seqlens.dtype != torch.int32:
+        raise TypeError("cu_seqlens must be int32")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [N + 1]")
+    return B, T, D, cu_seqlens.numel() - 1, _dense(cu_seqlens, cu_seqlens.shape, torch.int32, "cu_seqlens", dev)
+
+
+def _glr_slots(torch, state_slots, pool, N, D, dev, name):
+    """(pointer of the slots, rows of the pool)."""
+    if pool.dim() != 2:
+        raise ValueError(f"{name} must be [num_slots, {D}]")
+    return _dense(state_slots, (N,), torch.int32, "state_slots", dev), pool.shape[0]
 
 
 def glr_scan_fwd(x, g, initial_state=None, cu_seqlens=None, *, input_gate: str = "given",
@@ -575,38 +604,43 @@ def glr_scan_fwd(x, g, initial_state=None, cu_seqlens=None, *, input_gate: str =
     ``chunk_states`` tensor [ceil(B T / 64), D] fp32) keeps what glr_scan_bwd
     reads.  Returns (h, final_state, chunk_states, workspace)."""
     torch = _torch()
-    io, B, T, D, N = _glr_common(x, g, cu_seqlens)
-    code, dev, f32 = _glr_input(input_gate), x.device, torch.float32
-    _take(dev, g=g, initial_state=initial_state, cu_seqlens=cu_seqlens, h=h,
-          final_state=final_state, chunk_states=chunk_states, workspace=workspace,
-          state_pool=state_pool, state_slots=state_slots)
-    xp, ld_x = _rows(x, (B, T, D), x.dtype, "x")
-    gp, ld_g = _rows(g, (B, T, D), f32, "g")
-    slots, num_slots = _slots(state_slots, state_pool, N)
-    rows = N
-    if slots is not None:
+    dev = _device_of(x)
+    if not _current(torch, dev):
+        with torch.cuda.device(dev):
+            return glr_scan_fwd(
+                x, g, initial_state, cu_seqlens, input_gate=input_gate,
+                output_final_state=output_final_state, output_chunk_states=output_chunk_states,
+                h=h, final_state=final_state, chunk_states=chunk_states, workspace=workspace,
+                stream=stream, state_pool=state_pool, state_slots=state_slots)
+    io, code, f32, L = _dtype_code(x), _glr_input(input_gate), torch.float32, lib()
+    B, T, D, N, cup = _glr_shape(torch, x, cu_seqlens, dev)
+    shape, chunks = (B, T, D), (-(-B * T // GLR_CHUNK), D)
+    xp, ld_x = _rows(x, shape, x.dtype, "x", dev)
+    gp, ld_g = _rows(g, shape, f32, "g", dev)
+    slots, rows = None, N
+    if (state_slots is None) != (state_pool is None):
+        raise ValueError("state_pool and state_slots go together")
+    if state_pool is not None:
         if initial_state is not None or final_state is not None:
             raise ValueError("with state_pool, pass neither initial_state nor final_state")
+        slots, rows = _glr_slots(torch, state_slots, state_pool, N, D, dev, "state_pool")
         initial_state = final_state = state_pool
-        rows = num_slots
-    with _on(dev):
-        if h is None:
-            h = torch.empty((B, T, D), dtype=x.dtype, device=dev)
-        if final_state is None and output_final_state:
-            final_state = torch.empty((N, D), dtype=f32, device=dev)
-        if chunk_states is None and output_chunk_states:
-            chunk_states = torch.empty((-(-B * T // GLR_CHUNK), D), dtype=f32, device=dev)
-        L = lib()
-        need = L.glr_scan_fwd_workspace_size(B, T, D)
-        if workspace is None or workspace.numel() < need:
-            workspace = _alloc_workspace(need, dev)
-        _check(L.glr_scan_fwd(
-            xp, ld_x, gp, ld_g, _dense(h, (B, T, D), x.dtype, "h"),
-            _dense(initial_state, (rows, D), f32, "initial_state"),
-            _dense(final_state, (rows, D), f32, "final_state"), _ptr(slots), num_slots,
-            _dense(chunk_states, (-(-B * T // GLR_CHUNK), D), f32, "chunk_states"),
-            _ptr(cu_seqlens), N, B, T, D, code, io, _ptr(workspace), workspace.numel(),
-            _stream_handle(stream, dev)), "glr_scan_fwd")
+    elif final_state is None and output_final_state:
+        final_state = torch.empty((N, D), dtype=f32, device=x.device)
+    if h is None:
+        h = _like(torch, x)
+    if chunk_states is None and output_chunk_states:
+        chunk_states = torch.empty(chunks, dtype=f32, device=x.device)
+    need = L.glr_scan_fwd_workspace_size(B, T, D)
+    if workspace is None or workspace.numel() < need:
+        workspace = _alloc_workspace(need, x.device)
+    wp, have = _bytes(workspace, "workspace", dev)
+    _done(L.glr_scan_fwd(
+        xp, ld_x, gp, ld_g, _dense(h, shape, x.dtype, "h", dev),
+        _dense(initial_state, (rows, D), f32, "initial_state", dev),
+        _dense(final_state, (rows, D), f32, "final_state", dev), slots, rows,
+        _dense(chunk_states, chunks, f32, "chunk_states", dev), cup, N, B, T, D, code, io, wp, have,
+        _stream_of(torch, stream, dev)), "glr_scan_fwd")
     return h, final_state, chunk_states, workspace
 
 
@@ -618,33 +652,37 @@ def glr_scan_bwd(dh, x, g, initial_state=None, cu_seqlens=None, *, input_gate: s
     and input_gate as in the forward call, ``chunk_states`` what it returned
     (None: computed again).  Returns (dx, dg, dinitial_state, workspace)."""
     torch = _torch()
-    io, B, T, D, N = _glr_common(x, g, cu_seqlens)
-    code, dev, f32 = _glr_input(input_gate), x.device, torch.float32
-    _take(dev, dh=dh, g=g, initial_state=initial_state, cu_seqlens=cu_seqlens, dx=dx, dg=dg,
-          dfinal_state=dfinal_state, chunk_states=chunk_states, workspace=workspace,
-          dinitial_state=dinitial_state)
-    dp, ld_dh = _rows(dh, (B, T, D), x.dtype, "dh")
-    xp, ld_x = _rows(x, (B, T, D), x.dtype, "x")
-    gp, ld_g = _rows(g, (B, T, D), f32, "g")
-    with _on(dev):
-        if dx is None:
-            dx = torch.empty((B, T, D), dtype=x.dtype, device=dev)
-        if dg is None:
-            dg = torch.empty((B, T, D), dtype=f32, device=dev)
-        if dinitial_state is None and output_dinitial_state:
-            dinitial_state = torch.empty((N, D), dtype=f32, device=dev)
-        L = lib()
-        need = L.glr_scan_bwd_workspace_size(B, T, D, chunk_states is not None)
-        if workspace is None or workspace.numel() < need:
-            workspace = _alloc_workspace(need, dev)
-        _check(L.glr_scan_bwd(
-            dp, ld_dh, _dense(dfinal_state, (N, D), f32, "dfinal_state"), xp, ld_x, gp, ld_g,
-            _dense(initial_state, (N, D), f32, "initial_state"),
-            _dense(chunk_states, (-(-B * T // GLR_CHUNK), D), f32, "chunk_states"),
-            _dense(dx, (B, T, D), x.dtype, "dx"), _dense(dg, (B, T, D), f32, "dg"),
-            _dense(dinitial_state, (N, D), f32, "dinitial_state"), _ptr(cu_seqlens), N, B, T, D,
-            code, io, _ptr(workspace), workspace.numel(), _stream_handle(stream, dev)),
-            "glr_scan_bwd")
+    dev = _device_of(x)
+    if not _current(torch, dev):
+        with torch.cuda.device(dev):
+            return glr_scan_bwd(
+                dh, x, g, initial_state, cu_seqlens, input_gate=input_gate,
+                dfinal_state=dfinal_state, chunk_states=chunk_states,
+                output_dinitial_state=output_dinitial_state, dx=dx, dg=dg,
+                dinitial_state=dinitial_state, workspace=workspace, stream=stream)
+    io, code, f32, L = _dtype_code(x), _glr_input(input_gate), torch.float32, lib()
+    B, T, D, N, cup = _glr_shape(torch, x, cu_seqlens, dev)
+    shape, chunks, states = (B, T, D), (-(-B * T // GLR_CHUNK), D), (N, D)
+    dp, ld_dh = _rows(dh, shape, x.dtype, "dh", dev)
+    xp, ld_x = _rows(x, shape, x.dtype, "x", dev)
+    gp, ld_g = _rows(g, shape, f32, "g", dev)
+    if dx is None:
+        dx = _like(torch, x)
+    if dg is None:
+        dg = _like(torch, g)
+    if dinitial_state is None and output_dinitial_state:
+        dinitial_state = torch.empty(states, dtype=f32, device=x.device)
+    need = L.glr_scan_bwd_workspace_size(B, T, D, chunk_states is not None)
+    if workspace is None or workspace.numel() < need:
+        workspace = _alloc_workspace(need, x.device)
+    wp, have = _bytes(workspace, "workspace", dev)
+    _done(L.glr_scan_bwd(
+        dp, ld_dh, _dense(dfinal_state, states, f32, "dfinal_state", dev), xp, ld_x, gp, ld_g,
+        _dense(initial_state, states, f32, "initial_state", dev),
+        _dense(chunk_states, chunks, f32, "chunk_states", dev),
+        _dense(dx, shape, x.dtype, "dx", dev), _dense(dg, shape, f32, "dg", dev),
+        _dense(dinitial_state, states, f32, "dinitial_state", dev), cup, N, B, T, D, code, io, wp,
+        have, _stream_of(torch, stream, dev)), "glr_scan_bwd")
     return dx, dg, dinitial_state, workspace
 
 
@@ -654,38 +692,45 @@ def glr_step(x, g, state, *, state_slots=None, input_gate: str = "given", h=None
     indexed by ``state_slots`` (int32 [N]; a slot outside the pool is a padding
     entry), is updated in place.  Returns h [N,D]."""
     torch = _torch()
+    dev = _device_of(x)
+    if not _current(torch, dev):
+        with torch.cuda.device(dev):
+            return glr_step(x, g, state, state_slots=state_slots, input_gate=input_gate, h=h,
+                            stream=stream)
     if x.dim() != 2:
         raise ValueError("x must be [N, D]")
-    N, D = x.shape
-    io, code, dev, f32 = _dtype_code(x), _glr_input(input_gate), x.device, torch.float32
-    _take(dev, g=g, state=state, state_slots=state_slots, h=h)
-    xp, ld_x = _rows(x, (N, D), x.dtype, "x")
-    gp, ld_g = _rows(g, (N, D), f32, "g")
-    slots, num_slots = _slots(state_slots, state if state_slots is not None else None, N)
-    with _on(dev):
-        if h is None:
-            h = torch.empty((N, D), dtype=x.dtype, device=dev)
-        _check(lib().glr_step(
-            xp, ld_x, gp, ld_g, _dense(h, (N, D), x.dtype, "h"),
-            _dense(state, (num_slots if slots is not None else N, D), f32, "state"), _ptr(slots),
-            num_slots, N, D, code, io, _stream_handle(stream, dev)), "glr_step")
+    io, code, f32, shape = _dtype_code(x), _glr_input(input_gate), torch.float32, x.shape
+    N, D = shape
+    xp, ld_x = _rows(x, shape, x.dtype, "x", dev)
+    gp, ld_g = _rows(g, shape, f32, "g", dev)
+    slots, rows = None, N
+    if state_slots is not None:
+        slots, rows = _glr_slots(torch, state_slots, state, N, D, dev, "state")
+    if h is None:
+        h = _like(torch, x)
+    _done(lib().glr_step(
+        xp, ld_x, gp, ld_g, _dense(h, shape, x.dtype, "h", dev),
+        _dense(state, (rows, D), f32, "state", dev), slots, rows, N, D, code, io,
+        _stream_of(torch, stream, dev)), "glr_step")
     return h
 
 
-def _gate_code(gate) -> int:
+def _gate_code(gate, z) -> int:
     if gate not in _GATE:
         raise ValueError(f"gate must be None, 'silu' or 'sigmoid', got {gate!r}")
+    if (z is None) != (gate is None):
+        raise ValueError("z goes with a gate, and a gate with z")
     return _GATE[gate]
 
 
-def _heads(x):
+def _heads(shape):
     """(tokens, H, d) of [..., H, d]."""
-    if x.dim() < 2:
+    if len(shape) < 2:
         raise ValueError("x must be [..., H, d]")
     tokens = 1
-    for n in x.shape[:-2]:
+    for n in shape[:-2]:
         tokens *= n
-    return tokens, x.shape[-2], x.shape[-1]
+    return tokens, shape[-2], shape[-1]
 
 
 def gated_norm_fwd(x, z=None, weight=None, *, gate: Optional[str] = "silu", eps: float = 1e-6,
@@ -694,20 +739,20 @@ def gated_norm_fwd(x, z=None, weight=None, *, gate: Optional[str] = "silu", eps:
     x, z [...,H,d] (bf16 or fp32; z may be a slice of wider token rows), weight
     fp32 [d] or None; ``gate`` "silu", "sigmoid" or None (then no z).  Returns y."""
     torch = _torch()
-    code, io, dev = _gate_code(gate), _dtype_code(x), x.device
-    tokens, H, d = _heads(x)
-    _take(dev, z=z, weight=weight, y=y)
-    if (z is None) != (code == 0):
-        raise ValueError("z goes with a gate, and a gate with z")
-    xp, ld_x = _rows(x, x.shape, x.dtype, "x", 2)
-    zp, ld_z = (None, 0) if z is None else _rows(z, x.shape, x.dtype, "z", 2)
-    with _on(dev):
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        _check(lib().kda_gated_norm_fwd(
-            xp, ld_x, zp, ld_z, _dense(weight, (d,), torch.float32, "weight"),
-            _dense(y, x.shape, x.dtype, "y"), tokens, H, d, eps, code, io,
-            _stream_handle(stream, dev)), "kda_gated_norm_fwd")
+    dev = _device_of(x)
+    if not _current(torch, dev):
+        with torch.cuda.device(dev):
+            return gated_norm_fwd(x, z, weight, gate=gate, eps=eps, y=y, stream=stream)
+    code, io, dtype, shape = _gate_code(gate, z), _dtype_code(x), x.dtype, x.shape
+    tokens, H, d = _heads(shape)
+    xp, ld_x = _rows(x, shape, dtype, "x", dev, 2)
+    zp, ld_z = (None, 0) if z is None else _rows(z, shape, dtype, "z", dev, 2)
+    if y is None:
+        y = _like(torch, x)
+    _done(lib().kda_gated_norm_fwd(
+        xp, ld_x, zp, ld_z, _dense(weight, (d,), torch.float32, "weight", dev),
+        _dense(y, shape, dtype, "y", dev), tokens, H, d, eps, code, io,
+        _stream_of(torch, stream, dev)), "kda_gated_norm_fwd")
     return y
 
 
@@ -717,44 +762,48 @@ def gated_norm_bwd(dy, x, z=None, weight=None, *, gate: Optional[str] = "silu",
     """Gradients of gated_norm_fwd.  Returns (dx, dz, dweight, workspace); dz is
     None without a gate, dweight None without a weight."""
     torch = _torch()
-    code, io, dev = _gate_code(gate), _dtype_code(x), x.device
-    tokens, H, d = _heads(x)
-    _take(dev, dy=dy, z=z, weight=weight, dx=dx, dz=dz, dweight=dweight, workspace=workspace)
-    if (z is None) != (code == 0):
-        raise ValueError("z goes with a gate, and a gate with z")
-    dp, ld_dy = _rows(dy, x.shape, x.dtype, "dy", 2)
-    xp, ld_x = _rows(x, x.shape, x.dtype, "x", 2)
-    zp, ld_z = (None, 0) if z is None else _rows(z, x.shape, x.dtype, "z", 2)
-    with _on(dev):
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        if dz is None and z is not None:
-            dz = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        if weight is None:
-            dweight = None
-        elif dweight is None and output_dweight:
-            dweight = torch.empty(d, dtype=torch.float32, device=dev)
-        L = lib()
-        if dweight is not None:
-            need = L.kda_gated_norm_bwd_workspace_size(d)
-            if workspace is None or workspace.numel() < need:
-                workspace = _alloc_workspace(need, dev)
-        _check(L.kda_gated_norm_bwd(
-            dp, ld_dy, xp, ld_x, zp, ld_z, _dense(weight, (d,), torch.float32, "weight"),
-            _dense(dx, x.shape, x.dtype, "dx"), _dense(dz, x.shape, x.dtype, "dz"),
-            _dense(dweight, (d,), torch.float32, "dweight"), tokens, H, d, eps, code, io,
-            _ptr(workspace), 0 if workspace is None else workspace.numel(),
-            _stream_handle(stream, dev)), "kda_gated_norm_bwd")
+    dev = _device_of(x)
+    if not _current(torch, dev):
+        with torch.cuda.device(dev):
+            return gated_norm_bwd(dy, x, z, weight, gate=gate, eps=eps,
+                                  output_dweight=output_dweight, dx=dx, dz=dz, dweight=dweight,
+                                  workspace=workspace, stream=stream)
+    code, io, dtype, shape, f32 = _gate_code(gate, z), _dtype_code(x), x.dtype, x.shape, torch.float32
+    tokens, H, d = _heads(shape)
+    dp, ld_dy = _rows(dy, shape, dtype, "dy", dev, 2)
+    xp, ld_x = _rows(x, shape, dtype, "x", dev, 2)
+    zp, ld_z = (None, 0) if z is None else _rows(z, shape, dtype, "z", dev, 2)
+    if dx is None:
+        dx = _like(torch, x)
+    if z is None:
+        dz = None
+    elif dz is None:
+        dz = _like(torch, x)
+    if weight is None:
+        dweight = None
+    elif dweight is None and output_dweight:
+        dweight = torch.empty(d, dtype=f32, device=x.device)
+    L, wp, have = lib(), None, 0
+    if dweight is not None:
+        need = L.kda_gated_norm_bwd_workspace_size(d)
+        if workspace is None or workspace.numel() < need:
+            workspace = _alloc_workspace(need, x.device)
+        wp, have = _bytes(workspace, "workspace", dev)
+    _done(L.kda_gated_norm_bwd(
+        dp, ld_dy, xp, ld_x, zp, ld_z, _dense(weight, (d,), f32, "weight", dev),
+        _dense(dx, shape, dtype, "dx", dev), _dense(dz, shape, dtype, "dz", dev),
+        _dense(dweight, (d,), f32, "dweight", dev), tokens, H, d, eps, code, io, wp, have,
+        _stream_of(torch, stream, dev)), "kda_gated_norm_bwd")
     return dx, dz, dweight, workspace
 
 
-def _width(t):
-    if t.dim() < 1:
+def _width(shape):
+    if len(shape) < 1:
         raise ValueError("the residual must be [..., D]")
-    D, rows = t.shape[-1], 1
-    for n in t.shape[:-1]:
+    rows = 1
+    for n in shape[:-1]:
         rows *= n
-    return rows, D
+    return rows, shape[-1]
 
 
 def add_norm_fwd(residual, y, weight=None, scale=None, *, eps: float = 1e-6, residual_out=None,
@@ -764,22 +813,24 @@ def add_norm_fwd(residual, y, weight=None, scale=None, *, eps: float = 1e-6, res
     fp32 with either activation type), y [...,D]; scale, weight fp32 [D] or None.
     ``residual_out`` may be ``residual`` itself.  Returns (residual_out, n)."""
     torch = _torch()
-    rows, D = _width(residual)
-    dev, shape = residual.device, residual.shape
+    dev = _device_of(residual)
+    if not _current(torch, dev):
+        with torch.cuda.device(dev):
+            return add_norm_fwd(residual, y, weight, scale, eps=eps, residual_out=residual_out,
+                                n=n, stream=stream)
+    shape, f32 = residual.shape, torch.float32
+    rows, D = _width(shape)
     res, io = _dtype_code(residual), _dtype_code(y)
-    _take(dev, y=y, weight=weight, scale=scale, residual_out=residual_out, n=n)
-    with _on(dev):
-        if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
-        if n is None:
-            n = torch.empty(shape, dtype=y.dtype, device=dev)
-        _check(lib().kda_add_norm_fwd(
-            _ptr(residual), _dense(y, shape, y.dtype, "y"),
-            _dense(scale, (D,), torch.float32, "scale"),
-            _dense(weight, (D,), torch.float32, "weight"),
-            _dense(residual_out, shape, residual.dtype, "residual_out"),
-            _dense(n, shape, y.dtype, "n"), rows, D, eps, res, io, _stream_handle(stream, dev)),
-            "kda_add_norm_fwd")
+    if residual_out is None:
+        residual_out = _like(torch, residual)
+    if n is None:
+        n = _like(torch, y)
+    _done(lib().kda_add_norm_fwd(
+        _dense(residual, shape, residual.dtype, "residual", dev), _dense(y, shape, y.dtype, "y", dev),
+        _dense(scale, (D,), f32, "scale", dev), _dense(weight, (D,), f32, "weight", dev),
+        _dense(residual_out, shape, residual.dtype, "residual_out", dev),
+        _dense(n, shape, y.dtype, "n", dev), rows, D, eps, res, io,
+        _stream_of(torch, stream, dev)), "kda_add_norm_fwd")
     return residual_out, n
 
 
@@ -792,42 +843,44 @@ def add_norm_bwd(dn, dresidual_out, residual_out, y=None, weight=None, scale=Non
     type dy IS dresidual, the same tensor; dweight (dscale) is None without a
     weight (a scale)."""
     torch = _torch()
-    rows, D = _width(residual_out)
-    dev, shape, f32 = residual_out.device, residual_out.shape, torch.float32
-    res, io = _dtype_code(residual_out), _dtype_code(dn)
-    _take(dev, dn=dn, dresidual_out=dresidual_out, y=y, weight=weight, scale=scale,
-          dresidual=dresidual, dy=dy, dscale=dscale, dweight=dweight, workspace=workspace)
+    dev = _device_of(residual_out)
+    if not _current(torch, dev):
+        with torch.cuda.device(dev):
+            return add_norm_bwd(dn, dresidual_out, residual_out, y, weight, scale, eps=eps,
+                                dresidual=dresidual, dy=dy, dscale=dscale, dweight=dweight,
+                                workspace=workspace, stream=stream)
+    shape, f32, where = residual_out.shape, torch.float32, residual_out.device
+    rows, D = _width(shape)
+    res, io, dtype, rdtype = _dtype_code(residual_out), _dtype_code(dn), dn.dtype, residual_out.dtype
     if scale is not None and y is None:
         raise ValueError("the gradient of scale needs y")
-    with _on(dev):
-        if dresidual is None:
-            dresidual = torch.empty(shape, dtype=residual_out.dtype, device=dev)
-        shared = dy is None and scale is None and dn.dtype == residual_out.dtype
-        if dy is None and not shared:
-            dy = torch.empty(shape, dtype=dn.dtype, device=dev)
-        if weight is None:
-            dweight = None
-        elif dweight is None:
-            dweight = torch.empty(D, dtype=f32, device=dev)
-        if scale is None:
-            dscale = None
-        elif dscale is None:
-            dscale = torch.empty(D, dtype=f32, device=dev)
-        L = lib()
-        if dweight is not None or dscale is not None:
-            need = L.kda_add_norm_bwd_workspace_size(D)
-            if workspace is None or workspace.numel() < need:
-                workspace = _alloc_workspace(need, dev)
-        _check(L.kda_add_norm_bwd(
-            _dense(dn, shape, dn.dtype, "dn"),
-            _dense(dresidual_out, shape, residual_out.dtype, "dresidual_out"), _ptr(residual_out),
-            _dense(y, shape, dn.dtype, "y") if scale is not None else None,
-            _dense(scale, (D,), f32, "scale"), _dense(weight, (D,), f32, "weight"),
-            _dense(dresidual, shape, residual_out.dtype, "dresidual"),
-            _dense(dy, shape, dn.dtype, "dy"), _dense(dscale, (D,), f32, "dscale"),
-            _dense(dweight, (D,), f32, "dweight"), rows, D, eps, res, io, _ptr(workspace),
-            0 if workspace is None else workspace.numel(), _stream_handle(stream, dev)),
-            "kda_add_norm_bwd")
+    if dresidual is None:
+        dresidual = _like(torch, residual_out)
+    shared = dy is None and scale is None and dtype == rdtype
+    if dy is None and not shared:
+        dy = _like(torch, dn)
+    if weight is None:
+        dweight = None
+    elif dweight is None:
+        dweight = torch.empty(D, dtype=f32, device=where)
+    if scale is None:
+        dscale = None
+    elif dscale is None:
+        dscale = torch.empty(D, dtype=f32, device=where)
+    L, wp, have = lib(), None, 0
+    if dweight is not None or dscale is not None:
+        need = L.kda_add_norm_bwd_workspace_size(D)
+        if workspace is None or workspace.numel() < need:
+            workspace = _alloc_workspace(need, where)
+        wp, have = _bytes(workspace, "workspace", dev)
+    _done(L.kda_add_norm_bwd(
+        _dense(dn, shape, dtype, "dn", dev), _dense(dresidual_out, shape, rdtype, "dresidual_out", dev),
+        _dense(residual_out, shape, rdtype, "residual_out", dev),
+        _dense(y, shape, dtype, "y", dev) if scale is not None else None,
+        _dense(scale, (D,), f32, "scale", dev), _dense(weight, (D,), f32, "weight", dev),
+        _dense(dresidual, shape, rdtype, "dresidual", dev), _dense(dy, shape, dtype, "dy", dev),
+        _dense(dscale, (D,), f32, "dscale", dev), _dense(dweight, (D,), f32, "dweight", dev), rows, D,
+        eps, res, io, wp, have, _stream_of(torch, stream, dev)), "kda_add_norm_bwd")
     return dresidual, dresidual if shared else dy, dweight, dscale, workspace
 
 
