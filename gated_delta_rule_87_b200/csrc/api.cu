@@ -575,7 +575,8 @@ kda_status_t kda_bounds_violations(void *stream, uint32_t *count) {
   if (e != cudaSuccess) return cuda_fail(e, "synchronising before reading the bounds counters");
   const unsigned int parts[] = {gdr::oob_count_prefill_tc(), gdr::oob_count_prefill_simt(),
                                 gdr::oob_count_decode(), gdr::oob_count_api(),
-                                gdr::oob_count_glr(), gdr::oob_count_norms()};
+                                gdr::oob_count_glr(), gdr::oob_count_gated_norm(),
+                                gdr::oob_count_add_norm()};
   uint64_t total = 0;
   for (unsigned int p : parts) {
     if (p == ~0u) return fail(KDA_ERR_CUDA, "a bounds counter could not be read");

@@ -36,7 +36,8 @@ unsigned int oob_count_prefill_simt();
 unsigned int oob_count_decode();
 unsigned int oob_count_api();
 unsigned int oob_count_glr();
-unsigned int oob_count_norms();
+unsigned int oob_count_gated_norm();
+unsigned int oob_count_add_norm();
 
 // Token-by-token form: T tokens for each of N sequences ([N, T, H, d]
 // layout), state updated in place.  T = 1 is one decode step.
