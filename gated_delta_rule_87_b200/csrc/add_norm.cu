@@ -15,8 +15,8 @@ add_norm_fwd_kernel(const __grid_constant__ AddNormArgs p) {
   __shared__ float2 buf[64];
   extern __shared__ __align__(16) float shared[];
   Group<V, NV, LANES, ODD> grp(buf, p.rows, p.D);
-  const Columns<V, NV, LANES, ODD> weight(grp, p.weight, column_slots<V, NV, LANES>(shared, 0));
-  const Columns<V, NV, LANES, ODD> scale(grp, p.scale, column_slots<V, NV, LANES>(shared, 1));
+  const Columns<V, NV, LANES, ODD, kAgain<V, NV, LANES, ODD>> weight(grp, p.weight, column_slots<V, NV, LANES>(shared, 0));
+  const Columns<V, NV, LANES, ODD, kAgain<V, NV, LANES, ODD>> scale(grp, p.scale, column_slots<V, NV, LANES>(shared, 1));
   for (int64_t row = grp.row; grp.more(row); row += grp.step) {
     const bool live = row < grp.rows;
     Pack<RES, V> r[NV];
@@ -37,7 +37,7 @@ add_norm_fwd_kernel(const __grid_constant__ AddNormArgs p) {
         y[i].keep(grp.half[i]);
       }
       float2 sc[NP];
-      scale.get(i, sc);
+      scale.get(grp, i, sc);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         t[i][j] = fma2(sc[j], y[i].pair(j), r[i].pair(j));
@@ -50,7 +50,7 @@ add_norm_fwd_kernel(const __grid_constant__ AddNormArgs p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float2 w[NP];
-      weight.get(i, w);
+      weight.get(grp, i, w);
 #pragma unroll
       for (int j = 0; j < NP; ++j) w[j] = mul2(w[j], mul2(t[i][j], inv));
       if (live && grp.any[i] && GDR_IN_BOUNDS(row < p.rows))
@@ -70,8 +70,8 @@ add_norm_bwd_kernel(const __grid_constant__ AddNormArgs p) {
   extern __shared__ __align__(16) float shared[];
   Group<V, NV, LANES, ODD> grp(buf, p.rows, p.D);
   const bool want_dscale = p.dscale != nullptr;
-  const Columns<V, NV, LANES, ODD> weight(grp, p.weight, column_slots<V, NV, LANES>(shared, 0));
-  const Columns<V, NV, LANES, ODD> scale(grp, p.scale, column_slots<V, NV, LANES>(shared, 1));
+  const Columns<V, NV, LANES, ODD, false> weight(grp, p.weight, column_slots<V, NV, LANES>(shared, 0));
+  const Columns<V, NV, LANES, ODD, false> scale(grp, p.scale, column_slots<V, NV, LANES>(shared, 1));
   float2 aw[NV][NP], as[NV][NP];
   Pack<RES, V> t[NV], dt[NV];
   Pack<IO, V> dn[NV], y[NV];
@@ -118,7 +118,7 @@ add_norm_bwd_kernel(const __grid_constant__ AddNormArgs p) {
         cdn[i].keep(grp.half[i]);
       }
       float2 w[NP];
-      weight.get(i, w);
+      weight.get(grp, i, w);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const float2 tv = ct[i].pair(j);
@@ -133,7 +133,7 @@ add_norm_bwd_kernel(const __grid_constant__ AddNormArgs p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float2 d[NP], w[NP];
-      weight.get(i, w);
+      weight.get(grp, i, w);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {  // (sums of columns that are not the thread's are never written)
         const float2 tv = ct[i].pair(j), gv = cdn[i].pair(j);
@@ -144,7 +144,7 @@ add_norm_bwd_kernel(const __grid_constant__ AddNormArgs p) {
       if (live && grp.any[i] && GDR_IN_BOUNDS(row < p.rows)) {
         store_piece<RES, V>(static_cast<RES *>(p.dresidual) + row * p.D, grp.c[i], grp.whole[i], grp.half[i], d);
         if (p.dy) {
-          scale.get(i, w);
+          scale.get(grp, i, w);
 #pragma unroll
           for (int j = 0; j < NP; ++j) d[j] = mul2(d[j], w[j]);
           store_piece<IO, V>(static_cast<IO *>(p.dy) + row * p.D, grp.c[i], grp.whole[i], grp.half[i], d);
@@ -159,7 +159,7 @@ add_norm_bwd_kernel(const __grid_constant__ AddNormArgs p) {
 
 template <typename RES, typename IO, int V, bool ODD, bool BACK>
 cudaError_t add_plan(const AddNormArgs &p, cudaStream_t s) {
-  const Plan q = plan<V, BACK>(p.D, 2);
+  const Plan q = plan<V, BACK>(p.D, 2, ODD);
   int blocks = 0;
   cudaError_t e = cudaErrorInvalidValue;
 #define GDR_LAUNCH(NV, LANES)                                                                                  \
@@ -184,7 +184,7 @@ template <typename RES, typename IO> cudaError_t add_io(const AddNormArgs &p, bo
   const bool wide = aligned16(p.residual) && aligned16(p.y) && aligned16(p.residual_out) && aligned16(p.n) &&
                     aligned16(p.dn) && aligned16(p.dresidual_out) && aligned16(p.dresidual) && aligned16(p.dy);
   if (!wide) return add_vec<RES, IO, 1, false>(p, back, s);
-  return p.D % V == 0 ? add_vec<RES, IO, V, false>(p, back, s) : add_vec<RES, IO, V, true>(p, back, s);
+  return p.D % V == 0 && aligned16(p.weight) && aligned16(p.scale) ? add_vec<RES, IO, V, false>(p, back, s) : add_vec<RES, IO, V, true>(p, back, s);
 }
 
 cudaError_t add_any(const AddNormArgs &p, bool back, cudaStream_t s) {

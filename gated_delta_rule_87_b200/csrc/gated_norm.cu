@@ -63,7 +63,7 @@ gated_norm_fwd_kernel(const __grid_constant__ GatedNormArgs p) {
   __shared__ float2 buf[64];
   extern __shared__ __align__(16) float shared[];
   Group<V, NV, LANES, ODD> grp(buf, p.tokens * p.H, p.d);
-  const Columns<V, NV, LANES, ODD> weight(grp, p.weight, shared);
+  const Columns<V, NV, LANES, ODD, kAgain<V, NV, LANES, ODD>> weight(grp, p.weight, shared);
   const bool gated = SILU || p.gate != KDA_GATE_NONE;
   HeadRow at(grp.row, grp.step, p.H);
   for (int64_t row = grp.row; grp.more(row); row += grp.step, at.next()) {
@@ -89,7 +89,7 @@ gated_norm_fwd_kernel(const __grid_constant__ GatedNormArgs p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float2 w[NP];
-      weight.get(i, w);
+      weight.get(grp, i, w);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         w[j] = mul2(w[j], mul2(x[i].pair(j), inv));
@@ -110,7 +110,7 @@ gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
   __shared__ float2 buf[64];
   extern __shared__ __align__(16) float shared[];
   Group<V, NV, LANES, ODD> grp(buf, p.tokens * p.H, p.d);
-  const Columns<V, NV, LANES, ODD> weight(grp, p.weight, shared);
+  const Columns<V, NV, LANES, ODD, false> weight(grp, p.weight, shared);
   const bool gated = SILU || p.gate != KDA_GATE_NONE;
   HeadRow at(grp.row, grp.step, p.H);
   float2 acc[NV][NP];
@@ -152,7 +152,7 @@ gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
         cz[i].keep(grp.half[i]);
       }
       float2 w[NP];
-      weight.get(i, w);
+      weight.get(grp, i, w);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const float2 xv = cx[i].pair(j);
@@ -173,7 +173,7 @@ gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float2 dx[NP], dz[NP], w[NP];
-      weight.get(i, w);
+      weight.get(grp, i, w);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const float2 xv = cx[i].pair(j), gv = cdy[i].pair(j), zv = cz[i].pair(j);
@@ -195,7 +195,7 @@ gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
 
 template <typename IO, int V, bool ODD, bool SILU, bool BACK>
 cudaError_t gated_gate(const GatedNormArgs &p, cudaStream_t s) {
-  const Plan q = plan<V, BACK>(p.d, 1);
+  const Plan q = plan<V, BACK>(p.d, 1, ODD);
   const int64_t rows = p.tokens * p.H;
   int blocks = 0;
   cudaError_t e = cudaErrorInvalidValue;
@@ -226,7 +226,7 @@ template <typename IO> cudaError_t gated_io(const GatedNormArgs &p, bool back, c
   const bool wide = (packed || even) && aligned16(p.x) && aligned16(p.z) && aligned16(p.y) && aligned16(p.dy) &&
                     aligned16(p.dx) && aligned16(p.dz);
   if (!wide) return gated_vec<IO, 1, false>(p, back, s);
-  return p.d % V == 0 ? gated_vec<IO, V, false>(p, back, s) : gated_vec<IO, V, true>(p, back, s);
+  return p.d % V == 0 && aligned16(p.weight) ? gated_vec<IO, V, false>(p, back, s) : gated_vec<IO, V, true>(p, back, s);
 }
 
 // out[c] = sum of partial[b][c] over the blocks, in a fixed order.
