@@ -679,7 +679,10 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
       if (q.tile == 0) pass_empty(p, p.initial_state, p.final_state, true, q.stripe * kWide, kWide);
     }
     if (!more) return;
-    if (marked) begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    if (marked) {
+      if (PAIRS) tc::fence_async_smem();  // states were written over rows of g
+      begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    }
     marked = next_marked;
     q = nq;
   }
