@@ -65,6 +65,7 @@ template <typename RES, typename IO, int V, int NV, int LANES, bool ODD>
 __global__ void __launch_bounds__(LANES ? 256 : kBlockThreads<V, true>)
 add_norm_bwd_kernel(const __grid_constant__ AddNormArgs p) {
   constexpr int NP = Pairs<V>::N;
+  let_next_start();
   constexpr bool EARLY = NV == 1;
   __shared__ float2 buf[64];
   extern __shared__ __align__(16) float shared[];

@@ -38,6 +38,30 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// ---- a kernel behind the one before it ----
+// launch_behind() starts a kernel while the one before it on the stream still
+// runs, once every block of that one has called let_next_start(); what the
+// earlier kernel writes may be read after wait_for_last(), which every thread of
+// the later kernel calls first (so what follows on the stream waits for both).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... PARAMS, typename... ARGS>
+cudaError_t launch_behind(void (*kernel)(PARAMS...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                          const ARGS &...args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, PARAMS(args)...);
+}
+
 // ---- bounds-checked build (compiled with -DGDR_BOUNDS_CHECK) ----
 // Every index a kernel computes for a global-memory access of its own (not
 // the tensor-map copies, which the TMA unit bounds itself) is checked against

@@ -106,6 +106,7 @@ template <typename IO, int V, int NV, int LANES, bool ODD, bool SILU>
 __global__ void __launch_bounds__(LANES ? 256 : kBlockThreads<V, true>, LANES && NV == 1 ? SILU ? 2 : 3 : 1)
 gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
   constexpr int NP = Pairs<V>::N;
+  let_next_start();
   constexpr bool EARLY = NV == 1;
   __shared__ float2 buf[64];
   extern __shared__ __align__(16) float shared[];
@@ -233,6 +234,7 @@ template <typename IO> cudaError_t gated_io(const GatedNormArgs &p, bool back, c
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restrict__ partial0,
                                                           float *out0, const float *partial1,
                                                           float *out1, int blocks, int d) {
+  wait_for_last();
   const float *partial = blockIdx.y ? partial1 : partial0;
   float *out = blockIdx.y ? out1 : out0;
   if (!out) return;
@@ -253,9 +255,8 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restric
 cudaError_t sum_columns(const float *partial, float *out0, float *out1, int d, int blocks, cudaStream_t s) {
   if (!out0 && !out1) return cudaSuccess;
   TraceScope tr("column_sum_kernel", s);
-  column_sum_kernel<<<dim3((d + 31) / 32, out1 ? 2 : 1), dim3(32, 32), 0, s>>>(
-      partial, out0, partial + (int64_t)kNormBlocks * d, out1, blocks, d);
-  return cudaGetLastError();
+  return launch_behind(column_sum_kernel, dim3((d + 31) / 32, out1 ? 2 : 1), dim3(32, 32), 0, s, partial, out0,
+                       partial + (int64_t)kNormBlocks * d, out1, blocks, d);
 }
 
 }  // namespace norms

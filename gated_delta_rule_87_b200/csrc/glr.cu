@@ -572,11 +572,12 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
   constexpr int TOK = FwdShape<IO, PAIRS, COMPLEMENT>::kTok;
   __shared__ TileShared sh;
   extern __shared__ __align__(128) unsigned char tile_bytes[];
+  init_barriers(sh);
+  wait_for_last();
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   auto &rows = reinterpret_cast<WarpRows<IO, TOK> *>(tile_bytes)[w];
   uint32_t ticket = 0, parity = 0;
-  init_barriers(sh);
   if (threadIdx.x == 0) ticket = next_ticket(p, sh, blockIdx.x - gridDim.x);
   __syncthreads();
   Place q = taken<false>(p, sh);
@@ -699,11 +700,12 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
   __shared__ TileShared sh;
   __shared__ Map2 states[kWarps][32];  // the warps' maps of the states
   extern __shared__ __align__(128) unsigned char tile_bytes[];
+  init_barriers(sh);
+  wait_for_last();
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   auto &rows = reinterpret_cast<WarpRowsBwd<IO, TOK> *>(tile_bytes)[w];
   uint32_t ticket = 0, parity = 0;
-  init_barriers(sh);
   if (threadIdx.x == 0) ticket = next_ticket(p, sh, blockIdx.x - gridDim.x);
   __syncthreads();
   Place q = taken<true>(p, sh);
@@ -838,6 +840,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
 // packed offsets, writes the status word and marks the tiles in which a
 // sequence begins or ends.
 __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words) {
+  let_next_start();
   if (blockIdx.x == 0) {
     bool bad = false;
     if (p.cu_seqlens)
@@ -1027,8 +1030,7 @@ cudaError_t launch_tiles(const char *name, size_t smem, const GlrArgs &p, const 
   if (e != cudaSuccess) return e;
   const int64_t tiles = p.tiles * p.stripes;
   TraceScope tr(name, s);
-  KERNEL<<<(unsigned)(tiles < most ? tiles : most), kThreads, smem, s>>>(p, maps);
-  return cudaGetLastError();
+  return launch_behind(KERNEL, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kThreads), smem, s, p, maps);
 }
 
 template <typename IO, bool PAIRS, bool COMPLEMENT, bool STATES_ONLY>
