@@ -155,6 +155,12 @@ struct Marks {
   uint32_t first, last;
   int row;
   __device__ __forceinline__ int row_of(int i) const { return __shfl_sync(0xffffffffu, row, i); }
+  // Whether one begins behind the first token, or ends before the last.  Those
+  // that begin and end with the warp's tokens (sequences of whole warps) take the
+  // path without marks.
+  template <int TOK> __device__ __forceinline__ bool inside() const {
+    return (first & ~1u) | (last & ~(1u << (TOK - 1)));
+  }
 };
 template <int TOK> __device__ __forceinline__ Marks find_marks(const GlrArgs &p, uint32_t t0, int lane) {
   static_assert(TOK <= 32, "a lane a token");
@@ -571,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, (FwdShape<IO, PAIRS, COMPLEMENT>::kB
 glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
   constexpr int TOK = FwdShape<IO, PAIRS, COMPLEMENT>::kTok;
   __shared__ TileShared sh;
+  __shared__ float2 start[kWarps][32];  // a state that a warp's tokens begin with
   extern __shared__ __align__(128) unsigned char tile_bytes[];
   init_barriers(sh);
   wait_for_last();
@@ -593,6 +600,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     m.first = m.last = 0;
     m.row = -1;
     if (marked) m = find_marks<TOK>(p, t0, lane);
+    const bool inside = m.inside<TOK>();
     alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
     const int buf = parity;
     parity ^= 1;
@@ -605,7 +613,10 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
       const float2 ai = decay<IO>(g);
       return fma2(ai, y, input<IO, COMPLEMENT>(g, ai, read_row<PAIRS>(rows.x[i], lane).value()));
     };
-    if (!marked) {
+    // An initial state is read once, before the map is published: the sequence's
+    // last tile may write the final state over it as soon as that is done.
+    if (!inside) {
+      if (m.first) start[w][lane] = h = load_row<PAIRS>(p, p.initial_state, m.row_of(0), l);
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
         const float2 g = g_row(i);
@@ -618,9 +629,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
 #pragma unroll
       for (int i = 0; i < TOK; ++i) h = fma2(a[i], h, b_of(i));
     } else {
-      // The state after a start takes the place of its g: the initial state is
-      // read once, before the map is published (the sequence's last tile may
-      // write the final state over it as soon as that is done).  Four at a time.
+      // The state after a start takes the place of its g.  Four at a time.
       for (uint32_t todo = m.first; todo;) {
         int at[4];
         float2 h0[4];
@@ -646,7 +655,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     if (p.chained && w == kWarps - 1 && (q.step + 1) % Chain<TOK>::kGroup != 0) publish_tile<PAIRS, false>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<false>(p, sh);
     const bool more = nq.step < p.tiles;
-    if (more && !marked) begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    if (more && !inside) begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
     const bool next_marked = more && has_marks(p, nq.tile);
     h = both(0.f);
     if (p.chained) {
@@ -662,12 +671,14 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     if (!STATES_ONLY) {
       IO *out = static_cast<IO *>(p.h) + (int64_t)t0 * p.D;
       const int n = l.any() ? tokens_of<TOK>(p, t0) : 0;
-      if (!marked) {
+      if (!inside) {
+        if (m.first) h = start[w][lane];
 #pragma unroll
         for (int i = 0; i < TOK; ++i) {
           h = fma2(a[i], h, b_of(i));
           if (i < n && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens)) store2<PAIRS>(out + (int64_t)i * p.D, l, h);
         }
+        if (m.last) store_state<PAIRS>(p, p.final_state, m.row_of(TOK - 1), l, h);
       } else {
 #pragma unroll 4
         for (int i = 0; i < TOK; ++i) {
@@ -680,7 +691,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
       if (q.tile == 0) pass_empty(p, p.initial_state, p.final_state, true, q.stripe * kWide, kWide);
     }
     if (!more) return;
-    if (marked) {
+    if (inside) {
       if (PAIRS) tc::fence_async_smem();  // states were written over rows of g
       begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
     }
@@ -723,6 +734,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     m.first = m.last = 0;
     m.row = -1;
     if (marked) m = find_marks<TOK>(p, t0, lane);
+    const bool inside = m.inside<TOK>();
     alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
     const int buf = parity;
     parity ^= 1;
@@ -741,7 +753,9 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
       const float2 g = g_row(i), ai = decay<IO>(g);
       return fma2(ai, y, input<IO, COMPLEMENT>(g, ai, x_row(i)));
     };
-    if (!marked) {
+    if (!inside) {
+      if (m.first) s = load_row<PAIRS>(p, p.initial_state, m.row_of(0), l);
+      if (m.last) r = load_row<PAIRS>(p, p.dfinal, m.row_of(TOK - 1), l);
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
         const float2 g = g_row(i);
@@ -778,7 +792,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     if (p.chained && w == 0 && (q.step + 1) % Chain<TOK>::kGroup != 0) publish_tile<PAIRS, true>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<true>(p, sh);
     const bool more = nq.step < p.tiles;
-    if (EARLY && more && !marked) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    if (EARLY && more && !inside) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
     const bool next_marked = more && has_marks(p, nq.tile);
     enter_warp<false>(states, w, lane, h);
     r = both(0.f);
@@ -803,7 +817,9 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
       }
     };
     auto less = [&](float2 y, float2 x) { return COMPLEMENT ? fma2(x, both(-1.f), y) : y; };
-    if (!marked) {
+    if (!inside) {
+      if (m.first) h = load_row<PAIRS>(p, p.initial_state, m.row_of(0), l);
+      if (m.last) r = load_row<PAIRS>(p, p.dfinal, m.row_of(TOK - 1), l);
       float2 past[TOK];
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
@@ -813,6 +829,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
       }
 #pragma unroll
       for (int i = TOK - 1; i >= 0; --i) write(i, d_of(i), a[i], past[i]);
+      if (m.first) store_state<PAIRS>(p, p.dinitial, m.row_of(0), l, r);
     } else {
       float2 past[TOK];  // (indexed by a running i: local memory)
 #pragma unroll 2
@@ -830,7 +847,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     }
     if (q.tile == 0) pass_empty(p, p.dfinal, p.dinitial, false, q.stripe * kWide, kWide);
     if (!more) return;
-    if (!EARLY || marked) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    if (!EARLY || inside) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
     marked = next_marked;
     q = nq;
   }

@@ -223,6 +223,31 @@ def test_two_graphs_that_share_a_workspace_take_turns():
         assert torch.equal(w[0], o[0]) and torch.equal(w[1], o[1])
 
 
+@pytest.mark.parametrize("io,T", [("bf16", 64), ("bf16", 96), ("f32", 48), ("f32", 64)])
+def test_sequences_of_whole_warps_in_a_pool(io, T):
+    """Starts and ends on the first and last tokens of warps, a state read and
+    written by different tiles; the gradients beside it."""
+    import torch
+    import gated_delta_rule_87_b200 as gdr
+    N, D = 70, 192
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    x, dh = _wide((N, T, D), 1, dt), _wide((N, T, D), 2, dt)
+    g, h0, df = _wide((N, T, D), 3, torch.float32).abs_().neg_(), _wide((N, D), 4, torch.float32), _wide((N, D), 5, torch.float32)
+    offsets, flat = [T * n for n in range(N + 1)], lambda t: _host(t).reshape(-1, D)  # noqa: E731
+    rh, rf, eh, ef = R.scan(flat(x), flat(g), _host(h0), offsets, False)
+    slots = torch.randperm(N, device="cuda").to(torch.int32)
+    for _ in range(5):
+        pool = torch.empty_like(h0)
+        pool[slots.long()] = h0
+        h = gdr.glr_scan_fwd(x, g, state_pool=pool, state_slots=slots)[0]
+        R.check(flat(h), rh, eh, io, "h")
+        R.check(_host(pool[slots.long()]), rf, ef, "f32", "pool")
+    dx, dg, dh0, _ = gdr.glr_scan_bwd(dh, x, g, h0, dfinal_state=df)
+    want, err = R.scan_bwd(flat(dh), _host(df), flat(x), flat(g), _host(h0), offsets, False)
+    for got, w, e, kind in zip((dx, dg, dh0), want, err, (io, "f32", "f32")):
+        R.check(flat(got), w, e, kind)
+
+
 def test_entries_that_share_a_slot_keep_to_their_own_results():
     """Two sequences of one call in one slot: each is right from the state that
     the slot held before, or from the other's; other slots keep theirs."""
