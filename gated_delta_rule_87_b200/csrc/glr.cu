@@ -33,7 +33,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kWide = 64;         // channels of a tile, two a lane
 
 // The two channels of a lane.  PAIRS: neighbours, rows and pointers aligned for
-// it (and for tensor-map copies); else 32 apart, any alignment.
+// it (and every row for tensor-map copies); else 32 apart, any alignment.
 template <bool PAIRS> struct Lane {
   int c;         // the first channel
   bool on[2];    // which exist
@@ -458,8 +458,8 @@ __device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
 
 // ---- the kernels --------------------------------------------------------
 // Persistent blocks of four warps; a tile is TOK tokens a warp and 64 channels.
-// Each warp copies its own rows to shared memory (a tensor-map copy a tensor, or
-// lane by lane where rows are not aligned) and waits for them alone.  In the
+// Each warp copies its own rows to shared memory (tensor-map copies) and waits
+// for them alone.  In the
 // first pass over a tile its rows go to registers, so that the next tile's
 // copies run while this one waits for what enters it and is written: one read
 // of each input.  What an SM moves is what its blocks hold (registers and the
@@ -467,15 +467,42 @@ __device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
 //
 // A tile in which a sequence begins or ends takes rolled loops instead, over the
 // rows in shared memory, and its block's next copies begin after it.
-template <typename IO, int TOK> struct WarpRows {
-  float g[TOK][kWide];
-  IO x[TOK][kWide];
+//
+// A tensor-map copy begins on 16 bytes.  Where rows do not, every R-th one (R
+// elements in 16 bytes) is as far past a boundary as the first: R maps, each of
+// every R-th row and from the boundary before it, reach them all, and lanes read
+// `shift` elements on.  (By lane copies of 4 or 2 bytes instead: 431 us against
+// 292 for 32767 x 4095 fp32, 347 against 234 for bf16.)
+struct Shift {  // of row i, where the first token's is s: s + i l
+  int s, l;
 };
-template <typename IO, int TOK> struct WarpRowsBwd : WarpRows<IO, TOK> {
-  IO dh[TOK][kWide];
+template <typename T> __device__ __forceinline__ Shift shift_of(const void *base, int64_t ld) {
+  constexpr int R = 16 / sizeof(T);
+  return {(int)(reinterpret_cast<uintptr_t>(base) / sizeof(T) % R), (int)(ld % R)};
+}
+// A warp's rows of one tensor in shared memory.
+template <typename T, int TOK, bool PAIRS> struct alignas(128) TensorRows {
+  static constexpr int R = PAIRS ? 1 : 16 / sizeof(T), kPitch = kWide + (PAIRS ? 0 : R);
+  static constexpr int kBox = TOK / R * kPitch * (int)sizeof(T), kBytes = R * kBox;  // a copy, and all
+  static_assert(TOK % R == 0, "the same row of every warp has the same shift");
+  T v[R][(kBox + 127) / 128 * 128 / sizeof(T)];
+  __device__ __forceinline__ T *row(int i, Shift q) {
+    return v[i % R] + i / R * kPitch + (PAIRS ? 0 : (q.s + i * q.l) & (R - 1));
+  }
 };
-struct GlrMaps {
-  CUtensorMap x, g, dh;
+template <typename IO, bool PAIRS, int TOK, bool BWD> struct WarpRows {
+  TensorRows<float, TOK, PAIRS> g;
+  TensorRows<IO, TOK, PAIRS> x;
+  static constexpr int kBytes = decltype(g)::kBytes + decltype(x)::kBytes;
+};
+template <typename IO, bool PAIRS, int TOK> struct WarpRows<IO, PAIRS, TOK, true> {
+  TensorRows<float, TOK, PAIRS> g;
+  TensorRows<IO, TOK, PAIRS> x, dh;
+  static constexpr int kBytes = decltype(g)::kBytes + 2 * decltype(x)::kBytes;
+};
+template <typename IO, bool PAIRS, bool BWD> struct GlrMaps {
+  static constexpr int kIO = PAIRS ? 1 : 16 / sizeof(IO), kF = PAIRS ? 1 : 4;
+  CUtensorMap g[kF], x[kIO], dh[BWD ? kIO : 1];
 };
 
 // Tokens of a warp that exist.
@@ -484,71 +511,23 @@ template <int TOK> __device__ __forceinline__ int tokens_of(const GlrArgs &p, ui
   return left <= 0 ? 0 : left < TOK ? (int)left : TOK;
 }
 
-// Lane copies of one tensor's rows; zeros where nothing is.
-template <typename IO, int TOK>
-__device__ __forceinline__ void copy_rows(const GlrArgs &p, IO (&to)[TOK][kWide], const void *from, int64_t ld,
-                                          uint32_t t0, const Lane<false> &l, int lane) {
-  const int n = tokens_of<TOK>(p, t0);
-  const bool whole = n == TOK && l.c - lane + kWide <= p.D && GDR_IN_BOUNDS((int64_t)t0 + TOK <= p.tokens);
-  const IO *src = static_cast<const IO *>(from) + (int64_t)t0 * ld + l.c;
-  if constexpr (sizeof(IO) == 4) {
-    if (whole) {
-#pragma unroll
-      for (int i = 0; i < TOK; ++i, src += ld)
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(&to[i][lane + 32 * v])),
-                       "l"(src + 32 * v) : "memory");
-      return;
-    }
-  } else if (whole) {  // a single bf16 is too short for an asynchronous copy
-    IO t[TOK][2];
-#pragma unroll
-    for (int i = 0; i < TOK; ++i, src += ld)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) t[i][v] = __ldg(src + 32 * v);
-#pragma unroll
-    for (int i = 0; i < TOK; ++i)
-#pragma unroll
-      for (int v = 0; v < 2; ++v) to[i][lane + 32 * v] = t[i][v];
-    return;
-  }
-  for (int i = 0; i < TOK; ++i, src += ld)
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const bool ok = i < n && l.on[v] && GDR_IN_BOUNDS((int64_t)t0 + i < p.tokens && l.c + 32 * v < p.D);
-      IO x = IO(0.f);
-      if (ok) x = __ldg(src + 32 * v);
-      to[i][lane + 32 * v] = x;
-    }
-}
-
 // Begins the copies of a warp's rows of a tile.
-template <typename IO, bool PAIRS, bool BWD, int TOK, typename ROWS>
-__device__ __forceinline__ void begin_copies(const GlrArgs &p, const GlrMaps &maps, ROWS &rows, uint64_t *full,
-                                             const Place &q, int w, int lane) {
-  const uint32_t t0 = q.tile * (kWarps * TOK) + w * TOK;
-  if constexpr (PAIRS) {
-    __syncwarp();  // the rows have been read by every lane
-    if (lane == 0) {
-      const int c0 = q.stripe * kWide;
-      tc::mbar_arrive_expect_tx(full, sizeof(ROWS));
-      tc::tma_load_2d(rows.g, &maps.g, c0, (int)t0, full);
-      tc::tma_load_2d(rows.x, &maps.x, c0, (int)t0, full);
-      if constexpr (BWD) tc::tma_load_2d(rows.dh, &maps.dh, c0, (int)t0, full);
-    }
-  } else {
-    const Lane<false> l(q.stripe, p.D);
-    copy_rows<float, TOK>(p, rows.g, p.g, p.ld_g, t0, l, lane);
-    copy_rows<IO, TOK>(p, rows.x, p.x, p.ld_x, t0, l, lane);
-    if constexpr (BWD) copy_rows<IO, TOK>(p, rows.dh, p.dh, p.ld_dh, t0, l, lane);
+template <typename IO, bool PAIRS, int TOK, bool BWD>
+__device__ __forceinline__ void begin_copies(const GlrMaps<IO, PAIRS, BWD> &maps, WarpRows<IO, PAIRS, TOK, BWD> &rows,
+                                             uint64_t *full, const Place &q, int w, int lane) {
+  using Maps = GlrMaps<IO, PAIRS, BWD>;
+  const int t0 = (int)(q.tile * (kWarps * TOK) + w * TOK), c0 = q.stripe * kWide;
+  __syncwarp();  // the rows have been read by every lane
+  if (lane == 0) tc::mbar_arrive_expect_tx(full, rows.kBytes);
+  if (!PAIRS) __syncwarp();
+  if (lane < Maps::kF) tc::tma_load_2d(rows.g.v[lane], &maps.g[lane], c0, t0 / Maps::kF, full);
+  if (lane < Maps::kIO) {
+    tc::tma_load_2d(rows.x.v[lane], &maps.x[lane], c0, t0 / Maps::kIO, full);
+    if constexpr (BWD) tc::tma_load_2d(rows.dh.v[lane], &maps.dh[lane], c0, t0 / Maps::kIO, full);
   }
 }
-template <bool PAIRS>
 __device__ __forceinline__ bool copies_done(const GlrArgs &p, uint64_t *full, uint32_t parity) {
-  if constexpr (PAIRS) return tc::mbar_wait_warp(full, parity, p.status, KDA_DEVICE_TIMEOUT);
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  return true;
+  return tc::mbar_wait_warp(full, parity, p.status, KDA_DEVICE_TIMEOUT);
 }
 __device__ __forceinline__ void init_barriers(TileShared &sh) {
   if (threadIdx.x < kWarps) tc::mbar_init(&sh.full[threadIdx.x], 1);
@@ -574,7 +553,7 @@ template <typename IO, bool COMPLEMENT> struct BwdShape {
 // Forward.  STATES_ONLY: only the saved chunk states are written.
 template <typename IO, bool PAIRS, bool COMPLEMENT, bool STATES_ONLY>
 __global__ void __launch_bounds__(kThreads, (FwdShape<IO, PAIRS, COMPLEMENT>::kBlocks))
-glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
+glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps<IO, PAIRS, false> maps) {
   constexpr int TOK = FwdShape<IO, PAIRS, COMPLEMENT>::kTok;
   __shared__ TileShared sh;
   __shared__ float2 start[kWarps][32];  // a state that a warp's tokens begin with
@@ -583,14 +562,15 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
   wait_for_last();
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  auto &rows = reinterpret_cast<WarpRows<IO, TOK> *>(tile_bytes)[w];
+  auto &rows = reinterpret_cast<WarpRows<IO, PAIRS, TOK, false> *>(tile_bytes)[w];
+  const Shift sg = shift_of<float>(p.g, p.ld_g), sx = shift_of<IO>(p.x, p.ld_x);
   uint32_t ticket = 0, parity = 0;
   if (threadIdx.x == 0) ticket = next_ticket(p, sh, blockIdx.x - gridDim.x);
   __syncthreads();
   Place q = taken<false>(p, sh);
   if (q.step >= p.tiles) return;
   __syncthreads();
-  begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], q, w, lane);
+  begin_copies(maps, rows, &sh.full[w], q, w, lane);
   bool marked = has_marks(p, q.tile), alive = true;
   while (true) {
     if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
@@ -601,17 +581,17 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     m.row = -1;
     if (marked) m = find_marks<TOK>(p, t0, lane);
     const bool inside = m.inside<TOK>();
-    alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
+    alive &= copies_done(p, &sh.full[w], parity);
     const int buf = parity;
     parity ^= 1;
     // the map of the warp's tokens
     float2 a[TOK], b[COMPLEMENT ? TOK : 1], gs = both(0.f), h = both(0.f);
     Raw<IO> x[COMPLEMENT ? 1 : TOK];
     auto b_of = [&](int i) { return COMPLEMENT ? b[COMPLEMENT ? i : 0] : x[COMPLEMENT ? 0 : i].value(); };
-    auto g_row = [&](int i) { return read_row<PAIRS>(rows.g[i], lane).value(); };
+    auto g_row = [&](int i) { return read_row<PAIRS>(rows.g.row(i, sg), lane).value(); };
     auto rolled = [&](int i, float2 g, float2 y) {  // the state after y by token i
       const float2 ai = decay<IO>(g);
-      return fma2(ai, y, input<IO, COMPLEMENT>(g, ai, read_row<PAIRS>(rows.x[i], lane).value()));
+      return fma2(ai, y, input<IO, COMPLEMENT>(g, ai, read_row<PAIRS>(rows.x.row(i, sx), lane).value()));
     };
     // An initial state is read once, before the map is published: the sequence's
     // last tile may write the final state over it as soon as that is done.
@@ -620,7 +600,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
         const float2 g = g_row(i);
-        const Raw<IO> xi = read_row<PAIRS>(rows.x[i], lane);
+        const Raw<IO> xi = read_row<PAIRS>(rows.x.row(i, sx), lane);
         a[i] = decay<IO>(g);
         if (COMPLEMENT) b[COMPLEMENT ? i : 0] = input<IO, COMPLEMENT>(g, a[i], xi.value());
         else x[COMPLEMENT ? 0 : i] = xi;
@@ -641,7 +621,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (at[k] >= 0) write_row<PAIRS>(rows.g[at[k]], lane, rolled(at[k], g_row(at[k]), h0[k]));
+          if (at[k] >= 0) write_row<PAIRS>(rows.g.row(at[k], sg), lane, rolled(at[k], g_row(at[k]), h0[k]));
       }
 #pragma unroll 4
       for (int i = 0; i < TOK; ++i) {
@@ -655,7 +635,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     if (p.chained && w == kWarps - 1 && (q.step + 1) % Chain<TOK>::kGroup != 0) publish_tile<PAIRS, false>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<false>(p, sh);
     const bool more = nq.step < p.tiles;
-    if (more && !inside) begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    if (more && !inside) begin_copies(maps, rows, &sh.full[w], nq, w, lane);
     const bool next_marked = more && has_marks(p, nq.tile);
     h = both(0.f);
     if (p.chained) {
@@ -692,8 +672,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     }
     if (!more) return;
     if (inside) {
-      if (PAIRS) tc::fence_async_smem();  // states were written over rows of g
-      begin_copies<IO, PAIRS, false, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+      tc::fence_async_smem();  // states were written over rows of g
+      begin_copies(maps, rows, &sh.full[w], nq, w, lane);
     }
     marked = next_marked;
     q = nq;
@@ -704,7 +684,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
 // from what enters it from the tokens after it (chained).
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 __global__ void __launch_bounds__(kThreads, (BwdShape<IO, COMPLEMENT>::kBlocks))
-glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps maps) {
+glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps<IO, PAIRS, true> maps) {
   constexpr bool EARLY = BwdShape<IO, COMPLEMENT>::kEarly;
   constexpr int TOK = BwdShape<IO, COMPLEMENT>::kTok;
   static_assert(kWarps * TOK == kGlrChunk, "a tile is a chunk: its saved state enters it");
@@ -715,14 +695,15 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
   wait_for_last();
   if (bad_offsets(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  auto &rows = reinterpret_cast<WarpRowsBwd<IO, TOK> *>(tile_bytes)[w];
+  auto &rows = reinterpret_cast<WarpRows<IO, PAIRS, TOK, true> *>(tile_bytes)[w];
+  const Shift sg = shift_of<float>(p.g, p.ld_g), sx = shift_of<IO>(p.x, p.ld_x), sd = shift_of<IO>(p.dh, p.ld_dh);
   uint32_t ticket = 0, parity = 0;
   if (threadIdx.x == 0) ticket = next_ticket(p, sh, blockIdx.x - gridDim.x);
   __syncthreads();
   Place q = taken<true>(p, sh);
   if (q.step >= p.tiles) return;
   __syncthreads();
-  begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], q, w, lane);
+  begin_copies(maps, rows, &sh.full[w], q, w, lane);
   bool marked = has_marks(p, q.tile), alive = true;
   while (true) {
     if (threadIdx.x == 0) ticket = next_ticket(p, sh, ticket);
@@ -735,14 +716,14 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     m.row = -1;
     if (marked) m = find_marks<TOK>(p, t0, lane);
     const bool inside = m.inside<TOK>();
-    alive &= copies_done<PAIRS>(p, &sh.full[w], parity);
+    alive &= copies_done(p, &sh.full[w], parity);
     const int buf = parity;
     parity ^= 1;
     float2 a[TOK];
     Raw<IO> xk[EARLY ? TOK : 1], dk[EARLY ? TOK : 1];
-    auto g_row = [&](int i) { return read_row<PAIRS>(rows.g[i], lane).value(); };
-    auto x_row = [&](int i) { return read_row<PAIRS>(rows.x[i], lane).value(); };
-    auto d_row = [&](int i) { return read_row<PAIRS>(rows.dh[i], lane).value(); };
+    auto g_row = [&](int i) { return read_row<PAIRS>(rows.g.row(i, sg), lane).value(); };
+    auto x_row = [&](int i) { return read_row<PAIRS>(rows.x.row(i, sx), lane).value(); };
+    auto d_row = [&](int i) { return read_row<PAIRS>(rows.dh.row(i, sd), lane).value(); };
     auto x_of = [&](int i) { return EARLY ? xk[EARLY ? i : 0].value() : x_row(i); };
     auto d_of = [&](int i) { return EARLY ? dk[EARLY ? i : 0].value() : d_row(i); };
     // the state after y by token i
@@ -760,8 +741,8 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
       for (int i = 0; i < TOK; ++i) {
         const float2 g = g_row(i);
         if (EARLY) {
-          xk[EARLY ? i : 0] = read_row<PAIRS>(rows.x[i], lane);
-          dk[EARLY ? i : 0] = read_row<PAIRS>(rows.dh[i], lane);
+          xk[EARLY ? i : 0] = read_row<PAIRS>(rows.x.row(i, sx), lane);
+          dk[EARLY ? i : 0] = read_row<PAIRS>(rows.dh.row(i, sd), lane);
         }
         a[i] = decay<IO>(g);
         gs = add2(gs, g);
@@ -792,7 +773,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     if (p.chained && w == 0 && (q.step + 1) % Chain<TOK>::kGroup != 0) publish_tile<PAIRS, true>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<true>(p, sh);
     const bool more = nq.step < p.tiles;
-    if (EARLY && more && !inside) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    if (EARLY && more && !inside) begin_copies(maps, rows, &sh.full[w], nq, w, lane);
     const bool next_marked = more && has_marks(p, nq.tile);
     enter_warp<false>(states, w, lane, h);
     r = both(0.f);
@@ -847,7 +828,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     }
     if (q.tile == 0) pass_empty(p, p.dfinal, p.dinitial, false, q.stripe * kWide, kWide);
     if (!more) return;
-    if (!EARLY || inside) begin_copies<IO, PAIRS, true, TOK>(p, maps, rows, &sh.full[w], nq, w, lane);
+    if (!EARLY || inside) begin_copies(maps, rows, &sh.full[w], nq, w, lane);
     marked = next_marked;
     q = nq;
   }
@@ -977,17 +958,25 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A warp's rows of a [tokens, D] tensor: boxes of `tok` tokens x 64 channels, zeros outside.
-bool make_map(CUtensorMap *m, const void *base, bool bf16, const GlrArgs &p, int64_t ld, int tok) {
+// Maps of a [tokens, D] tensor of type T for a warp's rows, zeros outside: N = 1,
+// boxes of `tok` tokens x 64 channels; else every N-th row of each of the first N,
+// from the 16-byte boundary at or before it, boxes of tok / N rows.
+template <typename T, int N> bool make_maps(CUtensorMap (&m)[N], const void *base, const GlrArgs &p, int64_t ld, int tok) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t e = bf16 ? 2 : 4;
-  cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)p.tokens}, strides[1] = {(cuuint64_t)ld * e};
-  cuuint32_t box[2] = {kWide, (cuuint32_t)tok}, estr[2] = {1, 1};
-  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-            const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  for (int k = 0; k < N; ++k) {
+    const bool there = k < p.tokens;  // (a row that is not is never looked at)
+    const uintptr_t at = reinterpret_cast<uintptr_t>(base) + (there ? k * ld * sizeof(T) : 0);
+    cuuint64_t dims[2] = {(cuuint64_t)p.D + at % 16 / sizeof(T), (cuuint64_t)(there ? (p.tokens - k + N - 1) / N : 1)};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * N * sizeof(T)};
+    cuuint32_t box[2] = {kWide + (N > 1 ? N : 0), (cuuint32_t)(tok / N)}, estr[2] = {1, 1};
+    if (fn(&m[k], sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+           reinterpret_cast<void *>(at / 16 * 16), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
 }
 
 cudaError_t launch_begin(const GlrArgs &p, cudaStream_t s) {
@@ -1039,8 +1028,8 @@ template <typename K> cudaError_t resident_blocks(K kernel, std::atomic<int> *ca
 }
 
 // Launches a scan kernel with as many blocks as run at once, or one a tile.
-template <auto KERNEL>
-cudaError_t launch_tiles(const char *name, size_t smem, const GlrArgs &p, const GlrMaps &maps, cudaStream_t s) {
+template <auto KERNEL, typename MAPS>
+cudaError_t launch_tiles(const char *name, size_t smem, const GlrArgs &p, const MAPS &maps, cudaStream_t s) {
   static std::atomic<int> cache[kCachedDevices];
   int most = 0;
   cudaError_t e = resident_blocks(KERNEL, cache, smem, &most);
@@ -1057,11 +1046,11 @@ cudaError_t launch_scan(const GlrArgs &a, cudaStream_t s) {
   cudaError_t e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, false, s);
-  GlrMaps maps;
-  if (PAIRS && !(make_map(&maps.x, p.x, p.bf16, p, p.ld_x, TOK) && make_map(&maps.g, p.g, false, p, p.ld_g, TOK)))
+  GlrMaps<IO, PAIRS, false> maps{};
+  if (!(make_maps<IO>(maps.x, p.x, p, p.ld_x, TOK) && make_maps<float>(maps.g, p.g, p, p.ld_g, TOK)))
     return cudaErrorInvalidValue;
   return launch_tiles<glr_scan_kernel<IO, PAIRS, COMPLEMENT, STATES_ONLY>>(
-      "glr_scan_kernel", kWarps * sizeof(WarpRows<IO, TOK>), p, maps, s);
+      "glr_scan_kernel", kWarps * sizeof(WarpRows<IO, PAIRS, TOK, false>), p, maps, s);
 }
 
 template <typename IO, bool PAIRS, bool COMPLEMENT>
@@ -1078,12 +1067,12 @@ cudaError_t launch_bwd(const GlrArgs &a, cudaStream_t s) {
   if (e == cudaSuccess) e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, true, s);
-  GlrMaps maps;
-  if (PAIRS && !(make_map(&maps.x, p.x, p.bf16, p, p.ld_x, TOK) && make_map(&maps.g, p.g, false, p, p.ld_g, TOK) &&
-                 make_map(&maps.dh, p.dh, p.bf16, p, p.ld_dh, TOK)))
+  GlrMaps<IO, PAIRS, true> maps{};
+  if (!(make_maps<IO>(maps.x, p.x, p, p.ld_x, TOK) && make_maps<float>(maps.g, p.g, p, p.ld_g, TOK) &&
+        make_maps<IO>(maps.dh, p.dh, p, p.ld_dh, TOK)))
     return cudaErrorInvalidValue;
   return launch_tiles<glr_gradient_kernel<IO, PAIRS, COMPLEMENT>>(
-      "glr_gradient_kernel", kWarps * sizeof(WarpRowsBwd<IO, TOK>), p, maps, s);
+      "glr_gradient_kernel", kWarps * sizeof(WarpRows<IO, PAIRS, TOK, true>), p, maps, s);
 }
 
 template <typename IO, bool PAIRS, bool COMPLEMENT>

@@ -376,7 +376,7 @@ KDA_API kda_status_t kda_chunk_fwd_host(const void *q, const void *k, const void
  *
  * Any D > 0 and T >= 0.  Rows start `ld` elements apart (>= D), the same for
  * every token of the batch.  Data pointers are aligned to their element size
- * (even D with rows aligned to two elements runs faster).  States,
+ * (rows that begin on 16 bytes, with even D, run faster).  States,
  * products and sums are fp32; only h is rounded to io_dtype.  A non-finite
  * value of one sequence never reaches another.  final_state may be the
  * buffer of initial_state.  An invalid cu_seqlens leaves every output
