@@ -32,7 +32,7 @@ add_norm_fwd_kernel(const __grid_constant__ AddNormArgs p) {
     float2 t[NV][NP], ss = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (ODD) {
+      if (ODD && !grp.whole[i]) {
         r[i].keep(grp.half[i]);
         y[i].keep(grp.half[i]);
       }
@@ -114,7 +114,7 @@ add_norm_bwd_kernel(const __grid_constant__ AddNormArgs p) {
       cdt[i] = dt[i];
       cdn[i] = dn[i];
       cy[i] = y[i];
-      if (ODD) {
+      if (ODD && !grp.whole[i]) {
         ct[i].keep(grp.half[i]);
         cdn[i].keep(grp.half[i]);
       }

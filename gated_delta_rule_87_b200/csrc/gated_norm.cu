@@ -80,7 +80,7 @@ gated_norm_fwd_kernel(const __grid_constant__ GatedNormArgs p) {
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (ODD) x[i].keep(grp.half[i]);
+      if (ODD && !grp.whole[i]) x[i].keep(grp.half[i]);
 #pragma unroll
       for (int j = 0; j < NP; ++j) ss = fma2(x[i].pair(j), x[i].pair(j), ss);
     }
@@ -147,7 +147,7 @@ gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
       cx[i] = x[i];
       cdy[i] = dy[i];
       cz[i] = z[i];
-      if (ODD) {
+      if (ODD && !grp.whole[i]) {
         cx[i].keep(grp.half[i]);
         cdy[i].keep(grp.half[i]);
         cz[i].keep(grp.half[i]);
