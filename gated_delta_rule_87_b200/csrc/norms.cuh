@@ -9,8 +9,8 @@
 // Accesses are 16 bytes wide on 16-byte boundaries of the whole tensor, whatever
 // the row length: a row that begins `shift` elements past a boundary is cut there
 // (its first and last pieces are then partial: read whole and cleared at use,
-// written element by element).  A group's rows are a multiple of 8 rows apart, so
-// its shift, and with it the columns of each thread, stay the same: the column
+// written element by element).  A group's rows are whole periods of the shifts (8
+// rows at most) apart, so its shift, and with it the columns of each thread, stay the same: the column
 // sums of the weights' gradients are held in registers, then summed over a block's
 // groups and over the blocks in a fixed order (no atomics: the same inputs give
 // the same bits).
@@ -278,6 +278,7 @@ __device__ __forceinline__ void write_partial(const Group<V, NV, LANES, ODD> &gr
 
 struct Plan {
   int lanes, nv, threads;  // lanes 0: a block a row
+  int period;              // rows after which their shifts repeat
   size_t smem;             // the columns of the kernel's vectors (a block), or the groups' column sums
 };
 // Pieces a thread of a block (the last: as many as the longest row needs).
@@ -294,6 +295,7 @@ template <int V, bool BACK> Plan plan(int d, int vectors, bool odd) {
   Plan q{};
   const int vecs = d % V == 0 ? d / V : (d + 2 * V - 2) / V;  // pieces of a row that begins anywhere
   q.nv = 1;
+  for (q.period = 1; q.period * (d % V) % V != 0;) q.period *= 2;
   if (vecs <= 64) {
     q.lanes = V == 1 ? 32 : vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
     q.nv = vecs <= 32 ? 1 : 2;
@@ -350,15 +352,16 @@ template <auto KERNEL> cudaError_t resident_blocks(const Plan &q, int *blocks) {
 }
 
 // Launches a norm kernel over `rows` rows; `blocks` becomes its grid.  A group's
-// rows are `blocks` times its block's groups apart: a multiple of 8 where the
-// rows' shifts differ and a group has more than one.
+// rows are `blocks` times its block's groups apart: a multiple of the period of
+// the rows' shifts where a group has more than one (all 148 blocks of a full
+// grid where that is 4 or less, else 144).
 template <auto KERNEL, typename ARGS>
 cudaError_t launch_rows(const char *name, const ARGS &p, const Plan &q, int64_t rows, cudaStream_t s, int *blocks) {
   int most = 0;
   cudaError_t e = resident_blocks<KERNEL>(q, &most);
   if (e != cudaSuccess) return e;
   if (most > kNormBlocks) most = kNormBlocks;
-  if (most >= 8) most -= most % 8;
+  if (most >= q.period) most -= most % q.period;
   const int per = q.lanes ? q.threads / q.lanes : 1;
   const int64_t want = (rows + per - 1) / per;
   *blocks = (int)(want < most ? want : most);
