@@ -2,6 +2,9 @@
 //     t = residual + scale y,  n = t r w,   u = t r,  r = 1 / sqrt(mean(t^2) + eps)
 //     d = dt + r (dn w - u mean(dn w u)),  dresidual = d,  dy = scale d,
 //     dw = sum over rows of dn u,  dscale = sum of d y
+// 8192 x 4096 with an fp32 residual: 66 us = 6.1 TB/s, gradient 103 = 5.9; in bf16 52
+// and 83 us = 5.2 and 4.9 TB/s (a block a row: the sum over it and the
+// instructions around it show).  8192 x 4095 bf16: 64 and 99 us.
 #include "norms.cuh"
 
 namespace gdr {

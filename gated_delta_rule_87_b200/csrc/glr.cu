@@ -465,8 +465,14 @@ __device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
 // of each input.  What an SM moves is what its blocks hold (registers and the
 // copies under way) over the time a tile takes, two or three L2 round trips.
 //
-// A tile in which a sequence begins or ends takes rolled loops instead, over the
-// rows in shared memory, and its block's next copies begin after it.
+// A warp with a sequence start or end inside its tokens takes rolled loops instead,
+// over the rows in shared memory, and its next copies begin after them (256
+// sequences of 64 x 4096 bf16, all of whole warps: 83 us; by rolled loops 127).
+//
+// Bound by HBM where rows are long (32768 x 4096: bf16 173 us = 6.2 TB/s of 2e + 4
+// bytes an element, fp32 259 us = 6.2; a copy does 6.5), with few columns by the
+// chain (65536 x 256 bf16: 42 us = 3.2 TB/s).  The complement forms 1 - a, 8 warps
+// an SM: by its instructions (bf16 230 us).
 //
 // A tensor-map copy begins on 16 bytes.  Where rows do not, every R-th one (R
 // elements in 16 bytes) is as far past a boundary as the first: R maps, each of
@@ -681,7 +687,8 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
 }
 
 // Backward: the states again from what enters the tile (saved), the gradients
-// from what enters it from the tokens after it (chained).
+// from what enters it from the tokens after it (chained).  32768 x 4096: bf16 324
+// us = 5.8 TB/s of 3e + 8 bytes an element, fp32 429 us = 6.3; complement 386, 505.
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 __global__ void __launch_bounds__(kThreads, (BwdShape<IO, COMPLEMENT>::kBlocks))
 glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps<IO, PAIRS, true> maps) {
@@ -880,7 +887,8 @@ __global__ void __launch_bounds__(256) glr_no_tokens_kernel(GlrArgs p, bool back
   for (int c = threadIdx.x; c < p.D; c += blockDim.x) dst[r * p.D + c] = src ? src[r * p.D + c] : 0.f;
 }
 
-// One token for each sequence, the state in place.
+// One token for each sequence, the state in place: a thread a pair of channels, one
+// pass.  16 x 2048 to 256 x 4096 bf16: 11 us a call, the host's time for it.
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 __global__ void __launch_bounds__(256) glr_step_kernel(GlrArgs p) {
   constexpr int V = PAIRS ? 2 : 1;

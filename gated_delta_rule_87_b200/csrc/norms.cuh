@@ -28,8 +28,8 @@ namespace norms {
 // more rows fit an SM (a thread's addresses and counters cost as many registers as
 // a piece).  Backward, with column sums in registers too, one piece each and the
 // next row's loads under way was faster (8192 x 4096 bf16: 82 us, with two pieces
-// 111; the loads through shared memory instead of registers: 76, but 146 against
-// 107 with an fp32 residual).
+// 111, with two rows under way 89; the loads through shared memory instead of
+// registers: 76, but 146 against 107 with an fp32 residual).
 template <int V, bool BACK> constexpr int kBlockThreads = V == 1 || BACK ? 640 : 288;
 constexpr int kMostThreads = 640;
 constexpr int kCachedDevices = 64;
