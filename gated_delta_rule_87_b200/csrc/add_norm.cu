@@ -49,7 +49,7 @@ add_norm_fwd_kernel(const __grid_constant__ AddNormArgs p) {
       if (live && grp.any[i] && GDR_IN_BOUNDS(row < p.rows))
         store_piece<RES, V>(static_cast<RES *>(p.residual_out) + row * p.D, grp.c[i], grp.whole[i], grp.half[i], t[i]);
     }
-    const float2 inv = both(rsqrtf(grp.sum(ss.x + ss.y, 0.f).x / (float)p.D + p.eps));
+    const float2 inv = both(rsqrtf(grp.sum(ss.x + ss.y) / (float)p.D + p.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float2 w[NP];

@@ -86,7 +86,7 @@ gated_norm_fwd_kernel(const __grid_constant__ GatedNormArgs p) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) ss = fma2(x[i].pair(j), x[i].pair(j), ss);
     }
-    const float2 inv = both(rsqrtf(grp.sum(ss.x + ss.y, 0.f).x / (float)p.d + p.eps));
+    const float2 inv = both(rsqrtf(grp.sum(ss.x + ss.y) / (float)p.d + p.eps));
     IO *y = static_cast<IO *>(p.y) + row * p.d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
