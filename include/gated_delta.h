@@ -366,13 +366,16 @@ KDA_API kda_status_t kda_chunk_fwd_host(const void *q, const void *k, const void
  *   state_slots, num_slots
  *                 as kda_chunk_fwd_ex: the states are pools [num_slots, D],
  *                 sequence n reads and writes row state_slots[n]; a slot
- *                 outside the pool starts from zeros and stores nothing
+ *                 outside the pool starts from zeros and stores nothing; slots
+ *                 of different sequences must differ (of two that share one,
+ *                 either may find the other's state there)
  *   chunk_states  fp32, glr_chunk_states_size() bytes, written, or NULL: the
  *                 state that enters each chunk of 64 tokens of the token
  *                 axis, which glr_scan_bwd takes to read each input once
  *   cu_seqlens    as kda_chunk_fwd (packed sequences, B = 1); NULL: B dense
  *                 sequences of T tokens
- *   workspace     glr_scan_fwd_workspace_size() bytes, 256-byte aligned
+ *   workspace     glr_scan_fwd_workspace_size() bytes, 256-byte aligned; of one
+ *                 call at a time, also of calls replayed from graphs
  *
  * Any D > 0 and T >= 0.  Rows start `ld` elements apart (>= D), the same for
  * every token of the batch.  Data pointers are aligned to their element size
@@ -474,7 +477,7 @@ KDA_API kda_status_t kda_gated_norm_bwd(const void *dy, int64_t ld_dy, const voi
  *     n            = residual_out / sqrt(mean(residual_out^2) + eps) * weight
  *
  *   residual, residual_out  [rows, D] res_dtype; may be the same buffer
- *   y, n          [rows, D] io_dtype
+ *   y, n          [rows, D] io_dtype; may be the same buffer
  *   scale, weight [D] fp32, or NULL (ones)
  * res_dtype is io_dtype, or KDA_F32 with bf16 activations.  The norm is taken
  * of the fp32 sum, before residual_out is rounded.  D up to 16384; eps > 0.
@@ -483,7 +486,8 @@ KDA_API kda_status_t kda_gated_norm_bwd(const void *dy, int64_t ld_dy, const voi
  *   dn            [rows, D] io_dtype;  dresidual_out [rows, D] res_dtype, or
  *                 NULL for zeros;  residual_out as the forward call wrote it
  *   y, scale      as in the forward call (y is read only for dscale)
- *   dresidual     [rows, D] res_dtype, written (may be dresidual_out's buffer)
+ *   dresidual     [rows, D] res_dtype, written (may be the buffer of
+ *                 dresidual_out or of residual_out)
  *   dy            [rows, D] io_dtype, written, or NULL (without a scale and
  *                 with one type it equals dresidual)
  *   dscale, dweight  [D] fp32, written, or NULL; summed in a fixed order.  They
