@@ -6,6 +6,11 @@ arguments: every step of the computation runs in the library's CUDA kernels.
 PyTorch is used for device memory and streams.  There is no CPU path: if the
 library is missing or no CUDA device is present the calls raise.
 
+``stream`` is the stream that a call runs on (default: the current one of the
+tensors' device).  Outputs and workspaces that a call allocates belong to it, and
+tensors of other streams that it is given are kept until it is past them; the
+caller orders it with the streams that write those tensors and read the results.
+
 Operator (thethings.ai "The argument, in one page", table "Everything, in
 one table", rows "KDA" and "Gated DeltaNet"; column-vector keys):
 
@@ -231,6 +236,38 @@ def _stream_handle(stream, device) -> int:
     return s.cuda_stream
 
 
+def _raw_stream(torch, dev) -> int:
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 1.3 us less than the Stream object
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _here(torch, dev, stream) -> bool:
+    """Whether ``dev`` is the current device and ``stream`` (None: any) its current stream."""
+    return torch.cuda.current_device() == dev and (stream is None
+                                                   or stream.cuda_stream == _raw_stream(torch, dev))
+
+
+def _there(torch, dev, stream, call, *args, **kw):
+    """``call`` with ``dev`` and ``stream`` as the current ones.  What it allocates
+    (outputs, workspace) then belongs to the stream that uses it: memory freed on
+    another stream is not written while that one still reads it, and a workspace
+    that the caller drops is not handed out again before the stream is past it.
+    Tensors of other streams are recorded, so the same holds for them."""
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
+        elif stream.device.index != dev:
+            raise ValueError(f"stream must belong to CUDA device {dev}")
+        with torch.cuda.stream(stream):
+            out = call(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+        return out
+
+
 def _f32(t, name):
     torch = _torch()
     if t is not None and t.dtype != torch.float32:
@@ -275,6 +312,10 @@ def _chunk_fwd(gate, q, k, v, g, beta, initial_state, cu_seqlens, output_final_s
                o, final_state, workspace, stream, order=ERASE_THEN_DECAY, state_pool=None,
                state_slots=None):
     torch = _torch()
+    if stream is not None and q.is_cuda and not _here(torch, q.get_device(), stream):
+        return _there(torch, q.get_device(), stream, _chunk_fwd, gate, q, k, v, g, beta,
+                      initial_state, cu_seqlens, output_final_state, o, final_state, workspace,
+                      None, order, state_pool, state_slots)
     if q.dim() != 4:
         raise ValueError("q, k, v must be [B, T, H, d]")
     B, T, H_qk, d_k = q.shape
@@ -348,12 +389,17 @@ def kda_chunk_fwd_host(q, k, v, g, beta, initial_state=None, *, o, final_state=N
     torch = _torch()
     if q.is_cuda or o.is_cuda:
         raise ValueError("kda_chunk_fwd_host takes host tensors")
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    index = torch.device(dev).index if not isinstance(dev, int) else dev
+    if stream is not None and index is not None and not _here(torch, index, stream):
+        return _there(torch, index, stream, kda_chunk_fwd_host, q, k, v, g, beta, initial_state,
+                      o=o, final_state=final_state, device_buffer=device_buffer, pieces=pieces,
+                      device=dev)
     B, T, H, d_k = q.shape
     d_v = v.shape[3]
     io = _dtype_code(q)
     _f32(g, "g"), _f32(beta, "beta"), _f32(initial_state, "initial_state")
     _f32(final_state, "final_state")
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
     L = lib()
     need = int(L.kda_chunk_fwd_host_buffer_size(B, T, H, d_k, d_v, io, pieces))
     if device_buffer is None or device_buffer.numel() < need:
@@ -380,6 +426,9 @@ def gdn_chunk_fwd(q, k, v, g, beta, initial_state=None, cu_seqlens=None, *,
 
 def _decode(gate, q, k, v, g, beta, state, o, stream):
     torch = _torch()
+    if stream is not None and q.is_cuda and not _here(torch, q.get_device(), stream):
+        return _there(torch, q.get_device(), stream, _decode, gate, q, k, v, g, beta, state, o,
+                      None)
     N, H_qk, d_k = q.shape
     H_v, d_v = v.shape[1], v.shape[2]
     io = _dtype_code(q)
@@ -398,6 +447,9 @@ def _decode(gate, q, k, v, g, beta, state, o, stream):
 
 def _recurrent(gate, q, k, v, g, beta, state, state_slots, order, o, stream):
     torch = _torch()
+    if stream is not None and q.is_cuda and not _here(torch, q.get_device(), stream):
+        return _there(torch, q.get_device(), stream, _recurrent, gate, q, k, v, g, beta, state,
+                      state_slots, order, o, None)
     if q.dim() != 4:
         raise ValueError("q, k, v must be [N, T, H, d]")
     N, T, H_qk, d_k = q.shape
@@ -439,6 +491,8 @@ def gdn_recurrent_fwd(q, k, v, g, beta, state, *, state_slots=None, o=None, stre
 def state_gather(pool, state_slots, *, out=None, stream=None):
     """out[n] = pool[state_slots[n]] (zeros for a slot outside the pool)."""
     torch = _torch()
+    if stream is not None and pool.is_cuda and not _here(torch, pool.get_device(), stream):
+        return _there(torch, pool.get_device(), stream, state_gather, pool, state_slots, out=out)
     _f32(pool, "pool")
     N = state_slots.numel()
     _slots(state_slots, pool, N)
@@ -453,6 +507,9 @@ def state_gather(pool, state_slots, *, out=None, stream=None):
 
 def state_scatter(src, pool, state_slots, *, stream=None):
     """pool[state_slots[n]] = src[n] (skipped for a slot outside the pool)."""
+    torch = _torch()
+    if stream is not None and pool.is_cuda and not _here(torch, pool.get_device(), stream):
+        return _there(torch, pool.get_device(), stream, state_scatter, src, pool, state_slots)
     _f32(src, "src"), _f32(pool, "pool")
     N = state_slots.numel()
     _slots(state_slots, pool, N)
@@ -543,17 +600,6 @@ def _device_of(t) -> int:
     return dev
 
 
-def _current(torch, dev) -> bool:
-    return torch.cuda.current_device() == dev
-
-
-def _stream_of(torch, stream, dev) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 1.3 us less than the Stream object
-    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
-
-
 def _like(torch, t):
     """An empty contiguous tensor of t's shape, type and device."""
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
@@ -605,13 +651,12 @@ def glr_scan_fwd(x, g, initial_state=None, cu_seqlens=None, *, input_gate: str =
     reads.  Returns (h, final_state, chunk_states, workspace)."""
     torch = _torch()
     dev = _device_of(x)
-    if not _current(torch, dev):
-        with torch.cuda.device(dev):
-            return glr_scan_fwd(
-                x, g, initial_state, cu_seqlens, input_gate=input_gate,
-                output_final_state=output_final_state, output_chunk_states=output_chunk_states,
-                h=h, final_state=final_state, chunk_states=chunk_states, workspace=workspace,
-                stream=stream, state_pool=state_pool, state_slots=state_slots)
+    if not _here(torch, dev, stream):
+        return _there(torch, dev, stream, glr_scan_fwd, x, g, initial_state, cu_seqlens,
+                      input_gate=input_gate, output_final_state=output_final_state,
+                      output_chunk_states=output_chunk_states, h=h, final_state=final_state,
+                      chunk_states=chunk_states, workspace=workspace, state_pool=state_pool,
+                      state_slots=state_slots)
     io, code, f32, L = _dtype_code(x), _glr_input(input_gate), torch.float32, lib()
     B, T, D, N, cup = _glr_shape(torch, x, cu_seqlens, dev)
     shape, chunks = (B, T, D), (-(-B * T // GLR_CHUNK), D)
@@ -640,7 +685,7 @@ def glr_scan_fwd(x, g, initial_state=None, cu_seqlens=None, *, input_gate: str =
         _dense(initial_state, (rows, D), f32, "initial_state", dev),
         _dense(final_state, (rows, D), f32, "final_state", dev), slots, rows,
         _dense(chunk_states, chunks, f32, "chunk_states", dev), cup, N, B, T, D, code, io, wp, have,
-        _stream_of(torch, stream, dev)), "glr_scan_fwd")
+        _raw_stream(torch, dev)), "glr_scan_fwd")
     return h, final_state, chunk_states, workspace
 
 
@@ -653,13 +698,11 @@ def glr_scan_bwd(dh, x, g, initial_state=None, cu_seqlens=None, *, input_gate: s
     (None: computed again).  Returns (dx, dg, dinitial_state, workspace)."""
     torch = _torch()
     dev = _device_of(x)
-    if not _current(torch, dev):
-        with torch.cuda.device(dev):
-            return glr_scan_bwd(
-                dh, x, g, initial_state, cu_seqlens, input_gate=input_gate,
-                dfinal_state=dfinal_state, chunk_states=chunk_states,
-                output_dinitial_state=output_dinitial_state, dx=dx, dg=dg,
-                dinitial_state=dinitial_state, workspace=workspace, stream=stream)
+    if not _here(torch, dev, stream):
+        return _there(torch, dev, stream, glr_scan_bwd, dh, x, g, initial_state, cu_seqlens,
+                      input_gate=input_gate, dfinal_state=dfinal_state, chunk_states=chunk_states,
+                      output_dinitial_state=output_dinitial_state, dx=dx, dg=dg, dinitial_state=dinitial_state,
+                      workspace=workspace)
     io, code, f32, L = _dtype_code(x), _glr_input(input_gate), torch.float32, lib()
     B, T, D, N, cup = _glr_shape(torch, x, cu_seqlens, dev)
     shape, chunks, states = (B, T, D), (-(-B * T // GLR_CHUNK), D), (N, D)
@@ -682,7 +725,7 @@ def glr_scan_bwd(dh, x, g, initial_state=None, cu_seqlens=None, *, input_gate: s
         _dense(chunk_states, chunks, f32, "chunk_states", dev),
         _dense(dx, shape, x.dtype, "dx", dev), _dense(dg, shape, f32, "dg", dev),
         _dense(dinitial_state, states, f32, "dinitial_state", dev), cup, N, B, T, D, code, io, wp,
-        have, _stream_of(torch, stream, dev)), "glr_scan_bwd")
+        have, _raw_stream(torch, dev)), "glr_scan_bwd")
     return dx, dg, dinitial_state, workspace
 
 
@@ -693,10 +736,9 @@ def glr_step(x, g, state, *, state_slots=None, input_gate: str = "given", h=None
     entry), is updated in place.  Returns h [N,D]."""
     torch = _torch()
     dev = _device_of(x)
-    if not _current(torch, dev):
-        with torch.cuda.device(dev):
-            return glr_step(x, g, state, state_slots=state_slots, input_gate=input_gate, h=h,
-                            stream=stream)
+    if not _here(torch, dev, stream):
+        return _there(torch, dev, stream, glr_step, x, g, state, state_slots=state_slots,
+                      input_gate=input_gate, h=h)
     if x.dim() != 2:
         raise ValueError("x must be [N, D]")
     io, code, f32, shape = _dtype_code(x), _glr_input(input_gate), torch.float32, x.shape
@@ -711,7 +753,7 @@ def glr_step(x, g, state, *, state_slots=None, input_gate: str = "given", h=None
     _done(lib().glr_step(
         xp, ld_x, gp, ld_g, _dense(h, shape, x.dtype, "h", dev),
         _dense(state, (rows, D), f32, "state", dev), slots, rows, N, D, code, io,
-        _stream_of(torch, stream, dev)), "glr_step")
+        _raw_stream(torch, dev)), "glr_step")
     return h
 
 
@@ -740,9 +782,8 @@ def gated_norm_fwd(x, z=None, weight=None, *, gate: Optional[str] = "silu", eps:
     fp32 [d] or None; ``gate`` "silu", "sigmoid" or None (then no z).  Returns y."""
     torch = _torch()
     dev = _device_of(x)
-    if not _current(torch, dev):
-        with torch.cuda.device(dev):
-            return gated_norm_fwd(x, z, weight, gate=gate, eps=eps, y=y, stream=stream)
+    if not _here(torch, dev, stream):
+        return _there(torch, dev, stream, gated_norm_fwd, x, z, weight, gate=gate, eps=eps, y=y)
     code, io, dtype, shape = _gate_code(gate, z), _dtype_code(x), x.dtype, x.shape
     tokens, H, d = _heads(shape)
     xp, ld_x = _rows(x, shape, dtype, "x", dev, 2)
@@ -752,7 +793,7 @@ def gated_norm_fwd(x, z=None, weight=None, *, gate: Optional[str] = "silu", eps:
     _done(lib().kda_gated_norm_fwd(
         xp, ld_x, zp, ld_z, _dense(weight, (d,), torch.float32, "weight", dev),
         _dense(y, shape, dtype, "y", dev), tokens, H, d, eps, code, io,
-        _stream_of(torch, stream, dev)), "kda_gated_norm_fwd")
+        _raw_stream(torch, dev)), "kda_gated_norm_fwd")
     return y
 
 
@@ -763,11 +804,9 @@ def gated_norm_bwd(dy, x, z=None, weight=None, *, gate: Optional[str] = "silu",
     None without a gate, dweight None without a weight."""
     torch = _torch()
     dev = _device_of(x)
-    if not _current(torch, dev):
-        with torch.cuda.device(dev):
-            return gated_norm_bwd(dy, x, z, weight, gate=gate, eps=eps,
-                                  output_dweight=output_dweight, dx=dx, dz=dz, dweight=dweight,
-                                  workspace=workspace, stream=stream)
+    if not _here(torch, dev, stream):
+        return _there(torch, dev, stream, gated_norm_bwd, dy, x, z, weight, gate=gate, eps=eps,
+                      output_dweight=output_dweight, dx=dx, dz=dz, dweight=dweight, workspace=workspace)
     code, io, dtype, shape, f32 = _gate_code(gate, z), _dtype_code(x), x.dtype, x.shape, torch.float32
     tokens, H, d = _heads(shape)
     dp, ld_dy = _rows(dy, shape, dtype, "dy", dev, 2)
@@ -793,7 +832,7 @@ def gated_norm_bwd(dy, x, z=None, weight=None, *, gate: Optional[str] = "silu",
         dp, ld_dy, xp, ld_x, zp, ld_z, _dense(weight, (d,), f32, "weight", dev),
         _dense(dx, shape, dtype, "dx", dev), _dense(dz, shape, dtype, "dz", dev),
         _dense(dweight, (d,), f32, "dweight", dev), tokens, H, d, eps, code, io, wp, have,
-        _stream_of(torch, stream, dev)), "kda_gated_norm_bwd")
+        _raw_stream(torch, dev)), "kda_gated_norm_bwd")
     return dx, dz, dweight, workspace
 
 
@@ -814,10 +853,9 @@ def add_norm_fwd(residual, y, weight=None, scale=None, *, eps: float = 1e-6, res
     ``residual_out`` may be ``residual`` itself.  Returns (residual_out, n)."""
     torch = _torch()
     dev = _device_of(residual)
-    if not _current(torch, dev):
-        with torch.cuda.device(dev):
-            return add_norm_fwd(residual, y, weight, scale, eps=eps, residual_out=residual_out,
-                                n=n, stream=stream)
+    if not _here(torch, dev, stream):
+        return _there(torch, dev, stream, add_norm_fwd, residual, y, weight, scale, eps=eps,
+                      residual_out=residual_out, n=n)
     shape, f32 = residual.shape, torch.float32
     rows, D = _width(shape)
     res, io = _dtype_code(residual), _dtype_code(y)
@@ -830,7 +868,7 @@ def add_norm_fwd(residual, y, weight=None, scale=None, *, eps: float = 1e-6, res
         _dense(scale, (D,), f32, "scale", dev), _dense(weight, (D,), f32, "weight", dev),
         _dense(residual_out, shape, residual.dtype, "residual_out", dev),
         _dense(n, shape, y.dtype, "n", dev), rows, D, eps, res, io,
-        _stream_of(torch, stream, dev)), "kda_add_norm_fwd")
+        _raw_stream(torch, dev)), "kda_add_norm_fwd")
     return residual_out, n
 
 
@@ -844,11 +882,10 @@ def add_norm_bwd(dn, dresidual_out, residual_out, y=None, weight=None, scale=Non
     weight (a scale)."""
     torch = _torch()
     dev = _device_of(residual_out)
-    if not _current(torch, dev):
-        with torch.cuda.device(dev):
-            return add_norm_bwd(dn, dresidual_out, residual_out, y, weight, scale, eps=eps,
-                                dresidual=dresidual, dy=dy, dscale=dscale, dweight=dweight,
-                                workspace=workspace, stream=stream)
+    if not _here(torch, dev, stream):
+        return _there(torch, dev, stream, add_norm_bwd, dn, dresidual_out, residual_out, y, weight,
+                      scale, eps=eps, dresidual=dresidual, dy=dy, dscale=dscale, dweight=dweight,
+                      workspace=workspace)
     shape, f32, where = residual_out.shape, torch.float32, residual_out.device
     rows, D = _width(shape)
     res, io, dtype, rdtype = _dtype_code(residual_out), _dtype_code(dn), dn.dtype, residual_out.dtype
@@ -880,7 +917,7 @@ def add_norm_bwd(dn, dresidual_out, residual_out, y=None, weight=None, scale=Non
         _dense(scale, (D,), f32, "scale", dev), _dense(weight, (D,), f32, "weight", dev),
         _dense(dresidual, shape, rdtype, "dresidual", dev), _dense(dy, shape, dtype, "dy", dev),
         _dense(dscale, (D,), f32, "dscale", dev), _dense(dweight, (D,), f32, "dweight", dev), rows, D,
-        eps, res, io, wp, have, _stream_of(torch, stream, dev)), "kda_add_norm_bwd")
+        eps, res, io, wp, have, _raw_stream(torch, dev)), "kda_add_norm_bwd")
     return dresidual, dresidual if shared else dy, dweight, dscale, workspace
 
 
