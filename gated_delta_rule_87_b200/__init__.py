@@ -65,7 +65,8 @@ EXPORTED_SYMBOLS = (
     "kda_state_scatter", "kda_selftest_wait_timeout", "kda_bounds_checked",
     "kda_bounds_violations", "kda_chunk_fwd_host", "kda_chunk_fwd_host_buffer_size",
     "glr_chunk_states_size", "glr_scan_fwd_workspace_size", "glr_scan_fwd",
-    "glr_scan_bwd_workspace_size", "glr_scan_bwd", "glr_step", "kda_gated_norm_fwd",
+    "glr_scan_bwd_workspace_size", "glr_scan_bwd", "glr_selftest_wait_timeout", "glr_step",
+    "kda_gated_norm_fwd",
     "kda_gated_norm_bwd_workspace_size", "kda_gated_norm_bwd", "kda_add_norm_fwd",
     "kda_add_norm_bwd_workspace_size", "kda_add_norm_bwd",
 )
@@ -106,6 +107,7 @@ _SIGS = {
                      + [_int, _int, _vp, _sz, _vp], _int),
     "glr_scan_bwd": ([_vp, _i64, _vp, _vp, _i64, _vp, _i64] + [_vp] * 6 + [_i32] * 4
                      + [_int, _int, _vp, _sz, _vp], _int),
+    "glr_selftest_wait_timeout": ([_i32] + [_vp] * 4 + [_i32, _i32, _vp, _sz, _vp], _int),
     "glr_step": ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _int, _int, _vp], _int),
     "kda_gated_norm_fwd": ([_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _f, _int, _int, _vp],
                            _int),

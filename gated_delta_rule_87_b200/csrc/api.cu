@@ -657,6 +657,7 @@ kda_status_t check_glr(gdr::GlrArgs &a, int32_t B, glr_input_t input, kda_dtype_
   a.chunks = L.tiles;
   a.status = reinterpret_cast<int32_t *>(w);
   a.ticket = a.status + 32;
+  a.max_polls = gdr::kGlrMaxPolls;
   a.pitch = L.pitch;
   a.tile_marks = reinterpret_cast<int32_t *>(w + L.marks);
   a.tile_map = reinterpret_cast<uint64_t *>(w + L.map);
@@ -731,6 +732,25 @@ kda_status_t glr_scan_bwd(const void *dh, int64_t ld_dh, const float *dfinal_sta
     return fail(KDA_ERR_INVALID_ARG, "dinitial_state must not alias initial_state or dfinal_state");
   cudaError_t e = gdr::launch_glr_bwd(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : cuda_fail(e, "scan gradient launch");
+}
+
+kda_status_t glr_selftest_wait_timeout(int32_t backward, const float *x, const float *g, float *out,
+                                       float *dg, int32_t T, int32_t D, void *workspace,
+                                       size_t workspace_bytes, void *stream) {
+  constexpr int kSkipped = gdr::kGlrGroup * gdr::kGlrChunk;  // tokens of a group of fp32 tiles
+  gdr::GlrArgs a{};
+  a.x = x; a.ld_x = D; a.g = g; a.ld_g = D; a.T = T; a.D = D;
+  if (backward) { a.dh = x; a.ld_dh = D; a.dx = out; a.dg = dg; }
+  else a.h = out;
+  kda_status_t st = check_glr(a, 1, GLR_INPUT_GIVEN, KDA_F32, workspace, workspace_bytes, backward);
+  if (st != KDA_OK) return st;
+  if (T <= kSkipped) return fail(KDA_ERR_INVALID_ARG, "T must be above %d", kSkipped);
+  if (!out || (backward && !dg)) return fail(KDA_ERR_INVALID_ARG, "out and dg must be non-NULL");
+  a.first_ticket = (uint32_t)(gdr::kGlrGroup * (a.pitch / 64));
+  a.max_polls = 4096;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = backward ? gdr::launch_glr_bwd(a, s) : gdr::launch_glr_fwd(a, s);
+  return e == cudaSuccess ? KDA_OK : cuda_fail(e, "scan self-test launch");
 }
 
 kda_status_t glr_step(const void *x, int64_t ld_x, const float *g, int64_t ld_g, void *h,

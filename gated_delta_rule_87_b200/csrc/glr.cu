@@ -203,8 +203,10 @@ __device__ __forceinline__ void store_state(const GlrArgs &p, float *states, int
   if (states && l.any() && r >= 0 && GDR_IN_BOUNDS(r < p.num_slots)) store2<PAIRS>(states + (int64_t)r * p.D, l, x);
 }
 
-__device__ __forceinline__ bool bad_offsets(const GlrArgs &p) {
-  return p.cu_seqlens && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK;
+// Whether the call has failed before this kernel: bad offsets, or a wait of its
+// first pass that gave up.
+__device__ __forceinline__ bool failed(const GlrArgs &p) {
+  return (p.cu_seqlens || p.keep_status) && *reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK;
 }
 
 // ---- maps of spans ------------------------------------------------------
@@ -264,11 +266,9 @@ struct TileShared {
 // is 0.  So a hand-over is one store and one polling load, without a fence.  The
 // rows of words are as wide as the tiles (`pitch`), so every lane has its own.
 template <int TOK> struct Chain {
-  static constexpr int kGroup = 16, kPart = kGroup / kWarps;
+  static constexpr int kGroup = kGlrGroup, kPart = kGroup / kWarps;
   static_assert(kGroup >= kGlrShortestGroup, "the workspace counts groups of at least this length");
 };
-constexpr uint32_t kMaxChainPolls = 1u << 20;  // about a second
-
 struct Words {
   uint64_t u[2];
   __device__ __forceinline__ bool here() const { return min((uint32_t)(u[0] >> 32), (uint32_t)(u[1] >> 32)) != 0; }
@@ -324,7 +324,7 @@ template <bool REV> __device__ __forceinline__ Place taken(const GlrArgs &p, con
 __device__ __forceinline__ bool give_up(const GlrArgs &p, uint32_t poll) {
   if ((poll & 1023) != 1023) return false;
   if (*reinterpret_cast<const volatile int32_t *>(p.status) != KDA_DEVICE_OK) return true;
-  if (poll < kMaxChainPolls) return false;
+  if (poll < p.max_polls) return false;
   *p.status = KDA_DEVICE_TIMEOUT;
   return true;
 }
@@ -566,7 +566,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
   extern __shared__ __align__(128) unsigned char tile_bytes[];
   init_barriers(sh);
   wait_for_last();
-  if (bad_offsets(p)) return;
+  if (failed(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   auto &rows = reinterpret_cast<WarpRows<IO, PAIRS, TOK, false> *>(tile_bytes)[w];
   const Shift sg = shift_of<float>(p.g, p.ld_g), sx = shift_of<IO>(p.x, p.ld_x);
@@ -700,7 +700,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
   extern __shared__ __align__(128) unsigned char tile_bytes[];
   init_barriers(sh);
   wait_for_last();
-  if (bad_offsets(p)) return;
+  if (failed(p)) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   auto &rows = reinterpret_cast<WarpRows<IO, PAIRS, TOK, true> *>(tile_bytes)[w];
   const Shift sg = shift_of<float>(p.g, p.ld_g), sx = shift_of<IO>(p.x, p.ld_x), sd = shift_of<IO>(p.dh, p.ld_dh);
@@ -842,7 +842,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
 }
 
 // Before the scan kernels: zeroes the ticket and the chain's words, checks the
-// packed offsets, writes the status word and marks the tiles in which a
+// packed offsets, writes the status word (once a call) and marks the tiles in which a
 // sequence begins or ends.
 __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words) {
   let_next_start();
@@ -856,8 +856,9 @@ __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words
       }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) {
-      *p.status = bad ? KDA_DEVICE_BAD_CU_SEQLENS : KDA_DEVICE_OK;
-      *p.ticket = 0;
+      if (bad) *p.status = KDA_DEVICE_BAD_CU_SEQLENS;
+      else if (!p.keep_status) *p.status = KDA_DEVICE_OK;
+      *p.ticket = (int32_t)p.first_ticket;
     }
   }
   const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
@@ -878,7 +879,7 @@ __global__ void __launch_bounds__(256) glr_begin_kernel(GlrArgs p, int64_t words
 
 // Without any token: what leaves each sequence is what enters it.
 __global__ void __launch_bounds__(256) glr_no_tokens_kernel(GlrArgs p, bool backward) {
-  if (bad_offsets(p)) return;
+  if (failed(p)) return;
   const int n = blockIdx.x;
   const int64_t r = backward ? n : state_row(p, n);
   if (r < 0) return;
@@ -1069,9 +1070,13 @@ cudaError_t launch_fwd(const GlrArgs &a, cudaStream_t s) {
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 cudaError_t launch_bwd(const GlrArgs &a, cudaStream_t s) {
   constexpr int TOK = BwdShape<IO, COMPLEMENT>::kTok;
-  const GlrArgs p = with_tiles<TOK>(a);
+  GlrArgs p = with_tiles<TOK>(a);
+  p.first_ticket = 0;
   cudaError_t e = cudaSuccess;
-  if (p.own_chunks && p.tiles > 0) e = launch_scan<IO, PAIRS, COMPLEMENT, true>(a, s);
+  if (p.own_chunks && p.tiles > 0) {
+    e = launch_scan<IO, PAIRS, COMPLEMENT, true>(a, s);
+    p.keep_status = true;
+  }
   if (e == cudaSuccess) e = launch_begin(p, s);
   if (e != cudaSuccess) return e;
   if (p.tiles == 0) return launch_no_tokens(p, true, s);

@@ -134,7 +134,12 @@ struct GlrArgs {
   int stripes, tile_tokens;
   int64_t tiles, groups;
   bool chained;
+  bool keep_status;       // the second pass of a call: an error of the first one stays
+  uint32_t first_ticket;  // 0; the self-test leaves out the tiles before it ...
+  uint32_t max_polls;     // ... and gives up waiting for them after these
 };
+constexpr int kGlrGroup = 16;                  // tiles of a group of the chain
+constexpr uint32_t kGlrMaxPolls = 1u << 20;    // of one wait in the chain: about a second
 
 cudaError_t launch_glr_fwd(const GlrArgs &a, cudaStream_t stream);
 cudaError_t launch_glr_bwd(const GlrArgs &a, cudaStream_t stream);

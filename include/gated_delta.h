@@ -383,7 +383,8 @@ KDA_API kda_status_t kda_chunk_fwd_host(const void *q, const void *k, const void
  * products and sums are fp32; only h is rounded to io_dtype.  A non-finite
  * value of one sequence never reaches another.  final_state may be the
  * buffer of initial_state.  An invalid cu_seqlens leaves every output
- * unwritten (kda_check_device_status on the workspace).  B T D / 4096 must
+ * unwritten (kda_check_device_status on the workspace); after
+ * KDA_DEVICE_TIMEOUT they are incomplete.  B T D / 4096 must
  * fit in int32 (else KDA_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 typedef enum { GLR_INPUT_GIVEN = 0, GLR_INPUT_COMPLEMENT = 1 } glr_input_t;
@@ -426,6 +427,18 @@ KDA_API kda_status_t glr_scan_bwd(const void *dh, int64_t ld_dh, const float *df
                                   int32_t T, int32_t D, glr_input_t input,
                                   kda_dtype_t io_dtype, void *workspace,
                                   size_t workspace_bytes, void *stream);
+
+/* Diagnostic: a scan (or, with `backward`, its gradient without chunk_states,
+ * x taken for dh too) of one dense fp32 sequence x, g [T, D] in which the first
+ * 1024 tokens are left out, so that every later tile waits for what nobody
+ * writes: after a few thousand polls the waits expire, the status word becomes
+ * KDA_DEVICE_TIMEOUT and the kernels return, as a real expired wait would end
+ * them.  out, and backward dg, [T, D] fp32 are left unwritten.  T > 1024;
+ * workspace as glr_scan_fwd (glr_scan_bwd without chunk states).  Asynchronous. */
+KDA_API kda_status_t glr_selftest_wait_timeout(int32_t backward, const float *x, const float *g,
+                                               float *out, float *dg, int32_t T, int32_t D,
+                                               void *workspace, size_t workspace_bytes,
+                                               void *stream);
 
 /* One token for each of N sequences, the states updated in place:
  *   x [N, D] io_dtype (rows ld_x apart), g [N, D] fp32 (rows ld_g apart),
