@@ -4,8 +4,8 @@
 //     du = dy w s,  dx = r (du - u mean(du u)),  dz = dy u w s'(z),  dw = sum over rows of dy u s
 // mean(du u) = r mean(du x), so the backward pass takes both of its row sums in
 // one reduction.  16384 x 32 x 128 bf16: 68 us (sigmoid) = 5.9 TB/s and 70 (silu);
-// gradient 122 = 5.5 TB/s and 134 = 5.0, where the gate's instructions show; fp32 134
-// and 230 us = 6.0 and 5.8 TB/s.
+// gradient 120 = 5.6 TB/s and 132 = 5.1, where the gate's instructions show; fp32 134
+// and 214 us = 6.0 and 6.3 TB/s.
 #include "norms.cuh"
 
 namespace gdr {
@@ -15,25 +15,44 @@ namespace {
 // sigmoid.  bf16 results keep 8 bits, so the approximations' few ulp are far below
 // their rounding (an exponential that overflows gives 0, as it should); fp32 ones
 // take the accurate functions.
-template <typename IO> __device__ __forceinline__ float2 sigmoid(float2 z) {
+template <typename IO> __device__ __forceinline__ float2 exp_of_minus(float2 z) {
   if constexpr (sizeof(IO) == 2) {
     const float2 t = mul2(z, both(-1.44269504f));  // -log2 e
-    float2 e, g;
+    float2 e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-    e = add2(e, both(1.f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.x) : "f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.y) : "f"(e.y));
-    return g;
+    return e;
   } else {
-    return make_float2(1.f / (1.f + expf(-z.x)), 1.f / (1.f + expf(-z.y)));
+    return make_float2(expf(-z.x), expf(-z.y));
   }
 }
-// the gate's value, and its slope, from z and g = sigmoid(z)
-template <bool SILU> __device__ __forceinline__ float2 gate_value(float2 z, float2 g) { return SILU ? mul2(z, g) : g; }
-template <bool SILU> __device__ __forceinline__ float2 gate_slope(float2 z, float2 g) {
-  const float2 rest = fma2(g, both(-1.f), both(1.f));
-  return mul2(g, SILU ? fma2(z, rest, both(1.f)) : rest);
+template <typename IO> __device__ __forceinline__ float2 one_over(float2 x) {
+  if constexpr (sizeof(IO) == 2) {
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
+    return r;
+  } else {
+    return make_float2(1.f / x.x, 1.f / x.y);
+  }
+}
+template <typename IO, bool SILU> __device__ __forceinline__ float2 gate_value(float2 z) {
+  const float2 g = one_over<IO>(add2(exp_of_minus<IO>(z), both(1.f)));
+  return SILU ? mul2(z, g) : g;
+}
+
+// The gate's value and its slope.  1 - g of g = sigmoid(z) is exp(-z) g: as a
+// difference it has one digit left at z = 15 in fp32, and none at 17.  (Where the
+// exponential overflows, g is 0 and 1 - g of no account.)
+__device__ __forceinline__ float finite(float e) {
+  asm("min.NaN.f32 %0, %0, 0f7F7FFFFF;" : "+f"(e));
+  return e;
+}
+template <typename IO, bool SILU> __device__ __forceinline__ float2 gate_value(float2 z, float2 &slope) {
+  const float2 e = exp_of_minus<IO>(z), g = one_over<IO>(add2(e, both(1.f)));
+  const float2 rest = mul2(make_float2(finite(e.x), finite(e.y)), g);
+  slope = mul2(g, SILU ? fma2(z, rest, both(1.f)) : rest);
+  return SILU ? mul2(z, g) : g;
 }
 
 // A row of a [tokens, H, d] tensor whose tokens are ld elements apart, as the group walks.
@@ -95,7 +114,7 @@ gated_norm_fwd_kernel(const __grid_constant__ GatedNormArgs p) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         w[j] = mul2(w[j], mul2(x[i].pair(j), inv));
-        if (gated) w[j] = mul2(w[j], gate_value<SILU>(z[i].pair(j), sigmoid<IO>(z[i].pair(j))));
+        if (gated) w[j] = mul2(w[j], gate_value<IO, SILU>(z[i].pair(j)));
       }
       if (live && grp.any[i] && GDR_IN_BOUNDS(row < grp.rows)) store_piece<IO, V>(y, grp.c[i], grp.whole[i], grp.half[i], w);
     }
@@ -103,9 +122,15 @@ gated_norm_fwd_kernel(const __grid_constant__ GatedNormArgs p) {
 }
 
 // The next row's loads are under way while this one is worked on (few blocks fit
-// an SM), as far as a thread has one piece.
+// an SM), as far as a thread has one piece.  Registers for three blocks of warps
+// an SM (two with silu in bf16 or with masked pieces, which need more: they would
+// spill); for a block a row 80 a thread (65536 over 800), six blocks of 128: 16384
+// x 4 x 1000 bf16 118 us, with 82 registers 132.
+template <int LANES, int NV, bool ODD> constexpr int kBackThreads =
+    LANES ? 256 : NV == 1 && !ODD ? 800 : kMostThreads;
 template <typename IO, int V, int NV, int LANES, bool ODD, bool SILU>
-__global__ void __launch_bounds__(LANES ? 256 : kBlockThreads<V, true>, LANES && NV == 1 ? SILU ? 2 : 3 : 1)
+__global__ void __launch_bounds__(kBackThreads<LANES, NV, ODD>,
+                                  LANES && NV == 1 ? SILU && (sizeof(IO) == 2 || ODD) ? 2 : 3 : 1)
 gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
   constexpr int NP = Pairs<V>::N;
   let_next_start();
@@ -141,50 +166,48 @@ gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
   load(grp.row);
   for (int64_t row = grp.row; grp.more(row); row += grp.step) {
     const bool live = row < grp.rows;
-    Pack<IO, V> cdy[NV], cx[NV], cz[NV];
-    float2 g[NV][NP], ss = both(0.f), sd = both(0.f);  // g: sigmoid(z)
+    Pack<IO, V> cx[NV];
+    float2 t[NV][NP], ds[NV][NP], ss = both(0.f), sd = both(0.f);  // t: dy s; ds: dy s'
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (!live) dy[i].zero();  // (a group past the last row adds nothing)
       cx[i] = x[i];
-      cdy[i] = dy[i];
-      cz[i] = z[i];
+      Pack<IO, V> cdy = dy[i], cz = z[i];
       if (ODD && !grp.whole[i]) {
         cx[i].keep(grp.half[i]);
-        cdy[i].keep(grp.half[i]);
-        cz[i].keep(grp.half[i]);
+        cdy.keep(grp.half[i]);
+        cz.keep(grp.half[i]);
       }
       float2 w[NP];
       weight.get(grp, i, w);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const float2 xv = cx[i].pair(j);
-        float2 du = mul2(cdy[i].pair(j), w[j]);
-        g[i][j] = both(1.f);
+        t[i][j] = cdy.pair(j);
         if (gated) {
-          g[i][j] = sigmoid<IO>(cz[i].pair(j));
-          du = mul2(du, gate_value<SILU>(cz[i].pair(j), g[i][j]));
+          float2 slope;
+          const float2 g = gate_value<IO, SILU>(cz.pair(j), slope);
+          ds[i][j] = mul2(t[i][j], slope);
+          t[i][j] = mul2(t[i][j], g);
         }
         ss = fma2(xv, xv, ss);
-        sd = fma2(du, xv, sd);
+        sd = fma2(mul2(t[i][j], w[j]), xv, sd);
       }
     }
     if (EARLY) load(row + grp.step);
-    const float2 t = grp.sum(ss.x + ss.y, sd.x + sd.y);
-    const float inv = rsqrtf(t.x / (float)p.d + p.eps);
-    const float m = inv * inv * (t.y / (float)p.d);  // mean(du u) r
+    const float2 sum = grp.sum(ss.x + ss.y, sd.x + sd.y);
+    const float inv = rsqrtf(sum.x / (float)p.d + p.eps);
+    const float m = inv * inv * (sum.y / (float)p.d);  // mean(du u) r
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float2 dx[NP], dz[NP], w[NP];
       weight.get(grp, i, w);
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const float2 xv = cx[i].pair(j), gv = cdy[i].pair(j), zv = cz[i].pair(j);
-        const float2 s = gated ? gate_value<SILU>(zv, g[i][j]) : both(1.f);
-        const float2 gu = mul2(gv, mul2(xv, both(inv))), gw = mul2(gv, w[j]);
-        dx[j] = mul2(both(inv), fma2(xv, both(-m), mul2(gw, s)));
-        dz[j] = mul2(mul2(gu, w[j]), gate_slope<SILU>(zv, g[i][j]));
-        acc[i][j] = fma2(gu, s, acc[i][j]);
+        const float2 xv = cx[i].pair(j), u = mul2(xv, both(inv));
+        dx[j] = mul2(both(inv), fma2(xv, both(-m), mul2(t[i][j], w[j])));
+        acc[i][j] = fma2(t[i][j], u, acc[i][j]);
+        dz[j] = mul2(mul2(ds[i][j], w[j]), u);
       }
       if (live && grp.any[i] && GDR_IN_BOUNDS(row < grp.rows)) {
         store_piece<IO, V>(static_cast<IO *>(p.dx) + row * p.d, grp.c[i], grp.whole[i], grp.half[i], dx);
