@@ -109,9 +109,10 @@ add_norm_bwd_kernel(const __grid_constant__ AddNormArgs p) {
     float2 ss = both(0.f), sd = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!live) {  // (a group past the last row adds nothing)
+      if (!live) {  // (a group past the last row adds nothing, whatever it held; a block never is)
         dn[i].zero();
         y[i].zero();
+        if (LANES) dt[i].zero();
       }
       ct[i] = t[i];
       cdt[i] = dt[i];

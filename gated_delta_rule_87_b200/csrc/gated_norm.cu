@@ -170,7 +170,10 @@ gated_norm_bwd_kernel(const __grid_constant__ GatedNormArgs p) {
     float2 t[NV][NP], ds[NV][NP], ss = both(0.f), sd = both(0.f);  // t: dy s; ds: dy s'
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!live) dy[i].zero();  // (a group past the last row adds nothing)
+      if (!live) {  // (a group past the last row adds nothing, whatever it held; a block never is)
+        dy[i].zero();
+        if (LANES) z[i].zero();
+      }
       cx[i] = x[i];
       Pack<IO, V> cdy = dy[i], cz = z[i];
       if (ODD && !grp.whole[i]) {
