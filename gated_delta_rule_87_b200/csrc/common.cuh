@@ -42,7 +42,8 @@ __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u 
 // launch_behind() starts a kernel while the one before it on the stream still
 // runs, once every block of that one has called let_next_start(); what the
 // earlier kernel writes may be read after wait_for_last(), which every thread of
-// the later kernel calls first (so what follows on the stream waits for both).
+// the later kernel calls first (so what follows on the stream waits for both), and
+// by plain loads only: to the later kernel it is not read-only.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

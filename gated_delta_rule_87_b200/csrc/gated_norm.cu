@@ -258,10 +258,11 @@ template <typename IO> cudaError_t gated_io(const GatedNormArgs &p, bool back, c
   return p.d % V == 0 && aligned16(p.weight) ? gated_vec<IO, V, false>(p, back, s) : gated_vec<IO, V, true>(p, back, s);
 }
 
-// out[c] = sum of partial[b][c] over the blocks, in a fixed order.
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restrict__ partial0,
-                                                          float *out0, const float *partial1,
-                                                          float *out1, int blocks, int d) {
+// out[c] = sum of partial[b][c] over the blocks, in a fixed order.  (The partial
+// sums are still written when this kernel starts: no __restrict__, no read-only loads.)
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *partial0, float *out0,
+                                                          const float *partial1, float *out1, int blocks,
+                                                          int d) {
   wait_for_last();
   const float *partial = blockIdx.y ? partial1 : partial0;
   float *out = blockIdx.y ? out1 : out0;

@@ -449,9 +449,10 @@ __device__ __forceinline__ void pass_empty(const GlrArgs &p, const float *src, f
 }
 
 // Whether a tile holds the start or the end of a sequence (else its tokens take
-// the path without marks).
+// the path without marks).  (A plain load: the kernel that writes the marks may
+// still run when this one starts, so they are not read-only to it.)
 __device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
-  if (p.cu_seqlens) return __ldg(p.tile_marks + tile) != 0;
+  if (p.cu_seqlens) return p.tile_marks[tile] != 0;
   const uint32_t t = tile * p.tile_tokens, r = t % (uint32_t)p.T;
   return r == 0 || r + p.tile_tokens >= (uint32_t)p.T;
 }
