@@ -10,8 +10,10 @@
 //     dx_t = d_t  or  (1 - a_t) d_t,   dg_t = a_t d_t (h_{t-1} [- x_t]),   dh_0 = a_1 d_1.
 //
 // Both directions are affine maps of the value that enters a span of tokens:
-// (A, H) with out = A in + H.  The decay product of a span is exp of the sum
-// of its g, so a long memory loses no precision to the rounding of each a_t.
+// (A, H) with out = A in + H.  What is carried from one group of 1024 or 2048 tokens to
+// the next meets one rounded decay a group, exp of the sum of its g; within a group
+// at most a warp's 16 or 32 tokens, three warps and fifteen tiles are joined by
+// products of rounded ones.
 // A span that holds a sequence start (an end, for the gradient) is "closed":
 // what enters it does not reach what leaves it, whatever its value (an
 // infinity or NaN of one sequence stays in it).
@@ -103,9 +105,11 @@ template <bool PAIRS, typename IO> __device__ __forceinline__ void store2(IO *p,
   }
 }
 
-// The decay of one token.  With bf16 activations the fast exponential: its error
-// (2^-22 of the value) enters the state of a span of at most 32 tokens only,
-// the decay of longer spans comes from the sum of their g.
+// The decay of one token; for what enters from earlier tiles of the group, of a tile.
+// With bf16 activations the fast exponential: off by 2^-22 of the value and, from
+// the rounded product, 2^-24 |g|.  So much enters h before its rounding, and the fp32
+// states, dg and dinitial_state (the accurate one changed their errors by less than
+// a third, up as often as down, and cost 193 us instead of 180, 32768 x 4096).
 template <typename IO> __device__ __forceinline__ float2 decay(float2 g) {
   if constexpr (sizeof(IO) == 2) {
     const float2 t = mul2(g, both(1.44269504f));  // log2 e
@@ -118,7 +122,7 @@ template <typename IO> __device__ __forceinline__ float2 decay(float2 g) {
   }
 }
 // 1 - a of one token: near 0 the series of -expm1(g), whose first term left out
-// is below 2^-22 of the value (bf16 activations) or 2^-28, else the difference,
+// is below 2^-21.9 of the value (bf16 activations) or 2^-30, else the difference,
 // which then loses less than two bits.
 template <typename IO> __device__ __forceinline__ float2 fresh(float2 g, float2 a) {
   float2 s = both(1.f / 5040.f);
@@ -243,9 +247,12 @@ template <int N> __device__ __forceinline__ Map2 joined(const Map2 (&t)[N]) {
 }
 
 struct TileShared {
-  // the warps' maps; a tile's are read until its end, while the next one's are written
+  // the warps' maps and the sums of their log-decays; a tile's are read until its
+  // end, while the next one's are written
   Map2 map[2][kWarps][32];
+  float2 sum[2][kWarps][32];
   Map2 before[kWarps][32];  // of earlier tiles, a part a warp
+  float2 before_sum[kWarps][32];
   uint64_t full[kWarps];    // a warp's copies have landed
   uint32_t step;            // of the block's next tile
   int stripe;
@@ -261,10 +268,18 @@ struct TileShared {
 // values are joined, and in which order, depends on the sizes alone, never on
 // timing.
 //
-// A channel's map goes through the workspace as one 64-bit word (A with its sign
-// turned above, H below), which is its own flag: 0 is not there yet, and no map
-// is 0.  So a hand-over is one store and one polling load, without a fence.  The
-// rows of words are as wide as the tiles (`pitch`), so every lane has its own.
+// A group's decay is exp of the sum of its log-decays, not the product of its tiles'
+// decays: only what a group hands on is carried from group to group, and rounded
+// factors that are all alike err to the same side.  (Decays of 1e-5 a token, constant
+// over 32768: h off by 8e-7 of itself in fp32, by products of the warps' decays
+// 2.4e-5.  It costs bf16 1 % of its time.)
+//
+// A channel's map goes through the workspace as one 64-bit word (the bits of the
+// sum turned above, H below), which is its own flag: 0 is not there yet, and no map
+// is 0.  A closed map has a pattern of its own: that of a NaN which no sum gives (sums
+// that are not numbers have one pattern, 0x7fffffff).  So a hand-over is one store and
+// one polling load, without a fence.  The rows of words are as wide as the tiles
+// (`pitch`), so every lane has its own.
 template <int TOK> struct Chain {
   static constexpr int kGroup = kGlrGroup, kPart = kGroup / kWarps;
   static_assert(kGroup >= kGlrShortestGroup, "the workspace counts groups of at least this length");
@@ -272,13 +287,17 @@ template <int TOK> struct Chain {
 struct Words {
   uint64_t u[2];
   __device__ __forceinline__ bool here() const { return min((uint32_t)(u[0] >> 32), (uint32_t)(u[1] >> 32)) != 0; }
-  static __device__ __forceinline__ uint64_t pack(float A, float H) {
-    return (uint64_t)(__float_as_uint(A) ^ 0x80000000u) << 32 | __float_as_uint(H);
+  static constexpr uint32_t kClosedSum = 0x7ffffffeu;
+  static __device__ __forceinline__ uint64_t pack(bool closed, float sum, float H) {
+    return (uint64_t)max(~(closed ? kClosedSum : __float_as_uint(sum)), 1u) << 32 | __float_as_uint(H);
   }
-  static __device__ __forceinline__ float A(uint64_t u) { return __uint_as_float((uint32_t)(u >> 32) ^ 0x80000000u); }
-  static __device__ __forceinline__ float H(uint64_t u) { return __uint_as_float((uint32_t)u); }
-  __device__ __forceinline__ Map2 map() const {
-    return {make_float2(A(u[0]), A(u[1])), make_float2(H(u[0]), H(u[1]))};
+  static __device__ __forceinline__ uint32_t above(uint64_t u) { return ~(uint32_t)(u >> 32); }
+  __device__ __forceinline__ bool closed() const { return above(u[0]) == kClosedSum; }
+  __device__ __forceinline__ float2 sum() const {
+    return make_float2(__uint_as_float(above(u[0])), __uint_as_float(above(u[1])));
+  }
+  __device__ __forceinline__ float2 H() const {
+    return make_float2(__uint_as_float((uint32_t)u[0]), __uint_as_float((uint32_t)u[1]));
   }
 };
 template <bool PAIRS> __device__ __forceinline__ void load_words(const uint64_t *p, Words &w) {
@@ -289,8 +308,8 @@ template <bool PAIRS> __device__ __forceinline__ void load_words(const uint64_t 
     asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(w.u[1]) : "l"(p + 32) : "memory");
   }
 }
-template <bool PAIRS> __device__ __forceinline__ void store_words(uint64_t *p, const Map2 &m) {
-  const uint64_t u[2] = {Words::pack(m.A.x, m.H.x), Words::pack(m.A.y, m.H.y)};
+template <bool PAIRS> __device__ __forceinline__ void store_words(uint64_t *p, bool closed, float2 sum, float2 H) {
+  const uint64_t u[2] = {Words::pack(closed, sum.x, H.x), Words::pack(closed, sum.y, H.y)};
   if constexpr (PAIRS) {
     asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(p), "l"(u[0]), "l"(u[1]) : "memory");
   } else {
@@ -335,18 +354,23 @@ template <bool PAIRS, bool REV>
 __device__ __forceinline__ void publish_tile(const GlrArgs &p, const TileShared &sh, int buf, const Place &q,
                                              int c, int lane) {
   Map2 t[kWarps];
+  float2 sum = both(0.f);
 #pragma unroll
-  for (int k = 0; k < kWarps; ++k) t[k] = sh.map[buf][REV ? kWarps - 1 - k : k][lane];
+  for (int k = 0; k < kWarps; ++k) {
+    t[k] = sh.map[buf][REV ? kWarps - 1 - k : k][lane];
+    sum = add2(sum, sh.sum[buf][REV ? kWarps - 1 - k : k][lane]);
+  }
+  const Map2 m = joined(t);
   if (GDR_IN_BOUNDS(q.step < p.tiles && c < p.pitch))
-    store_words<PAIRS>(p.tile_map + (int64_t)q.step * p.pitch + c, joined(t));
+    store_words<PAIRS>(p.tile_map + (int64_t)q.step * p.pitch + c, m.closed(), sum, m.H);
 }
 
 // What enters the tile.  Each warp joins its part of the group's earlier maps,
 // then all wait for what enters the group and take it through the parts.  That
-// wait is the serial part of the chain: the tile that ends a group sends on
-// what leaves it at once.  Every thread of the block takes part.  False: a wait
-// gave up.
-template <int TOK, bool PAIRS, bool REV>
+// wait is the serial part of the chain: the tile that ends a group has the whole
+// group's map ready and sends on what leaves it at once.  Every thread of the block
+// takes part.  False: a wait gave up.
+template <typename IO, int TOK, bool PAIRS, bool REV>
 __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int buf, const Place &q, int c, int w,
                                            int lane, float2 &in) {
   constexpr int kGroup = Chain<TOK>::kGroup, kPart = Chain<TOK>::kPart;
@@ -364,7 +388,7 @@ __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int
     Words t[kPart];
 #pragma unroll
     for (int j = 0; j < kPart; ++j) {
-      t[j].u[0] = t[j].u[1] = Words::pack(1.f, 0.f);  // nothing changes
+      t[j].u[0] = t[j].u[1] = Words::pack(false, 0.f, 0.f);  // nothing changes
       if (j < n) load_words<PAIRS>(from + (int64_t)j * p.pitch, t[j]);
     }
     for (uint32_t poll = 0;; ++poll) {
@@ -381,21 +405,40 @@ __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int
         if (!t[j].here()) load_words<PAIRS>(from + (int64_t)j * p.pitch, t[j]);
     }
     Map2 m[kPart];
+    float2 sum = both(0.f);
 #pragma unroll
-    for (int j = 0; j < kPart; ++j) m[j] = t[j].map();
+    for (int j = 0; j < kPart; ++j) {
+      m[j] = {t[j].closed() ? both(kClosed) : decay<IO>(t[j].sum()), t[j].H()};
+      sum = add2(sum, t[j].sum());
+    }
     sh.before[w][lane] = joined(m);
+    sh.before_sum[w][lane] = sum;
   }
   if (__syncthreads_or(!ok)) return false;
-  Map2 part[kWarps];
-  bool closed = false;  // nothing to wait for where a sequence began since
+  Map2 pre = {both(1.f), both(0.f)};  // of the group's tiles before this one
 #pragma unroll
   for (int k = 0; k < kWarps; ++k)
     if (k * kPart < at) {
-      part[k] = sh.before[k][lane];
-      closed |= part[k].closed();
+      const Map2 t = sh.before[k][lane];
+      pre = {pre.closed() || t.closed() ? both(kClosed) : mul2(pre.A, t.A), t.of(pre.H)};
     }
+  // and of the whole group, by the warp that sends on what leaves it
+  const bool ends = at == kGroup - 1 && w == (REV ? 0 : kWarps - 1);
+  Map2 all = pre;
+  if (ends) {
+    float2 sum = both(0.f);
+    bool shut = pre.closed();
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const Map2 t = sh.map[buf][REV ? kWarps - 1 - k : k][lane];
+      all.H = t.of(all.H);
+      shut |= t.closed();
+      sum = add2(sum, add2(sh.before_sum[k][lane], sh.sum[buf][k][lane]));
+    }
+    all.A = shut ? both(kClosed) : make_float2(expf(sum.x), expf(sum.y));
+  }
   in = both(0.f);
-  if (behind && !closed) {
+  if (behind && !pre.closed()) {  // (nothing to wait for where a sequence began since)
     for (uint32_t poll = 0; !__all_sync(0xffffffffu, u.here()); ++poll) {
       if (give_up(p, poll)) {
         ok = false;  // the block finds out at its next barrier
@@ -403,17 +446,11 @@ __device__ __forceinline__ bool enter_tile(const GlrArgs &p, TileShared &sh, int
       }
       load_words<PAIRS>(carry, u);
     }
-    in = u.map().H;
+    in = u.H();
   }
-#pragma unroll
-  for (int k = 0; k < kWarps; ++k)
-    if (k * kPart < at) in = part[k].of(in);
-  if (ok && at == kGroup - 1 && w == (REV ? 0 : kWarps - 1) && GDR_IN_BOUNDS(group < p.groups && c < p.pitch)) {
-    Map2 out = {both(kClosed), in};
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) out.H = sh.map[buf][REV ? kWarps - 1 - k : k][lane].of(out.H);
-    store_words<PAIRS>(p.carry + (int64_t)group * p.pitch + c, out);
-  }
+  if (ok && ends && GDR_IN_BOUNDS(group < p.groups && c < p.pitch))
+    store_words<PAIRS>(p.carry + (int64_t)group * p.pitch + c, true, both(0.f), all.of(in));
+  in = pre.of(in);
   return ok;
 }
 
@@ -470,10 +507,10 @@ __device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
 // over the rows in shared memory, and its next copies begin after them (256
 // sequences of 64 x 4096 bf16, all of whole warps: 83 us; by rolled loops 127).
 //
-// Bound by HBM where rows are long (32768 x 4096: bf16 173 us = 6.2 TB/s of 2e + 4
-// bytes an element, fp32 259 us = 6.2; a copy does 6.5), with few columns by the
+// Bound by HBM where rows are long (32768 x 4096: bf16 174 us = 6.2 TB/s of 2e + 4
+// bytes an element, fp32 253 us = 6.4; a copy does 6.5), with few columns by the
 // chain (65536 x 256 bf16: 42 us = 3.2 TB/s).  The complement forms 1 - a, 8 warps
-// an SM: by its instructions (bf16 230 us).
+// an SM (bf16 237 us, fp32 269).
 //
 // A tensor-map copy begins on 16 bytes.  Where rows do not, every R-th one (R
 // elements in 16 bytes) is as far past a boundary as the first: R maps, each of
@@ -551,10 +588,11 @@ template <typename IO, bool PAIRS, bool COMPLEMENT> struct FwdShape {
 };
 // Backward: in bf16 x and dh go to registers as well; else (x and dh too wide, or
 // g needed again) they are read from shared memory in both passes, and the next
-// copies begin after the second.
+// copies begin after the second.  Three blocks also in fp32, whose tiles leave room
+// for no more (with the registers of four: 459 and 529 us against 453 and 502).
 template <typename IO, bool COMPLEMENT> struct BwdShape {
   static constexpr bool kEarly = sizeof(IO) == 2 && !COMPLEMENT;
-  static constexpr int kTok = 16, kBlocks = kEarly ? 3 : 4;
+  static constexpr int kTok = 16, kBlocks = kEarly || sizeof(IO) == 4 ? 3 : 4;
 };
 
 // Forward.  STATES_ONLY: only the saved chunk states are written.
@@ -638,6 +676,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
       }
     }
     sh.map[buf][w][lane] = {m.first ? both(kClosed) : make_float2(expf(gs.x), expf(gs.y)), h};
+    sh.sum[buf][w][lane] = gs;
     if (__syncthreads_or(!alive)) return;  // a wait gave up; no copy is under way
     if (p.chained && w == kWarps - 1 && (q.step + 1) % Chain<TOK>::kGroup != 0) publish_tile<PAIRS, false>(p, sh, buf, q, l.c, lane);
     const Place nq = taken<false>(p, sh);
@@ -646,7 +685,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
     const bool next_marked = more && has_marks(p, nq.tile);
     h = both(0.f);
     if (p.chained) {
-      alive = enter_tile<TOK, PAIRS, false>(p, sh, buf, q, l.c, w, lane, h);
+      alive = enter_tile<IO, TOK, PAIRS, false>(p, sh, buf, q, l.c, w, lane, h);
       if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced
@@ -689,7 +728,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
 
 // Backward: the states again from what enters the tile (saved), the gradients
 // from what enters it from the tokens after it (chained).  32768 x 4096: bf16 324
-// us = 5.8 TB/s of 3e + 8 bytes an element, fp32 429 us = 6.3; complement 386, 505.
+// us = 5.8 TB/s of 3e + 8 bytes an element, fp32 447 us = 6.0; complement 372, 490.
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 __global__ void __launch_bounds__(kThreads, (BwdShape<IO, COMPLEMENT>::kBlocks))
 glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps<IO, PAIRS, true> maps) {
@@ -775,6 +814,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     {
       const float2 A = make_float2(expf(gs.x), expf(gs.y));
       sh.map[buf][w][lane] = {m.last ? both(kClosed) : A, r};
+      sh.sum[buf][w][lane] = gs;
       states[w][lane] = {m.first ? both(kClosed) : A, s};
     }
     if (__syncthreads_or(!alive)) return;  // a wait gave up; no copy is under way
@@ -786,7 +826,7 @@ glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ G
     enter_warp<false>(states, w, lane, h);
     r = both(0.f);
     if (p.chained) {
-      alive = enter_tile<TOK, PAIRS, true>(p, sh, buf, q, l.c, w, lane, r);
+      alive = enter_tile<IO, TOK, PAIRS, true>(p, sh, buf, q, l.c, w, lane, r);
       if (!alive) l.on[0] = l.on[1] = false;  // writes nothing, and ends at the next barrier
     } else {
       __syncthreads();  // the next ticket is read before it is replaced

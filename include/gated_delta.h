@@ -380,7 +380,9 @@ KDA_API kda_status_t kda_chunk_fwd_host(const void *q, const void *k, const void
  * Any D > 0 and T >= 0.  Rows start `ld` elements apart (>= D), the same for
  * every token of the batch.  Data pointers are aligned to their element size
  * (rows that begin on 16 bytes, with even D, run faster).  States,
- * products and sums are fp32; only h is rounded to io_dtype.  A non-finite
+ * products and sums are fp32; only h is rounded to io_dtype.  With bf16 x the
+ * exponential of a token's g is the hardware's (2^-22 of its value and 2^-24 |g|
+ * off), in glr_step and with fp32 x the accurate one.  A non-finite
  * value of one sequence never reaches another.  final_state may be the
  * buffer of initial_state.  An invalid cu_seqlens leaves every output
  * unwritten (kda_check_device_status on the workspace); after

@@ -54,3 +54,29 @@ def test_bad_offsets_are_reported_by_a_gradient_of_two_passes():
         ws = gdr.glr_scan_bwd(x, x, g, None, cud, dx=dx)[3]
         assert gdr.check_device_status(ws) == (gdr.KDA_ERR_DEVICE_CHECK, gdr.KDA_DEVICE_BAD_CU_SEQLENS)
         assert bool((dx == 7).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bits", [0x7fffffff, 0x7ffffffe, 0x7fc00000, -1, -2, -0x400000, -0x800000, 0x7f800000])
+def test_decays_that_are_not_numbers_stall_nothing(bits):
+    """NaN of every sign and payload, and infinities, in one channel of one
+    sequence: the chain goes on, other channels and sequences keep their values."""
+    import torch
+    T, D, c = 6000, 70, 5
+    for dt in (torch.float32, torch.bfloat16):
+        x, g = torch.randn((1, T, D), device="cuda").to(dt), -torch.rand((1, T, D), device="cuda")
+        cu = torch.tensor([0, 300, 4500, T], dtype=torch.int32, device="cuda")
+        clean = (*gdr.glr_scan_fwd(x, g, None, cu)[:1], *gdr.glr_scan_bwd(x, x, g, None, cu)[:2])
+        g.view(torch.int32)[0, 400:4400, c] = bits
+        h, _, _, ws = gdr.glr_scan_fwd(x, g, None, cu)
+        assert gdr.check_device_status(ws) == (gdr.KDA_OK, gdr.KDA_DEVICE_OK)
+        dx, dg, _, ws = gdr.glr_scan_bwd(x, x, g, None, cu)
+        assert gdr.check_device_status(ws) == (gdr.KDA_OK, gdr.KDA_DEVICE_OK)
+        keep = torch.ones((T, D), dtype=torch.bool, device="cuda")
+        keep[300:4500, c] = False
+        for got, want in zip((h, dx, dg), clean):
+            assert torch.equal(got[0][keep], want[0][keep])
+        if bits != -0x800000:  # (-inf forgets)
+            assert not bool(torch.isfinite(h[0, 4000, c].float()))
+        else:
+            assert torch.equal(h[0, 400:4400, c], x[0, 400:4400, c])
