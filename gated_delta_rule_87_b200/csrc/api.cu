@@ -727,6 +727,7 @@ kda_status_t glr_scan_bwd(const void *dh, int64_t ld_dh, const float *dfinal_sta
     for (const void *p : in)
       if (dx == p || (const void *)dg == p)
         return fail(KDA_ERR_INVALID_ARG, "dx and dg must not alias an input");
+    if (dx == (const void *)dg) return fail(KDA_ERR_INVALID_ARG, "dx and dg must not be the same buffer");
   }
   if (dinitial_state && (dinitial_state == initial_state || dinitial_state == dfinal_state))
     return fail(KDA_ERR_INVALID_ARG, "dinitial_state must not alias initial_state or dfinal_state");
@@ -827,6 +828,21 @@ static kda_status_t check_gated(const gdr::GatedNormArgs &a, kda_gate_t gate, kd
   return KDA_OK;
 }
 
+// An output may be an input's buffer where that one's rows lie as the output's do.
+static bool same_rows(const void *out, const void *in, int64_t ld, int64_t row) {
+  return !out || out != in || ld == row;
+}
+
+static kda_status_t check_gated_sharing(const gdr::GatedNormArgs &a) {
+  const int64_t row = (int64_t)a.H * a.d;
+  const void *outs[] = {a.y, a.dx, a.dz};
+  for (const void *o : outs)
+    if (!same_rows(o, a.x, a.ld_x, row) || !same_rows(o, a.z, a.ld_z, row) || !same_rows(o, a.dy, a.ld_dy, row))
+      return fail(KDA_ERR_INVALID_ARG, "an output shares a buffer with an input whose rows are further apart");
+  if (a.dz && a.dx == a.dz) return fail(KDA_ERR_INVALID_ARG, "dx and dz must not be the same buffer");
+  return KDA_OK;
+}
+
 kda_status_t kda_gated_norm_fwd(const void *x, int64_t ld_x, const void *z, int64_t ld_z,
                                 const float *weight, void *y, int64_t tokens, int32_t H, int32_t d,
                                 float eps, kda_gate_t gate, kda_dtype_t io_dtype, void *stream) {
@@ -836,6 +852,7 @@ kda_status_t kda_gated_norm_fwd(const void *x, int64_t ld_x, const void *z, int6
   a.y = y; a.tokens = tokens; a.H = H; a.d = d; a.eps = eps; a.gate = gate;
   a.bf16 = io_dtype == KDA_BF16;
   kda_status_t st = check_gated(a, gate, io_dtype, false);
+  if (st == KDA_OK && tokens > 0) st = check_gated_sharing(a);
   if (st != KDA_OK || tokens == 0) return st;
   cudaError_t e = gdr::launch_gated_norm_fwd(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KDA_OK : cuda_fail(e, "gated norm launch");
@@ -860,6 +877,7 @@ kda_status_t kda_gated_norm_bwd(const void *dy, int64_t ld_dy, const void *x, in
   kda_status_t st = check_gated(a, gate, io_dtype, true);
   if (st == KDA_OK && dweight)
     st = check_norm_workspace(workspace, workspace_bytes, kda_gated_norm_bwd_workspace_size(d));
+  if (st == KDA_OK && tokens > 0) st = check_gated_sharing(a);
   if (st != KDA_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   a.partial = dweight ? static_cast<float *>(workspace) : nullptr;

@@ -465,12 +465,16 @@ KDA_API kda_status_t glr_step(const void *x, int64_t ld_x, const float *g, int64
  *   weight  [d] fp32, shared by the heads, or NULL (ones)
  *   y       [tokens, H, d] io_dtype, contiguous, written
  * d up to 16384; eps > 0; tokens * H up to 2^31 - 1.  fp32 throughout, rounded
- * once at the end.  No workspace.
+ * once at the end.  (With bf16 x the gate takes the hardware's exponential and
+ * reciprocal: 2^-21 of its value and 2^-24 |z| off, also in dweight.)  No workspace.
+ * y may be the buffer of x or of z where that one's tokens follow each other
+ * (ld = H d).
  *
  * Backward: dx, dz [tokens, H, d] io_dtype (contiguous, written; dz unused
  * without a gate) and dweight [d] fp32 (written, or NULL), summed in a fixed
  * order.  dweight needs a workspace of kda_gated_norm_bwd_workspace_size()
- * bytes, 256-byte aligned. */
+ * bytes, 256-byte aligned.  dx and dz may each be the buffer of dy, x or z where
+ * that one's tokens follow each other; not the same. */
 typedef enum { KDA_GATE_NONE = 0, KDA_GATE_SILU = 1, KDA_GATE_SIGMOID = 2 } kda_gate_t;
 
 KDA_API kda_status_t kda_gated_norm_fwd(const void *x, int64_t ld_x, const void *z, int64_t ld_z,
