@@ -10,6 +10,7 @@ library is missing or no CUDA device is present the calls raise.
 tensors' device).  Outputs and workspaces that a call allocates belong to it, and
 tensors of other streams that it is given are kept until it is past them; the
 caller orders it with the streams that write those tensors and read the results.
+No call is recorded by autograd: the gradients are calls of their own (``*_bwd``).
 
 Operator (thethings.ai "The argument, in one page", table "Everything, in
 one table", rows "KDA" and "Gated DeltaNet"; column-vector keys):

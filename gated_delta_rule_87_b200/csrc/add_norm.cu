@@ -4,7 +4,9 @@
 //     dw = sum over rows of dn u,  dscale = sum of d y
 // 8192 x 4096 with an fp32 residual: 66 us = 6.1 TB/s, gradient 103 = 5.9; in bf16 52
 // and 83 us = 5.2 and 4.9 TB/s (a block a row: the sum over it and the
-// instructions around it show).  8192 x 4095 bf16: 64 and 99 us.
+// instructions around it show).  8192 x 4095 bf16: 66 and 99 us.  Gradients of long
+// rows spill (more than 10240 channels in bf16, 5120 in fp32): 4096 x 16384 bf16 126 and
+// 252 us = 4.3 and 3.2 TB/s, 4096 x 8192 fp32 155 and 510 = 3.5 and 1.6.
 #include "norms.cuh"
 
 namespace gdr {

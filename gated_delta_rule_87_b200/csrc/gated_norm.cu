@@ -4,8 +4,9 @@
 //     du = dy w s,  dx = r (du - u mean(du u)),  dz = dy u w s'(z),  dw = sum over rows of dy u s
 // mean(du u) = r mean(du x), so the backward pass takes both of its row sums in
 // one reduction.  16384 x 32 x 128 bf16: 68 us (sigmoid) = 5.9 TB/s and 70 (silu);
-// gradient 120 = 5.6 TB/s and 132 = 5.1, where the gate's instructions show; fp32 134
-// and 214 us = 6.0 and 6.3 TB/s.
+// gradient 120 = 5.6 TB/s and 133 = 5.0, where the gate's instructions show; fp32 133
+// and 224 us = 6.1 and 6.0 TB/s.  Other head sizes are slower: 16384 x 32 x 96 bf16 66
+// and 123 us = 4.6 and 4.1 TB/s, 16384 x 16 x 333 175 and 304 = 3.0 and 2.9.
 #include "norms.cuh"
 
 namespace gdr {

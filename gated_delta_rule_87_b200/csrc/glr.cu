@@ -509,14 +509,14 @@ __device__ __forceinline__ bool has_marks(const GlrArgs &p, uint32_t tile) {
 //
 // Bound by HBM where rows are long (32768 x 4096: bf16 174 us = 6.2 TB/s of 2e + 4
 // bytes an element, fp32 253 us = 6.4; a copy does 6.5), with few columns by the
-// chain (65536 x 256 bf16: 42 us = 3.2 TB/s).  The complement forms 1 - a, 8 warps
-// an SM (bf16 237 us, fp32 269).
+// chain (65536 x 256 bf16: 40 us = 3.4 TB/s).  The complement forms 1 - a, 8 warps
+// an SM (bf16 237 us, fp32 267).
 //
 // A tensor-map copy begins on 16 bytes.  Where rows do not, every R-th one (R
 // elements in 16 bytes) is as far past a boundary as the first: R maps, each of
 // every R-th row and from the boundary before it, reach them all, and lanes read
 // `shift` elements on.  (By lane copies of 4 or 2 bytes instead: 431 us against
-// 292 for 32767 x 4095 fp32, 347 against 234 for bf16.)
+// 275 for 32767 x 4095 fp32, 347 against 239 for bf16.)
 struct Shift {  // of row i, where the first token's is s: s + i l
   int s, l;
 };
@@ -728,7 +728,7 @@ glr_scan_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMa
 
 // Backward: the states again from what enters the tile (saved), the gradients
 // from what enters it from the tokens after it (chained).  32768 x 4096: bf16 324
-// us = 5.8 TB/s of 3e + 8 bytes an element, fp32 447 us = 6.0; complement 372, 490.
+// us = 5.8 TB/s of 3e + 8 bytes an element, fp32 443 us = 6.1; complement 372, 490.
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 __global__ void __launch_bounds__(kThreads, (BwdShape<IO, COMPLEMENT>::kBlocks))
 glr_gradient_kernel(const __grid_constant__ GlrArgs p, const __grid_constant__ GlrMaps<IO, PAIRS, true> maps) {
@@ -930,7 +930,8 @@ __global__ void __launch_bounds__(256) glr_no_tokens_kernel(GlrArgs p, bool back
 }
 
 // One token for each sequence, the state in place: a thread a pair of channels, one
-// pass.  16 x 2048 to 256 x 4096 bf16: 11 us a call, the host's time for it.
+// pass.  16 x 2048 to 256 x 4096 bf16: 11 us a call, the host's time for it; in a
+// replayed graph 1.5 and 5.4 us, 512 x 8192 14.2 = 4.7 TB/s (fp32 14.9 = 5.6).
 template <typename IO, bool PAIRS, bool COMPLEMENT>
 __global__ void __launch_bounds__(256) glr_step_kernel(GlrArgs p) {
   constexpr int V = PAIRS ? 2 : 1;
