@@ -829,16 +829,14 @@ static kda_status_t check_gated(const gdr::GatedNormArgs &a, kda_gate_t gate, kd
 }
 
 // An output may be an input's buffer where that one's rows lie as the output's do.
-static bool same_rows(const void *out, const void *in, int64_t ld, int64_t row) {
-  return !out || out != in || ld == row;
-}
-
 static kda_status_t check_gated_sharing(const gdr::GatedNormArgs &a) {
   const int64_t row = (int64_t)a.H * a.d;
-  const void *outs[] = {a.y, a.dx, a.dz};
+  const void *outs[] = {a.y, a.dx, a.dz}, *ins[] = {a.x, a.z, a.dy};
+  const int64_t lds[] = {a.ld_x, a.ld_z, a.ld_dy};
   for (const void *o : outs)
-    if (!same_rows(o, a.x, a.ld_x, row) || !same_rows(o, a.z, a.ld_z, row) || !same_rows(o, a.dy, a.ld_dy, row))
-      return fail(KDA_ERR_INVALID_ARG, "an output shares a buffer with an input whose rows are further apart");
+    for (int k = 0; k < 3; ++k)
+      if (o && o == ins[k] && a.tokens > 1 && lds[k] != row)
+        return fail(KDA_ERR_INVALID_ARG, "an output shares a buffer with an input whose rows are further apart");
   if (a.dz && a.dx == a.dz) return fail(KDA_ERR_INVALID_ARG, "dx and dz must not be the same buffer");
   return KDA_OK;
 }

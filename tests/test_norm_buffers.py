@@ -26,6 +26,22 @@ def test_gradient_refuses_buffers_that_it_would_overwrite(over):
     assert b"buffer" in gdr.lib().kda_last_error()
 
 
+def test_gradient_of_one_token_refuses_one_buffer_for_two_outputs():
+    assert gdr.lib().kda_gated_norm_bwd(FAKE, 128, FAKE + 4096, 128, FAKE + 8192, 128, None, FAKE + 12288, FAKE + 12288, None,
+                                        1, 2, 64, 1e-6, 1, 1, None, 0, None) == ARG
+
+
+@pytest.mark.gpu
+def test_one_token_in_place_at_any_pitch():
+    """The distance between tokens is of no account where there is one."""
+    import torch
+    x, z = (torch.randn((1, 2, 64), device="cuda") for _ in range(2))
+    want = gdr.gated_norm_fwd(x, z)
+    st = gdr.lib().kda_gated_norm_fwd(x.data_ptr(), 200, z.data_ptr(), 300, None, x.data_ptr(), 1, 2, 64, 1e-6, 1, 0,
+                                      torch.cuda.current_stream().cuda_stream)
+    assert st == gdr.KDA_OK and torch.allclose(x, want, rtol=1e-5, atol=1e-6)
+
+
 def test_scan_gradient_refuses_one_buffer_for_two_outputs():
     kw = dict(dh=FAKE, ld_dh=8, df=None, x=FAKE + 4096, ld_x=8, g=FAKE + 8192, ld_g=8, h0=None, chunks=None, dx=FAKE + 12288,
               dg=FAKE + 12288, dh0=None, cu=None, n=0, B=1, T=64, D=8, input=0, io=0, ws=FAKE, ws_bytes=1 << 20)
