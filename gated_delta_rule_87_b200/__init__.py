@@ -8,8 +8,9 @@ library is missing or no CUDA device is present the calls raise.
 
 ``stream`` is the stream that a call runs on (default: the current one of the
 tensors' device).  Outputs and workspaces that a call allocates belong to it, and
-tensors of other streams that it is given are kept until it is past them; the
-caller orders it with the streams that write those tensors and read the results.
+tensors of other streams that it is given are kept until it is past them (the
+caller keeps them for a stream that torch does not own); the caller orders it with
+the streams that write those tensors and read the results.
 No call is recorded by autograd: the gradients are calls of their own (``*_bwd``).
 
 Operator (thethings.ai "The argument, in one page", table "Everything, in
@@ -255,7 +256,8 @@ def _there(torch, dev, stream, call, *args, **kw):
     (outputs, workspace) then belongs to the stream that uses it: memory freed on
     another stream is not written while that one still reads it, and a workspace
     that the caller drops is not handed out again before the stream is past it.
-    Tensors of other streams are recorded, so the same holds for them."""
+    Tensors of other streams are recorded, so the same holds for them; not on a
+    stream that torch does not own, which may be gone when they are freed."""
     with torch.cuda.device(dev):
         if stream is None:
             return call(*args, **kw)
@@ -265,9 +267,10 @@ def _there(torch, dev, stream, call, *args, **kw):
             raise ValueError(f"stream must belong to CUDA device {dev}")
         with torch.cuda.stream(stream):
             out = call(*args, **kw)
-        for t in (*args, *kw.values()):
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(stream)
+        if not isinstance(stream, torch.cuda.ExternalStream):
+            for t in (*args, *kw.values()):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
         return out
 
 

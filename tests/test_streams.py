@@ -9,8 +9,12 @@ import gated_delta_rule_87_b200 as gdr
 
 
 class _Stream:
-    def __init__(self, handle, index=0):
-        self.cuda_stream, self.device = handle, types.SimpleNamespace(index=index)
+    def __init__(self, handle, device=0):
+        self.cuda_stream, self.device = handle, types.SimpleNamespace(index=device)
+
+
+class _External(_Stream):
+    pass
 
 
 class _Tensor:
@@ -42,7 +46,7 @@ def _fake_torch():
     fake.cuda = types.SimpleNamespace(
         Stream=_Stream, device=device, stream=stream, current_device=lambda: fake.at[0],
         current_stream=lambda dev: _Stream(fake.at[1], dev),
-        ExternalStream=lambda handle, device: _Stream(handle, device))
+        ExternalStream=_External)
     fake._C = types.SimpleNamespace()
     return fake
 
@@ -55,14 +59,15 @@ def test_a_call_runs_under_the_stream_that_it_is_given():
     out = gdr._there(torch, 0, _Stream(7), lambda *a, **kw: seen.append(torch.at) or "out", x, None, kw=y, n=3)
     assert out == "out" and seen == [(0, 7)] and torch.at == (0, 0)
     assert x.recorded == [7] and y.recorded == [7]
-    # a stream of another library, known by its handle alone
-    gdr._there(torch, 0, types.SimpleNamespace(cuda_stream=9), lambda a: seen.append(torch.at), x)
-    assert seen[-1] == (0, 9) and x.recorded == [7, 9]
+    # a stream of another library, known by its handle alone or wrapped: it may be gone when x is freed
+    for other in (types.SimpleNamespace(cuda_stream=9), _External(9)):
+        gdr._there(torch, 0, other, lambda a: seen.append(torch.at), x)
+        assert seen[-1] == (0, 9) and x.recorded == [7]
     # another device, its current stream: nothing to record
     gdr._there(torch, 1, None, lambda a: seen.append(torch.at), x)
-    assert seen[-1] == (1, 0) and x.recorded == [7, 9]
+    assert seen[-1] == (1, 0) and x.recorded == [7]
     with pytest.raises(ValueError, match="CUDA device 0"):
-        gdr._there(torch, 0, _Stream(7, index=1), lambda: None)
+        gdr._there(torch, 0, _Stream(7, device=1), lambda: None)
 
 
 def _calls(torch):
